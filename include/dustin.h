@@ -18,6 +18,10 @@
  *                      the full KV cache (the comparator).
  *   dustin_kv_append   section 3, step 5: accepted tokens are appended.
  *   dustin_verify_step score -> select -> verify in one call on one stream.
+ * Beside them, not in the pages: attention through a sliding window with sinks
+ * (dustin_window_attn) and behind a prefix that a batch shares
+ * (dustin_prefix_attn), and caches bounded by accumulated attention weight
+ * (dustin_accumulate, dustin_evict).
  *
  * Conventions (all calls):
  *  - The caller owns every buffer.  Pointers named "device" are CUDA device
@@ -261,6 +265,88 @@ int dustin_step_launches(const dustin_step* s, int32_t* n_launches, int32_t* gro
  * verification calls would return for the shape. */
 int dustin_verify_split(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d,
                         int32_t n_layers, int32_t dense, int32_t* grid, int32_t* tiles_per_unit);
+
+/* ---- cache operators ------------------------------------------------------
+ * Attention whose output is bf16 (the type the next projection reads) with its
+ * log-sum-exp, and the calls that keep a cache within a budget by the weight
+ * its rows have been given.  The pages have no counterpart; they share the
+ * types and conventions above.  A pass of a server that bounds its caches:
+ * dustin_prefix_attn (o, lse) -> accept -> dustin_kv_append ->
+ * dustin_accumulate -> dustin_evict. */
+
+/* Bytes of workspace that dustin_window_attn (prefix_cap = 0),
+ * dustin_prefix_attn, dustin_accumulate and dustin_evict (n_layers) need with
+ * these arguments; hq = 0: no attention, n_layers = 0: no eviction.  Returns 0
+ * if the arguments are invalid. */
+size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d,
+                                    int32_t n_layers, int32_t prefix_cap);
+
+/* Attention of the draft block through a sliding window with sinks.  Query t of
+ * sequence b has position i = seq_len[b] + t; cache row j < seq_len[b] has
+ * position j, block row u position seq_len[b] + u.  A key at position j is
+ * visible iff j <= i and (i - j < p->window or j < p->sinks): the window counts
+ * the query's own position, and the first p->sinks positions stay visible.
+ * Cache rows that no query of the block sees are never read (they may hold
+ * anything); keys and values that some query sees must be finite.
+ *   o    device, bf16 [B][gamma+1][hq][d], not q: softmax(q.k/sqrt(d)) v over the
+ *        visible keys, 0 where there is none (window = 0)
+ *   lse  device, fp32 [B][gamma+1][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf
+ *        where no key is visible
+ * q, k, v, kb, vb as in dustin_verify_layer; hkv * B <= 16384 (DUSTIN_ERANGE).
+ * p->m and p->k are not used beyond their checks.  A sequence whose seq_len is
+ * outside [0, Lcap] is flagged (DUSTIN_DEV_SEQLEN) and taken as empty. */
+int dustin_window_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv k, dustin_kv v,
+                       const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse,
+                       void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of the draft block of a batch whose sequences share a prefix: the
+ * keys of sequence b are rows 0..*prefix_len-1 of the one prefix cache, then
+ * its own rows 0..seq_len[b]-1, then the block rows u <= t.  The prefix is read
+ * once for the whole batch.
+ *   pk, pv      the prefix caches, [hkv][prefix_cap][d] (their sb is not used)
+ *   prefix_len  device int32 scalar, 0..prefix_cap (0: plain dense attention);
+ *               outside: flagged (DUSTIN_DEV_SEQLEN), taken as 0
+ * The rest as in dustin_window_attn, without a window: p->sinks and p->window
+ * are not used. */
+int dustin_prefix_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv pk, dustin_kv pv,
+                       int32_t prefix_cap, const int32_t* prefix_len, dustin_kv k, dustin_kv v,
+                       const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse,
+                       void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Adds the attention that the accepted rows of a block paid to each row of a
+ * cache.  Call it after the accepted rows were appended: the last n = n_new[b]
+ * of the L = seq_len[b] cache rows are theirs, and query t < n (the first n of
+ * the block's gamma+1 queries) sits at row L - n + t.  For every KV head g and
+ * row j < L
+ *   weight[b][g][j] += sum over t < n with j <= L - n + t, over the query heads
+ *                      of g, of exp(q.k_j/sqrt(d) - lse[b][t][h]),
+ * with weight taken as 0 and pos[b][g][j] set to n_seen[b] - (L - j) for the new
+ * rows j >= L - n.  A row whose lse is -inf adds nothing.
+ *   q, lse         of the attention call that verified the block
+ *   n_seen         device int32 [B]: tokens the sequence has had so far, the new
+ *                  ones included (n_seen[b] >= seq_len[b]; more once rows were evicted)
+ *   weight, pos    device fp32 / int32 [B][hkv][Lcap]; rows at or beyond
+ *                  seq_len[b] are left as they were
+ * A sequence whose n is outside [0, min(gamma+1, L)], L outside [0, Lcap] or
+ * n_seen below L is left untouched and flagged (DUSTIN_DEV_APPEND). */
+int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const float* lse, dustin_kv k,
+                      const int32_t* n_new, const int32_t* seq_len, const int32_t* n_seen, float* weight,
+                      int32_t* pos, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Evicts from the caches of n_layers layers, in place, down to p->k rows.  For
+ * every layer, sequence and KV head with more than k rows the kept ones are
+ * those with pos < p->sinks or pos >= n_seen[b] - p->window, then the largest
+ * weights; equal weights go to the lower row, and should more than k rows be
+ * protected (repeated positions) the lower ones stay.  The rows dropped below k,
+ * ascending, take the kept rows at or beyond k, ascending -- K and V rows,
+ * weight and pos -- so that as few rows move as can; rows at or beyond k keep
+ * their old contents.  Then seq_len[b] = min(seq_len[b], k).  A NaN or negative
+ * weight ranks as 0 and sets DUSTIN_DEV_NAN.  Every buffer may be given once
+ * only (DUSTIN_EINVAL); a sequence whose seq_len is outside [0, Lcap] is left
+ * untouched and flagged (DUSTIN_DEV_SEQLEN). */
+int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, const dustin_kv* v,
+                 float* const* weight, int32_t* const* pos, const int32_t* n_seen, int32_t* seq_len,
+                 void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Self-test of the bounded waits (no counterpart in the pages).  Every
  * on-chip wait of the kernels above gives up after 2 s, sets

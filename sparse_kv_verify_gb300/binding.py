@@ -28,7 +28,8 @@ EXPORTS = ["dustin_version", "dustin_workspace_bytes", "dustin_workspace_init", 
            "dustin_score", "dustin_select", "dustin_verify_attn", "dense_verify_attn",
            "dustin_kv_append", "dustin_verify_step", "dustin_step_launches", "dustin_compact_kv",
            "dustin_score_noalloc", "dustin_score_noalloc_check", "dustin_wait_selftest",
-           "dustin_verify_split"]
+           "dustin_verify_split", "dustin_cache_workspace_bytes", "dustin_window_attn",
+           "dustin_prefix_attn", "dustin_accumulate", "dustin_evict"]
 
 
 class DustinError(RuntimeError):
@@ -118,9 +119,24 @@ def lib():
         L.dustin_score_noalloc_check.argtypes = [c_void_p, POINTER(c_int32)]
         L.dustin_verify_split.argtypes = [POINTER(CParams), c_int32, c_int32, c_int32, c_int32,
                                           c_int32, POINTER(c_int32), POINTER(c_int32)]
+        L.dustin_cache_workspace_bytes.restype = c_size_t
+        L.dustin_cache_workspace_bytes.argtypes = [POINTER(CParams), c_int32, c_int32, c_int32, c_int32,
+                                                   c_int32]
+        L.dustin_window_attn.argtypes = [POINTER(CParams), c_int32, c_void_p, CKV, CKV, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                         c_void_p]
+        L.dustin_prefix_attn.argtypes = [POINTER(CParams), c_int32, c_void_p, CKV, CKV, c_int32, c_void_p,
+                                         CKV, CKV, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_size_t, c_void_p]
+        L.dustin_accumulate.argtypes = [POINTER(CParams), c_int32, c_void_p, c_void_p, CKV, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                        c_void_p]
+        L.dustin_evict.argtypes = [POINTER(CParams), c_int32, POINTER(CKV), POINTER(CKV),
+                                   POINTER(c_void_p), POINTER(c_void_p), c_void_p, c_void_p, c_void_p,
+                                   c_size_t, c_void_p]
         L.dustin_wait_selftest.argtypes = [ctypes.c_int64, c_void_p, c_void_p, c_size_t, c_void_p]
         for f in EXPORTS[1:]:
-            if f != "dustin_workspace_bytes":
+            if f not in ("dustin_workspace_bytes", "dustin_cache_workspace_bytes"):
                 getattr(L, f).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -505,3 +521,193 @@ def dustin_verify_step(p: Params, draft: Signal, target: Signal, srh, layers, se
                        importance=None, i_verify=None, ws=None, events=None, stream=None):
     return StepCall(p, draft, target, srh, layers, seq_len, importance, i_verify, ws, events,
                     stream)(stream)
+
+
+# ------------------------------------------------------------------ cache operators
+
+
+def cache_workspace_bytes(p: Params, hq: int = 0, hkv: int = 1, d: int = 128, n_layers: int = 0,
+                          prefix_cap: int = 0) -> int:
+    """Workspace bytes of the cache operators: attention for ``hq`` query heads
+    (0: none) behind a prefix of up to ``prefix_cap`` rows, accumulation, and
+    eviction from ``n_layers`` layers (0: none)."""
+    n = lib().dustin_cache_workspace_bytes(ctypes.byref(p.c()), hq, hkv, d, n_layers, prefix_cap)
+    if n == 0:
+        raise DustinError("dustin_cache_workspace_bytes", -1)
+    return int(n)
+
+
+def _shape(name: str, t: torch.Tensor, *want: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name}: expected shape {list(want)}, got {list(t.shape)}")
+
+
+class _CacheCall:
+    """A pre-marshalled call: checks its tensors' shapes, types and devices
+    once and keeps them alive; calling it enqueues the operator on ``stream``
+    (default: the current stream of the tensors' device)."""
+
+    def __init__(self, fn: str, p: Params, tensors, ws, need: int, stream):
+        self._name, self._p = fn, p.c()
+        self._tensors = [t for t in tensors if t is not None]
+        self.device = self._tensors[0].device
+        for t in self._tensors:
+            if t.device != self.device:
+                raise ValueError(f"{fn}: tensors on {self.device} and {t.device}")
+        if ws is None:
+            with torch.cuda.device(self.device):
+                ws = Workspace(need, device=self.device,
+                               stream=stream or torch.cuda.current_stream(self.device))
+        elif ws.buf.device != self.device:
+            raise ValueError(f"{fn}: tensors on {self.device} and a workspace on {ws.buf.device}")
+        self.ws = ws
+        self._fn = getattr(lib(), fn)
+
+    def __call__(self, stream=None):
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if s.device != self.device:
+            raise ValueError(f"{self._name}: tensors on {self.device} and a stream on {s.device}")
+        if torch.cuda.current_device() == self.device.index:
+            st = self._fn(*self._args, self.ws.ptr, self.ws.nbytes, s.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = self._fn(*self._args, self.ws.ptr, self.ws.nbytes, s.cuda_stream)
+        if st != 0:
+            raise DustinError(self._name, st)
+        return self._result
+
+
+def _block_args(p: Params, q, k, v, kb, vb, seq_len, o, lse):
+    """Checks the tensors of an attention call and allocates its outputs."""
+    T = p.gamma + 1
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B][gamma+1][hq][d] and the caches [B][hkv][Lcap][d]")
+    hq, hkv, d = q.shape[2], k.shape[1], k.shape[3]
+    _shape("q", q, p.B, T, hq, d)
+    _shape("k", k, p.B, hkv, p.Lcap, d)
+    _shape("v", v, p.B, hkv, p.Lcap, d)
+    _shape("kb", kb, p.B, hkv, T, d)
+    _shape("vb", vb, p.B, hkv, T, d)
+    _shape("seq_len", seq_len, p.B)
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _shape("o", o, p.B, T, hq, d)
+    _shape("lse", lse, p.B, T, hq)
+    return hq, hkv, d, o, lse
+
+
+class WindowCall(_CacheCall):
+    """Pre-marshalled ``dustin_window_attn``; calling it returns ``(o, lse)``."""
+
+    def __init__(self, p: Params, q, k, v, kb, vb, seq_len, o=None, lse=None, ws=None, stream=None):
+        hq, hkv, d, o, lse = _block_args(p, q, k, v, kb, vb, seq_len, o, lse)
+        bf = torch.bfloat16
+        args = (hq, _ptr(q, bf), kv_view(k), kv_view(v), _ptr(kb, bf), _ptr(vb, bf),
+                _ptr(seq_len, torch.int32), _ptr(o, bf), _ptr(lse, torch.float32))
+        super().__init__("dustin_window_attn", p, (q, k, v, kb, vb, seq_len, o, lse), ws,
+                         0 if ws is not None else cache_workspace_bytes(p, hq, hkv, d), stream)
+        self._args = (ctypes.byref(self._p),) + args
+        self._result = (o, lse)
+
+
+class PrefixCall(_CacheCall):
+    """Pre-marshalled ``dustin_prefix_attn``; calling it returns ``(o, lse)``."""
+
+    def __init__(self, p: Params, q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o=None, lse=None,
+                 ws=None, stream=None):
+        hq, hkv, d, o, lse = _block_args(p, q, k, v, kb, vb, seq_len, o, lse)
+        if pk.dim() != 4:
+            raise ValueError("the prefix caches must be [1][hkv][prefix_cap][d]")
+        cap = pk.shape[2]
+        _shape("pk", pk, 1, hkv, cap, d)
+        _shape("pv", pv, 1, hkv, cap, d)
+        _shape("prefix_len", prefix_len, 1)
+        bf = torch.bfloat16
+        args = (hq, _ptr(q, bf), kv_view(pk), kv_view(pv), cap, _ptr(prefix_len, torch.int32), kv_view(k),
+                kv_view(v), _ptr(kb, bf), _ptr(vb, bf), _ptr(seq_len, torch.int32), _ptr(o, bf),
+                _ptr(lse, torch.float32))
+        super().__init__("dustin_prefix_attn", p, (q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o, lse),
+                         ws, 0 if ws is not None else cache_workspace_bytes(p, hq, hkv, d, prefix_cap=cap),
+                         stream)
+        self._args = (ctypes.byref(self._p),) + args
+        self._result = (o, lse)
+
+
+class AccumulateCall(_CacheCall):
+    """Pre-marshalled ``dustin_accumulate``; calling it returns ``(weight, pos)``."""
+
+    def __init__(self, p: Params, q, lse, k, n_new, seq_len, n_seen, weight, pos, ws=None, stream=None):
+        if q.dim() != 4 or k.dim() != 4:
+            raise ValueError("q must be [B][gamma+1][hq][d] and the cache [B][hkv][Lcap][d]")
+        hq, hkv, d = q.shape[2], k.shape[1], k.shape[3]
+        _shape("q", q, p.B, p.gamma + 1, hq, d)
+        _shape("lse", lse, p.B, p.gamma + 1, hq)
+        _shape("k", k, p.B, hkv, p.Lcap, d)
+        for name, t in (("n_new", n_new), ("seq_len", seq_len), ("n_seen", n_seen)):
+            _shape(name, t, p.B)
+        _shape("weight", weight, p.B, hkv, p.Lcap)
+        _shape("pos", pos, p.B, hkv, p.Lcap)
+        i32, f32 = torch.int32, torch.float32
+        args = (hq, _ptr(q, torch.bfloat16), _ptr(lse, f32), kv_view(k), _ptr(n_new, i32), _ptr(seq_len, i32),
+                _ptr(n_seen, i32), _ptr(weight, f32), _ptr(pos, i32))
+        super().__init__("dustin_accumulate", p, (q, lse, k, n_new, seq_len, n_seen, weight, pos), ws,
+                         0 if ws is not None else cache_workspace_bytes(p), stream)
+        self._args = (ctypes.byref(self._p),) + args
+        self._result = (weight, pos)
+
+
+class EvictCall(_CacheCall):
+    """Pre-marshalled ``dustin_evict`` over lists of layers; calling it returns
+    ``seq_len`` (the caches, weights and positions change in place)."""
+
+    def __init__(self, p: Params, ks, vs, weights, poss, n_seen, seq_len, ws=None, stream=None):
+        n = len(ks)
+        if n < 1 or not (len(vs) == len(weights) == len(poss) == n):
+            raise ValueError("ks, vs, weights and poss must hold one tensor per layer")
+        hkv, d = ks[0].shape[1], ks[0].shape[3]
+        for l in range(n):
+            _shape(f"ks[{l}]", ks[l], p.B, hkv, p.Lcap, d)
+            _shape(f"vs[{l}]", vs[l], p.B, hkv, p.Lcap, d)
+            _shape(f"weights[{l}]", weights[l], p.B, hkv, p.Lcap)
+            _shape(f"poss[{l}]", poss[l], p.B, hkv, p.Lcap)
+        _shape("n_seen", n_seen, p.B)
+        _shape("seq_len", seq_len, p.B)
+        args = (n, (CKV * n)(*[kv_view(t) for t in ks]), (CKV * n)(*[kv_view(t) for t in vs]),
+                (c_void_p * n)(*[_ptr(t, torch.float32) for t in weights]),
+                (c_void_p * n)(*[_ptr(t, torch.int32) for t in poss]),
+                _ptr(n_seen, torch.int32), _ptr(seq_len, torch.int32))
+        super().__init__("dustin_evict", p, (*ks, *vs, *weights, *poss, n_seen, seq_len), ws,
+                         0 if ws is not None else cache_workspace_bytes(p, hkv=hkv, n_layers=n), stream)
+        self._args = (ctypes.byref(self._p),) + args
+        self._result = seq_len
+
+
+def dustin_window_attn(p: Params, q, k, v, kb, vb, seq_len, o=None, lse=None, ws=None, stream=None):
+    """Attention of the draft block through a sliding window (``p.window``
+    positions, the query's own included) with ``p.sinks`` first positions that
+    stay visible; returns ``(o bf16, lse fp32)``."""
+    return WindowCall(p, q, k, v, kb, vb, seq_len, o, lse, ws, stream)(stream)
+
+
+def dustin_prefix_attn(p: Params, q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o=None, lse=None,
+                       ws=None, stream=None):
+    """Attention of the draft block over a prefix cache ``[1][hkv][cap][d]`` that
+    the batch shares (``prefix_len`` int32 [1] rows of it), then each
+    sequence's own cache and the block; returns ``(o bf16, lse fp32)``."""
+    return PrefixCall(p, q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o, lse, ws, stream)(stream)
+
+
+def dustin_accumulate(p: Params, q, lse, k, n_new, seq_len, n_seen, weight, pos, ws=None, stream=None):
+    """Adds the attention of the ``n_new[b]`` accepted (and appended) rows to
+    ``weight`` and sets the new rows' ``pos``; both ``[B][hkv][Lcap]``."""
+    return AccumulateCall(p, q, lse, k, n_new, seq_len, n_seen, weight, pos, ws, stream)(stream)
+
+
+def dustin_evict(p: Params, ks, vs, weights, poss, n_seen, seq_len, ws=None, stream=None):
+    """Evicts, in place, down to ``p.k`` rows per layer, sequence and KV head,
+    keeping sinks, the recent window and the largest weights."""
+    return EvictCall(p, ks, vs, weights, poss, n_seen, seq_len, ws, stream)(stream)

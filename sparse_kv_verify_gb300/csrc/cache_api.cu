@@ -1,0 +1,191 @@
+// C entry points of the cache operators (windowed and shared-prefix attention,
+// accumulated attention weights, eviction): argument checks and launches.
+// Nothing here allocates device memory.  Workspace: the header of api.cu, then
+// the scratch of the one operator that runs.
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+
+using namespace dustin;
+
+namespace {
+
+float scale_log2_of(int d) { return float(1.4426950408889634 / std::sqrt(double(d))); }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The shape rules of the attention calls.
+int attend_shape(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d) {
+  if (!params_ok(p)) return DUSTIN_EINVAL;
+  if (hkv < 1 || hq < 1 || hq % hkv || (d != 64 && d != 128)) return DUSTIN_EINVAL;
+  if (p->gamma + 1 > DUSTIN_MAX_BLOCK || int64_t(p->gamma + 1) * (hq / hkv) > DUSTIN_MAX_QROWS)
+    return DUSTIN_ERANGE;
+  if (int64_t(p->B) * hkv > kVerifyUnitsMax) return DUSTIN_ERANGE;
+  return DUSTIN_OK;
+}
+
+// pk == nullptr: windowed attention.
+int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_kv* pk, const dustin_kv* pv,
+               int32_t prefix_cap, const int32_t* prefix_len, const dustin_kv& k, const dustin_kv& v,
+               const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse, void* ws,
+               size_t ws_bytes, cudaStream_t stream) {
+  if (!params_ok(p)) return DUSTIN_EINVAL;
+  if (!q || !kb || !vb || !o || !seq_len || o == q) return DUSTIN_EINVAL;
+  if (!aligned16(q) || !aligned16(kb) || !aligned16(vb) || !aligned16(o) || !aligned4(lse)) return DUSTIN_EINVAL;
+  if (!kv_ok(k, p->Lcap) || !kv_ok(v, p->Lcap) || k.hkv != v.hkv || k.d != v.d) return DUSTIN_EINVAL;
+  if (pk) {
+    if (!prefix_len || prefix_cap < 1) return DUSTIN_EINVAL;
+    if (prefix_cap > DUSTIN_MAX_LCAP) return DUSTIN_ERANGE;
+    for (const dustin_kv* t : {pk, pv})
+      if (!kv_ok(*t, prefix_cap) || t->hkv != k.hkv || t->d != k.d) return DUSTIN_EINVAL;
+  }
+  const int st = attend_shape(p, hq, k.hkv, k.d);
+  if (st != DUSTIN_OK) return st;
+  const size_t need = kScratch + attend_scratch_bytes(p->B, hq, k.hkv, k.d, p->gamma + 1, pk ? prefix_cap : 0);
+  if (!ws_ok(ws, ws_bytes, need)) return DUSTIN_EWORKSPACE;
+  AttendArgs a{};
+  a.B = p->B;
+  a.Lcap = p->Lcap;
+  a.T = p->gamma + 1;
+  a.hq = hq;
+  a.hkv = k.hkv;
+  a.sinks = pk ? 0 : p->sinks;
+  a.window = pk ? INT_MAX : p->window;
+  a.Pcap = pk ? prefix_cap : 0;
+  a.scale_log2 = scale_log2_of(k.d);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k.ptr);
+  a.v = static_cast<const uint16_t*>(v.ptr);
+  a.kb = static_cast<const uint16_t*>(kb);
+  a.vb = static_cast<const uint16_t*>(vb);
+  a.ksb = k.sb; a.ksh = k.sh; a.ksl = k.sl;
+  a.vsb = v.sb; a.vsh = v.sh; a.vsl = v.sl;
+  if (pk) {
+    a.pk = static_cast<const uint16_t*>(pk->ptr);
+    a.pv = static_cast<const uint16_t*>(pv->ptr);
+    a.pksh = pk->sh; a.pksl = pk->sl;
+    a.pvsh = pv->sh; a.pvsl = pv->sl;
+    a.prefix_len = prefix_len;
+  }
+  a.seq_len = seq_len;
+  a.err = err_word(ws);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  return attend_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d,
+                                    int32_t n_layers, int32_t prefix_cap) {
+  if (!params_ok(p) || hkv < 1 || n_layers < 0 || n_layers > DUSTIN_MAX_LAYERS || prefix_cap < 0 ||
+      prefix_cap > DUSTIN_MAX_LCAP || int64_t(p->B) * hkv > kVerifyUnitsMax)
+    return 0;
+  size_t need = kScratch;
+  if (hq != 0) {
+    if (attend_shape(p, hq, hkv, d) != DUSTIN_OK) return 0;
+    need = kScratch + attend_scratch_bytes(p->B, hq, hkv, d, p->gamma + 1, prefix_cap);
+  }
+  if (n_layers != 0) {
+    const size_t e = kScratch + evict_scratch_bytes(p->B, hkv, n_layers, p->k);
+    need = e > need ? e : need;
+  }
+  return round256(need);
+}
+
+int dustin_window_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv k, dustin_kv v,
+                       const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse,
+                       void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return run_attend(p, hq, q, nullptr, nullptr, 0, nullptr, k, v, kb, vb, seq_len, o, lse, ws, ws_bytes, stream);
+}
+
+int dustin_prefix_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv pk, dustin_kv pv,
+                       int32_t prefix_cap, const int32_t* prefix_len, dustin_kv k, dustin_kv v,
+                       const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse,
+                       void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return run_attend(p, hq, q, &pk, &pv, prefix_cap, prefix_len, k, v, kb, vb, seq_len, o, lse, ws, ws_bytes, stream);
+}
+
+int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const float* lse, dustin_kv k,
+                      const int32_t* n_new, const int32_t* seq_len, const int32_t* n_seen, float* weight,
+                      int32_t* pos, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!params_ok(p)) return DUSTIN_EINVAL;
+  if (!q || !lse || !n_new || !seq_len || !n_seen || !weight || !pos) return DUSTIN_EINVAL;
+  if (!aligned16(q) || !aligned4(lse) || !aligned4(weight) || !aligned4(pos)) return DUSTIN_EINVAL;
+  if (static_cast<const void*>(weight) == pos || weight == lse) return DUSTIN_EINVAL;
+  if (!kv_ok(k, p->Lcap)) return DUSTIN_EINVAL;
+  const int st = attend_shape(p, hq, k.hkv, k.d);
+  if (st != DUSTIN_OK) return st;
+  if (!ws_ok(ws, ws_bytes, kScratch)) return DUSTIN_EWORKSPACE;
+  AccumulateArgs a{};
+  a.B = p->B;
+  a.Lcap = p->Lcap;
+  a.T = p->gamma + 1;
+  a.G = hq / k.hkv;
+  a.hkv = k.hkv;
+  a.scale_log2 = scale_log2_of(k.d);
+  a.q = static_cast<const uint16_t*>(q);
+  a.lse = lse;
+  a.k = static_cast<const uint16_t*>(k.ptr);
+  a.ksb = k.sb; a.ksh = k.sh; a.ksl = k.sl;
+  a.n_new = n_new;
+  a.seq_len = seq_len;
+  a.n_seen = n_seen;
+  a.weight = weight;
+  a.pos = pos;
+  a.err = err_word(ws);
+  return accumulate_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+}
+
+int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, const dustin_kv* v,
+                 float* const* weight, int32_t* const* pos, const int32_t* n_seen, int32_t* seq_len,
+                 void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!params_ok(p)) return DUSTIN_EINVAL;
+  if (n_layers < 1) return DUSTIN_EINVAL;
+  if (n_layers > DUSTIN_MAX_LAYERS) return DUSTIN_ERANGE;
+  if (!k || !v || !weight || !pos || !n_seen || !seq_len || n_seen == seq_len) return DUSTIN_EINVAL;
+  EvictArgs a{};
+  a.B = p->B;
+  a.Lcap = p->Lcap;
+  a.hkv = k[0].hkv;
+  a.D = k[0].d;
+  a.n_layers = n_layers;
+  a.sinks = p->sinks;
+  a.window = p->window;
+  a.k = p->k;
+  a.n_seen = n_seen;
+  a.seq_len = seq_len;
+  const void* seen[4 * DUSTIN_MAX_LAYERS];   // every buffer once: rows move in place
+  int n_seen_bufs = 0;
+  for (int l = 0; l < n_layers; ++l) {
+    if (!kv_ok(k[l], p->Lcap) || !kv_ok(v[l], p->Lcap)) return DUSTIN_EINVAL;
+    if (k[l].hkv != a.hkv || v[l].hkv != a.hkv || k[l].d != a.D || v[l].d != a.D) return DUSTIN_EINVAL;
+    if (!weight[l] || !pos[l] || !aligned4(weight[l]) || !aligned4(pos[l])) return DUSTIN_EINVAL;
+    for (const void* t : {static_cast<const void*>(k[l].ptr), static_cast<const void*>(v[l].ptr),
+                          static_cast<const void*>(weight[l]), static_cast<const void*>(pos[l])}) {
+      for (int x = 0; x < n_seen_bufs; ++x)
+        if (seen[x] == t) return DUSTIN_EINVAL;
+      seen[n_seen_bufs++] = t;
+    }
+    EvictLayerDev& L = a.layer[l];
+    L.k = static_cast<uint16_t*>(k[l].ptr);
+    L.v = static_cast<uint16_t*>(v[l].ptr);
+    L.weight = weight[l];
+    L.pos = pos[l];
+    L.ksb = k[l].sb; L.ksh = k[l].sh; L.ksl = k[l].sl;
+    L.vsb = v[l].sb; L.vsh = v[l].sh; L.vsl = v[l].sl;
+  }
+  if (int64_t(p->B) * a.hkv > kVerifyUnitsMax) return DUSTIN_ERANGE;
+  if (!ws_ok(ws, ws_bytes, kScratch + evict_scratch_bytes(p->B, a.hkv, n_layers, p->k))) return DUSTIN_EWORKSPACE;
+  a.err = err_word(ws);
+  a.lists = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kScratch);
+  return evict_launch(a, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+}
+
+}  // extern "C"

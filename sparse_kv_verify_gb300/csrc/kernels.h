@@ -261,6 +261,74 @@ struct CompactArgs {
 };
 cudaError_t compact_launch(const CompactArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------- windowed / prefix attention
+
+struct AttendArgs {
+  int B, Lcap, T, hq, hkv;
+  int sinks, window;         // shared-prefix attention: sinks = 0, window = INT32_MAX
+  int Pcap;                  // rows of the prefix caches (0: no prefix)
+  float scale_log2;          // log2(e) / sqrt(D)
+  const uint16_t* q;         // [B][T][hq][D]
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* pk;        // prefix caches: element (g, pos, x) at g*sh + pos*sl + x
+  const uint16_t* pv;
+  const uint16_t* kb;        // [B][hkv][T][D]
+  const uint16_t* vb;
+  int64_t ksb, ksh, ksl, vsb, vsh, vsl, pksh, pksl, pvsh, pvsl;
+  const int32_t* seq_len;
+  const int32_t* prefix_len; // device scalar, or nullptr
+  int* err;
+  uint16_t* o;               // [B][T][hq][D] bf16
+  float* lse;                // [B][T][hq], or nullptr
+};
+size_t attend_scratch_bytes(int B, int hq, int hkv, int D, int T, int Pcap);
+cudaError_t attend_launch(const AttendArgs& a, int D, cudaStream_t stream);
+
+// -------------------------------------------------------------- accumulate
+
+struct AccumulateArgs {
+  int B, Lcap, T, G, hkv;
+  float scale_log2;          // log2(e) / sqrt(D)
+  const uint16_t* q;         // [B][T][hkv * G][D]
+  const float* lse;          // [B][T][hkv * G]
+  const uint16_t* k;
+  int64_t ksb, ksh, ksl;
+  const int32_t* n_new;
+  const int32_t* seq_len;
+  const int32_t* n_seen;
+  float* weight;             // [B][hkv][Lcap]
+  int32_t* pos;              // [B][hkv][Lcap]
+  int* err;
+};
+// Whether sequence lengths (rows, new rows, positions seen) are consistent; a
+// sequence that fails is flagged and left as it was.
+__host__ __device__ inline bool accumulate_ok(const AccumulateArgs& a, int L, int n, int seen) {
+  return L >= 0 && L <= a.Lcap && n >= 0 && n <= a.T && n <= L && seen >= L;
+}
+cudaError_t accumulate_launch(const AccumulateArgs& a, int D, cudaStream_t stream);
+
+// ------------------------------------------------------------------- evict
+
+struct EvictLayerDev {
+  uint16_t* k;
+  uint16_t* v;
+  float* weight;             // [B][hkv][Lcap]
+  int32_t* pos;              // [B][hkv][Lcap]
+  int64_t ksb, ksh, ksl, vsb, vsh, vsl;
+};
+
+struct EvictArgs {
+  int B, Lcap, hkv, D, n_layers, sinks, window, k;
+  const int32_t* n_seen;
+  int32_t* seq_len;
+  int* err;
+  int32_t* lists;            // [n_layers][B][hkv][2][k]: holes, movers
+  EvictLayerDev layer[DUSTIN_MAX_LAYERS];
+};
+size_t evict_scratch_bytes(int B, int hkv, int n_layers, int k);
+cudaError_t evict_launch(const EvictArgs& a, cudaStream_t stream);
+
 // ------------------------------------------------------------ wait self-test
 cudaError_t wait_selftest_launch(int* err, long long* waited, unsigned long long limit_ns,
                                  cudaStream_t stream);
