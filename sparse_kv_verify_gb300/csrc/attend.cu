@@ -1,95 +1,750 @@
-// Windowed attention with sinks and shared-prefix attention for a draft block.
+// Windowed attention with sinks for a draft block, and the sequences' own part
+// of shared-prefix attention.
 //
 // For query t of sequence b (position i = L + t, L = seq_len[b]) the visible
-// keys are the shared prefix (if any), the cache rows j < L and the block rows
-// u (position L + u) with j <= i and (i - j < window or j < sinks);
-// o = softmax(q.k / sqrt(d)) v and lse = ln sum exp(q.k / sqrt(d)) over them,
-// o = 0 and lse = -inf where nothing is visible.
+// keys are the cache rows j < L and the block rows u (position L + u) with
+// j <= i and (i - j < window or j < sinks); o = softmax(q.k / sqrt(d)) v and
+// lse = ln sum exp(q.k / sqrt(d)) over them, o = 0 and lse = -inf where nothing
+// is visible.
 //
-// One warp per query row walks its visible keys with a running maximum and
-// sum; lane x holds columns x, x + 32, ... of q and of the output.
+// Tiles: a unit (sequence b, KV head g) reads the 64-row tiles of the ranges
+// [0, min(sinks, L)) and [max(L - window + 1, sinks), L) -- one range [0, L)
+// where they meet -- and one tile of block rows.  Only a range's last tile and
+// the block tile are partial; a row's own window start and the causal rule are
+// masks inside a tile.  How many tiles a unit has depends on its sequence's
+// length, which only the device knows: every CTA sums the tile counts of the
+// batch (one warp, 32 sequences at a time) and takes its equal share of the
+// flattened tiles (stream-K), so that ragged lengths and any B and hkv load the
+// SMs alike.
+//
+// Roles inside a CTA (warp specialised, handing over through mbarriers):
+//   warps 4-7    loaders: a whole tile comes as tiled TMA loads (a K and a V
+//                box of 64 rows per 64 columns) issued by one thread, a partial
+//                one as 16-byte cp.async of its rows with the others
+//                zero-filled (rows past a range may hold anything), both into
+//                the 128-byte-swizzled layout that the MMAs read;
+//   warp 8       one thread issues S = Q K^T into one of two buffers in tensor
+//                memory as soon as a tile's rows have landed;
+//   warp 9       one thread issues O += P V with P read from tensor memory;
+//   warps 0-3    softmax in the log2 domain, the reference maximum moved only
+//                when a tile passes it by more than 2^8 (O is rarely rescaled).
+//                P is rounded to bf16 for the second MMA; the row sum adds the
+//                unrounded fp32 values, so lse keeps fp32 accuracy.
+//
+// A segment that covers a whole unit writes o and lse; otherwise its row
+// maxima, sums and unnormalised O go to slot unit + cta of the workspace (both
+// indices only grow along the flattened tiles, so no two segments share one),
+// and a second kernel merges them.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace dustin {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int TK = kAttendTile;     // keys per tile (and the largest draft block)
+constexpr int kSoftmaxWarps = 4;    // one thread per tensor-memory lane
+constexpr int kLoaders = 4;         // loader warps, kKpw keys of a partial tile each
+constexpr int kKpw = TK / kLoaders;
+constexpr int kLoaderWarp0 = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + kLoaders;
+constexpr int kPvWarp = kMmaWarp + 1;
+constexpr int NTH = 32 * (kPvWarp + 1);
+constexpr int kSCol = 0;            // S buffers: columns [0, 64) and [64, 128)
+constexpr int kPCol = 128;          // P buffers (bf16 pairs) with one CTA per SM
+constexpr uint32_t kSmemPerSm = 228 * 1024;
+static_assert(TK == DUSTIN_MAX_BLOCK, "the draft block must fit one tile");
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) attend_kernel(const __grid_constant__ AttendArgs A) {
+// Tensor memory, query buffers and K/V stages per head dimension and CTAs per
+// SM: with two CTAs per SM (256 columns each) P is stored over the S buffer it
+// came from, and the next segment's query rows wait for this one's MMAs.
+template <int D, int CPS>
+struct Cfg {
+  static constexpr int cols = CPS == 2 ? 256 : (D == 128 ? 512 : 256);
+  static constexpr int o_col = CPS == 2 ? 128 : (D == 128 ? 256 : 192);
+  static constexpr int p_col = CPS == 2 ? kSCol : kPCol;
+  static constexpr int p_stride = CPS == 2 ? TK : TK / 2;
+  static constexpr int nqb = CPS == 2 ? 1 : 2;
+  static constexpr int nst = CPS == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr uint32_t kv_panel = TK * 128;
+  static constexpr uint32_t half = (D / 64) * kv_panel;
+  static constexpr uint32_t stage = 2 * half;
+};
+
+struct Lay {
+  uint32_t q_panel, q_buf, ring_off, bar_off, misc_off, total;
+};
+
+template <int D, int CPS>
+__host__ __device__ inline Lay make_lay(int NQ) {
+  using C = Cfg<D, CPS>;
+  Lay L;
+  const int q_rows = NQ < 8 ? 8 : (NQ + 7) & ~7;
+  L.q_panel = uint32_t(q_rows) * 128;
+  L.q_buf = (D / 64) * L.q_panel;
+  L.ring_off = (C::nqb * L.q_buf + 1023u) & ~1023u;
+  L.bar_off = L.ring_off + C::nst * C::stage;
+  L.misc_off = L.bar_off + uint32_t(2 * C::nst + 4 + 2 * C::nqb + 2) * 8;
+  L.total = L.misc_off + 48 + 1024;
+  return L;
+}
+
+// The tiles of one sequence's units.
+struct Tiles {
+  int L, w0;      // rows; start of the window range
+  int nA, nB, n;  // tiles of the first and the window range; all, the block tile included
+  int a_end;      // rows of the first range
+};
+__device__ __forceinline__ Tiles tiles_of(const AttendArgs& A, int b) {
+  Tiles s;
+  int L = A.seq_len[b];
+  if (L < 0 || L > A.Lcap) L = 0;
+  s.L = L;
+  s.a_end = min(A.sinks, L);
+  int w0 = A.window > 0 ? L - A.window + 1 : L;   // the first query's window
+  if (A.window > 0 && w0 <= s.a_end) {            // the ranges meet: one range [0, L)
+    s.a_end = L;
+    w0 = L;
+  }
+  s.w0 = w0;
+  s.nA = (s.a_end + TK - 1) / TK;
+  s.nB = (L - w0 + TK - 1) / TK;
+  s.n = s.nA + s.nB + 1;
+  return s;
+}
+
+// Walks this CTA's segments: tiles [ta, ta + n) of unit (b, g).
+struct Walk {
+  long long left;     // tiles this CTA still has
+  int b, g, ta, n;
+  Tiles s;
+};
+__device__ __forceinline__ void walk_init(Walk& w, const AttendArgs& A, long long count, int b0, long long rem0) {
+  w.left = count;
+  w.b = b0;
+  if (count > 0) {
+    w.s = tiles_of(A, b0);
+    w.g = int(rem0 / w.s.n);
+    w.ta = int(rem0 - (long long)w.g * w.s.n);
+    w.n = int(w.left < w.s.n - w.ta ? w.left : w.s.n - w.ta);
+  }
+}
+__device__ __forceinline__ void walk_next(Walk& w, const AttendArgs& A) {
+  w.left -= w.n;
+  if (w.left <= 0) return;
+  if (++w.g == A.hkv) {
+    w.g = 0;
+    ++w.b;
+    w.s = tiles_of(A, w.b);
+  }
+  w.ta = 0;
+  w.n = int(w.left < w.s.n ? w.left : w.s.n);
+}
+
+// First key position and number of rows of tile tt.
+__device__ __forceinline__ void tile_rows(const Walk& w, int T, int tt, int& base, int& nv, bool& blk) {
+  const Tiles& s = w.s;
+  blk = tt == s.n - 1;
+  if (blk) {
+    base = s.L;
+    nv = T;
+  } else if (tt < s.nA) {
+    base = tt * TK;
+    nv = min(TK, s.a_end - base);
+  } else {
+    base = s.w0 + (tt - s.nA) * TK;
+    nv = min(TK, s.L - base);
+  }
+}
+
+// M: rows of the MMAs, 64 when the query rows fit (16 rows per lane quarter),
+// else 128 (one row per lane).  CPS: CTAs per SM (2 only with M = 64).
+template <int D, int M, int CPS>
+__global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant__ AttendArgs A) {
+  static_assert(M == 64 || M == 128, "MMA rows");
+  static_assert(CPS == 1 || (CPS == 2 && M == 64), "two CTAs per SM only with 64-row MMAs");
+  using C = Cfg<D, CPS>;
+  constexpr int NST = C::nst, NQB = C::nqb;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int T = A.T, GQ = A.hq / A.hkv, NQ = T * GQ;
+  const Lay Ly = make_lay<D, CPS>(NQ);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly.bar_off);
+  uint64_t* empty = full + NST;
+  uint64_t* s_full = empty + NST;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* q_full = p_full + 2;
+  uint64_t* q_empty = q_full + NQB;
+  uint64_t* mma_done = q_empty + NQB;
+  uint64_t* pv_done = mma_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly.misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly.misc_off + 8);
+  int* q_hi = reinterpret_cast<int*>(smem + Ly.misc_off + 12);   // query loads issued: [0, q_hi)
+  long long* share = reinterpret_cast<long long*>(smem + Ly.misc_off + 16);   // tiles, offset in b0, b0
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int n_act = M == 64 ? (NQ + 15) >> 4 : (NQ + 31) >> 5;   // softmax warps holding query rows
+  if (tid == 32) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 32 * kLoaders + kLoaders);
+      mbar_init(&empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 32 * n_act);
+    }
+    for (int x = 0; x < NQB; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(pv_done, 1);
+    *abort_flag = 0;
+    *q_hi = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "n"(C::cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int NC = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int T = A.T, hq = A.hq, G = hq / A.hkv;
-  if (row >= (long long)A.B * T * hq) return;
-  const int h = int(row % hq), t = int(row / hq % T), b = int(row / hq / T), g = h / G;
-  int L = A.seq_len[b];
-  if (L < 0 || L > A.Lcap) {
-    if (lane == 0 && h == 0 && t == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
-    L = 0;
-  }
-  int P = 0;
-  if (A.prefix_len) {
-    P = *A.prefix_len;
-    if (P < 0 || P > A.Pcap) {
-      if (lane == 0 && row == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
-      P = 0;
+  if (warp == 0) {
+    // this CTA's share [t0, t1) of the batch's tiles and the sequence it starts in
+    long long total = 0;
+    for (int b0 = 0; b0 < A.B; b0 += 32) {
+      int n = b0 + lane < A.B ? tiles_of(A, b0 + lane).n * A.hkv : 0;
+      if (blockIdx.x == 0 && b0 + lane < A.B) {
+        const int L = A.seq_len[b0 + lane];
+        if (L < 0 || L > A.Lcap) flag_error(A.err, DUSTIN_DEV_SEQLEN);
+      }
+      total += __reduce_add_sync(0xffffffffu, unsigned(n));
+    }
+    // (at most as many CTAs as tiles: a unit's segments then lie in consecutive CTAs)
+    const long long ctas = total < gridDim.x ? total : gridDim.x;
+    const long long t0 = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
+    const long long t1 = blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
+    long long before = 0;
+    int at = 0;
+    for (int b0 = 0; b0 < A.B; b0 += 32) {
+      const int n = b0 + lane < A.B ? tiles_of(A, b0 + lane).n * A.hkv : 0;
+      int inc = n;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, x);
+        if (lane >= x) inc += y;
+      }
+      const long long end = before + inc;
+      const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && t0 < end);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        at = b0 + src;
+        before = __shfl_sync(0xffffffffu, end - n, src);
+        break;
+      }
+      before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) {
+      share[0] = t1 - t0;
+      share[1] = t0 - before;
+      share[2] = at;
     }
   }
-  float q[NC], o[NC];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk w;
+  walk_init(w, A, share[0], int(share[2]), share[1]);
+
+  if (warp >= kLoaderWarp0 && warp < kLoaderWarp0 + kLoaders) {
+    // =============================================================== loaders
+    const int lw = warp - kLoaderWarp0;
+    constexpr int CH = D / 8;             // 16-byte chunks per row
+    constexpr int KPI = 32 / CH;          // rows per warp instruction
+    constexpr int NI = kKpw / KPI;        // instructions per tensor
+    const int c = lane % CH, ksub = lane / CH;
+    int gi = 0, s = 0;
+    bool live = true;     // false once a wait gave up
+    uint32_t tmask = 0;   // bit j: tile gi - 1 - j came by TMA boxes
+    const uint64_t pol = policy_evict_first();
+    for (; w.left > 0 && live; walk_next(w, A), ++s) {
+      // this segment's query rows -> query buffer s % NQB, once the MMAs of the
+      // segment that used it last are done
+      const int qb = s % NQB;
+      if (s % kLoaders == lw) {
+        bool ok = true;
+        if (lane == 0) {
+          if (s >= NQB) ok = mbar_wait(&q_empty[qb], uint32_t(s / NQB - 1) & 1u, A.err, abort_flag);
+          if (ok) {
+            mbar_arrive_expect_tx(&q_full[qb], uint32_t(NQ) * D * 2);
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    q[c] = __uint_as_float(uint32_t(A.q[row * D + 32 * c + lane]) << 16) * A.scale_log2;
-    o[c] = 0.f;
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sbase + qb * Ly.q_buf + h * Ly.q_panel, &A.qmap, h * 64, w.g * GQ, w.b * T, &q_full[qb]);
+            atomicMax(q_hi, s + 1);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
+      }
+      const uint16_t* kbase = A.k + size_t(w.b) * A.ksb + size_t(w.g) * A.ksh;
+      const uint16_t* vbase = A.v + size_t(w.b) * A.vsb + size_t(w.g) * A.vsh;
+      const size_t blk_off = (size_t(w.b) * A.hkv + w.g) * T * D;
+      for (int i = 0; i < w.n; ++i, ++gi) {
+        int base, nv;
+        bool blk;
+        tile_rows(w, T, w.ta + i, base, nv, blk);
+        const int st = gi % NST;
+        if (gi >= NST &&
+            !__all_sync(0xffffffffu, mbar_wait(&empty[st], uint32_t(gi / NST - 1) & 1u, A.err, abort_flag))) {
+          live = false;
+          break;
+        }
+        const uint32_t stage = sbase + Ly.ring_off + uint32_t(st) * C::stage;
+        const bool by_tma = A.tma && !blk && nv == TK;
+        tmask = (tmask << 1) | uint32_t(by_tma);
+        if (by_tma) {
+          // boxes issued by one lane, the byte count armed with its arrival
+          // (the other threads arrive as for gathered rows, with nothing in flight)
+          if (lw == 0 && lane == 0) {
+            mbar_arrive_expect_tx(&full[st], C::stage);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              const uint32_t dk = stage + h * C::kv_panel, dv = dk + C::half;
+              const int row = (w.b * A.hkv + w.g) * A.Lcap + base;
+              if (A.krank == 2) tma_load_2d_u32(dk, &A.kmap, h * 64, row, &full[st], pol);
+              else tma_load_4d_u32(dk, &A.kmap, h * 64, base, w.g, w.b, &full[st], pol);
+              if (A.vrank == 2) tma_load_2d_u32(dv, &A.vmap, h * 64, row, &full[st], pol);
+              else tma_load_4d_u32(dv, &A.vmap, h * 64, base, w.g, w.b, &full[st], pol);
+            }
+          } else if (lane == 0) {
+            mbar_arrive(&full[st]);
+          }
+          cp_async_arrive_noinc(&full[st]);
+          continue;
+        }
+        const uint16_t* ksrc = blk ? A.kb + blk_off : kbase + size_t(base) * A.ksl;
+        const uint16_t* vsrc = blk ? A.vb + blk_off : vbase + size_t(base) * A.vsl;
+        const int64_t kst = blk ? D : A.ksl, vst = blk ? D : A.vsl;
+#pragma unroll
+        for (int m = 0; m < 2 * NI; ++m) {
+          const int which = m / NI;
+          const int key = kKpw * lw + (m % NI) * KPI + ksub;
+          const bool ok = key < nv;
+          const uint16_t* src = which ? vsrc + size_t(ok ? key : 0) * vst : ksrc + size_t(ok ? key : 0) * kst;
+          cp_async16(stage + which * C::half + uint32_t(c >> 3) * C::kv_panel + swz(key, c & 7), src + c * 8,
+                     ok ? 16u : 0u);
+        }
+        cp_async_arrive_noinc(&full[st]);
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+    }
+    cp_async_wait_all();
+    // the boxes this lane issued for the last NST tiles have landed (each is
+    // the latest phase of its stage) before the CTA may exit
+    if (lw == 0 && lane == 0)
+      for (int j = 0; j < NST && j < gi; ++j)
+        if ((tmask >> j) & 1u) mbar_drain(&full[(gi - 1 - j) % NST], uint32_t((gi - 1 - j) / NST) & 1u, A.err);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ================================================================ S MMAs
+    if (lane == 0) {
+      constexpr uint32_t kIdS = tc_idesc(M, TK, 0);
+      int gi = 0, s = 0;
+      bool issued = false, live = true;
+      for (; w.left > 0 && live; walk_next(w, A), ++s) {
+        const int qb = s % NQB;
+        const uint32_t qbuf = sbase + qb * Ly.q_buf;
+        if (!mbar_wait(&q_full[qb], uint32_t(s / NQB) & 1u, A.err, abort_flag)) break;
+        for (int i = 0; i < w.n; ++i, ++gi) {
+          const int st = gi % NST;
+          if ((gi >= 2 && !(CPS == 2 ? mbar_wait(&empty[(gi - 2) % NST], uint32_t((gi - 2) / NST) & 1u, A.err, abort_flag)
+                                     : mbar_wait(&p_full[gi & 1], uint32_t((gi >> 1) - 1) & 1u, A.err, abort_flag))) ||
+              !mbar_wait(&full[st], uint32_t(gi / NST) & 1u, A.err, abort_flag)) {
+            live = false;
+            break;
+          }
+          issued = true;
+          fence_proxy_async();   // partial tiles were written by cp.async (generic proxy)
+          tc_fence_after();
+          const uint32_t kst = sbase + Ly.ring_off + uint32_t(st) * C::stage;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t koff = uint32_t((kk & 3) * 32);
+            const uint64_t a = tc_desc(qbuf + (kk >> 2) * Ly.q_panel + koff, 16, 1024);
+            const uint64_t bd = tc_desc(kst + (kk >> 2) * C::kv_panel + koff, 16, 1024);
+            tc_mma_ss(tmem + uint32_t(kSCol + (gi & 1) * TK), a, bd, kIdS, kk > 0);
+          }
+          tc_commit(&s_full[gi & 1]);
+        }
+        if (live) tc_commit(&q_empty[qb]);   // the segment's query rows are no longer read
+      }
+      if (issued) {   // every MMA this thread issued has completed before tensor memory is freed
+        tc_commit(mma_done);
+        mbar_drain(mma_done, 0, A.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ============================================================== P V MMAs
+    if (lane == 0) {
+      constexpr uint32_t kIdPV = tc_idesc(M, D, 1);
+      int gi = 0;
+      bool issued = false, live = true;
+      for (; w.left > 0 && live; walk_next(w, A)) {
+        for (int i = 0; i < w.n; ++i, ++gi) {
+          if (!mbar_wait(&p_full[gi & 1], uint32_t(gi >> 1) & 1u, A.err, abort_flag)) {
+            live = false;
+            break;
+          }
+          issued = true;
+          tc_fence_after();
+          const int st = gi % NST;
+          const uint32_t vst = sbase + Ly.ring_off + uint32_t(st) * C::stage + C::half;
+          const uint32_t p_tmem = tmem + uint32_t(C::p_col + (gi & 1) * C::p_stride);
+#pragma unroll
+          for (int kk = 0; kk < TK / 16; ++kk)
+            tc_mma_ts(tmem + C::o_col, p_tmem + uint32_t(kk * 8), tc_desc(vst + uint32_t(kk * 2048), C::kv_panel, 1024),
+                      kIdPV, (i > 0 || kk > 0) ? 1 : 0);
+          tc_commit(&empty[st]);   // S and P V of tile gi done: its stage is free
+        }
+      }
+      if (issued) {
+        tc_commit(pv_done);
+        mbar_drain(pv_done, 0, A.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp < n_act) {
+    // =============================================================== softmax
+    // M = 128: thread tid holds row tid.  M = 64: warp x holds rows 16 x ..
+    // 16 x + 15; thread y takes rows 16 x + y / 4 and that + 8 and, of each, the
+    // keys 8 c + 2 (y % 4) + {0, 1}; the four threads of a quad share maxima by
+    // shuffles and add their partial sums up at the end.
+    constexpr int R = M == 64 ? 2 : 1;          // rows of this thread
+    constexpr int KR = M == 64 ? 16 : 64;       // scores of each row
+    const int q4 = lane & 3;
+    int row[R], tq[R];
+    bool act[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      row[r] = M == 64 ? 16 * warp + (lane >> 2) + 8 * r : tid;
+      act[r] = row[r] < NQ;
+      tq[r] = act[r] ? row[r] / GQ : 0;
+    }
+    const float scale = A.scale_log2;
+    const uint32_t lane_base = tmem + (uint32_t(warp * 32) << 16);
+    const uint32_t o_lane = lane_base + uint32_t(C::o_col);
+    int gi = 0;
+    bool live = true;   // false once a wait gave up (warp-uniform)
+    for (; w.left > 0 && live; walk_next(w, A)) {
+      float mref[R], lsum[R];   // reference maxima (log2 domain), this thread's share of the row sums
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mref[r] = -INFINITY;
+        lsum[r] = 0.f;
+      }
+      for (int i = 0; i < w.n; ++i, ++gi) {
+        int base, nv;
+        bool blk;
+        tile_rows(w, T, w.ta + i, base, nv, blk);
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[gi & 1], uint32_t(gi >> 1) & 1u, A.err, abort_flag))) {
+          live = false;
+          break;
+        }
+        tc_fence_after();
+        float x[R][KR];
+        if constexpr (M == 64) {
+          uint32_t sv[32];
+          tc_ld16x256_x8(lane_base + uint32_t(kSCol + (gi & 1) * TK), sv);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              x[r][2 * c] = __uint_as_float(sv[4 * c + 2 * r]);
+              x[r][2 * c + 1] = __uint_as_float(sv[4 * c + 2 * r + 1]);
+            }
+        } else {
+          tc_ld32(lane_base + uint32_t(kSCol + (gi & 1) * TK), reinterpret_cast<uint32_t*>(x[0]));
+          tc_ld32(lane_base + uint32_t(kSCol + (gi & 1) * TK + 32), reinterpret_cast<uint32_t*>(x[0] + 32));
+        }
+        // masks: rows past nv, keys outside a row's window (sinks apart), u > t
+        const int lo0 = w.s.L - A.window + 1 - base;   // row 0's first key in the window
+        const int sk = A.sinks - base;                 // keys before it are sinks
+        if (blk || nv < TK || (lo0 + T - 1 > 0 && sk < TK)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int lo = lo0 + tq[r], hi = blk ? tq[r] + 1 : nv;
+#pragma unroll
+            for (int j = 0; j < KR; ++j) {
+              const int key = M == 64 ? 8 * (j >> 1) + 2 * q4 + (j & 1) : j;
+              x[r][j] = key < hi && (key >= lo || key < sk) ? x[r][j] : -INFINITY;
+            }
+          }
+        }
+        float mx[R], alpha[R], nb[R];
+        bool moved = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float m4[4] = {x[r][0], x[r][1], x[r][2], x[r][3]};
+#pragma unroll
+          for (int j = 4; j < KR; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[r][j]);
+          mx[r] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          if constexpr (M == 64) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+          }
+          // (a row past NQ takes -inf as its max: it never rescales O, and its
+          // P and O rows are never read)
+          mx[r] = act[r] ? mx[r] * scale : -INFINITY;
+          alpha[r] = 1.f;
+          if (mx[r] > mref[r] + 8.f) {   // also the first tile with a visible key
+            alpha[r] = fast_exp2(mref[r] - mx[r]);
+            mref[r] = mx[r];
+            lsum[r] *= alpha[r];
+            moved = true;
+          }
+          nb[r] = mref[r] == -INFINITY ? 0.f : -mref[r];
+        }
+        uint32_t pk[R * KR / 2];   // M = 64: entry 2 c + r is row r's pair of chunk c
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float l2[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < KR; j += 2) {
+            const float p0 = fast_exp2(fmaf(x[r][j], scale, nb[r])), p1 = fast_exp2(fmaf(x[r][j + 1], scale, nb[r]));
+            pk[M == 64 ? j + r : j / 2] = pack_bf16(p0, p1);
+            l2[0] += p0;
+            l2[1] += p1;
+          }
+          lsum[r] += l2[0] + l2[1];
+        }
+        // rescale O once P V of the previous tile is in (the first tile of a
+        // segment overwrites O); tensor-memory accesses are collective
+        if (i > 0 && __any_sync(0xffffffffu, moved)) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[(gi - 1) % NST], uint32_t((gi - 1) / NST) & 1u, A.err, abort_flag))) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            if constexpr (M == 64) {
+              uint32_t o[16];
+              tc_ld16x256_x4(o_lane + uint32_t(c), o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha[(y >> 1) & 1]);
+              tc_st16x256_x4(o_lane + uint32_t(c), o);
+            } else {
+              uint32_t o[32];
+              tc_ld32(o_lane + uint32_t(c), o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha[0]);
+              tc_st32(o_lane + uint32_t(c), o);
+            }
+          }
+        }
+        // P buffer gi % 2 is free once P V of tile gi - 2 has completed (when P
+        // is stored over S, S of tile gi was issued only after that)
+        if (CPS == 1 && gi >= 2 &&
+            !__all_sync(0xffffffffu, mbar_wait(&empty[(gi - 2) % NST], uint32_t((gi - 2) / NST) & 1u, A.err, abort_flag))) {
+          live = false;
+          break;
+        }
+        const uint32_t p_tmem = lane_base + uint32_t(C::p_col + (gi & 1) * C::p_stride);
+        if constexpr (M == 64) tc_st16x128_x8(p_tmem, pk);
+        else tc_st32(p_tmem, pk);
+        tc_fence_before();
+        mbar_arrive(&p_full[gi & 1]);
+      }
+      if (!live) break;
+      // ----------------------------------------------------------- epilogue
+      const bool whole = A.direct && w.n == w.s.n;
+      const long long unit = (long long)w.b * A.hkv + w.g;
+      if (tid == 0) {
+        if (w.ta == 0) A.seg_cta[2 * unit] = int(blockIdx.x);
+        if (w.ta + w.n == w.s.n) A.seg_cta[2 * unit + 1] = int(blockIdx.x);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[(gi - 1) % NST], uint32_t((gi - 1) / NST) & 1u, A.err, abort_flag))) {
+        live = false;
+        break;
+      }
+      tc_fence_after();
+      float* part = A.partial + (size_t(unit) + blockIdx.x) * A.slot_floats;
+      size_t orow[R];
+      float osc[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if constexpr (M == 64) {
+          lsum[r] += __shfl_xor_sync(0xffffffffu, lsum[r], 1);
+          lsum[r] += __shfl_xor_sync(0xffffffffu, lsum[r], 2);
+        }
+        const int rr = act[r] ? row[r] : 0;
+        orow[r] = (size_t(w.b) * T + rr / GQ) * A.hq + size_t(w.g) * GQ + rr % GQ;
+        osc[r] = lsum[r] > 0.f ? 1.f / lsum[r] : 0.f;
+        if (act[r] && (M == 128 || q4 == 0)) {
+          if (whole) {
+            if (A.lse)
+              A.lse[orow[r]] = lsum[r] > 0.f ? (mref[r] + log2f(lsum[r])) * kLn2 : -INFINITY;
+          } else {
+            part[size_t(NQ) * D + row[r]] = mref[r];
+            part[size_t(NQ) * D + NQ + row[r]] = lsum[r];
+          }
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        if constexpr (M == 64) {
+          uint32_t o[16];
+          tc_ld16x256_x4(o_lane + uint32_t(c), o);   // collective: every lane loads
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (!act[r]) continue;
+              const int col = c + 8 * cc + 2 * q4;
+              const float o0 = __uint_as_float(o[4 * cc + 2 * r]), o1 = __uint_as_float(o[4 * cc + 2 * r + 1]);
+              if (whole) *reinterpret_cast<uint32_t*>(A.o + orow[r] * D + col) = pack_bf16(o0 * osc[r], o1 * osc[r]);
+              else *reinterpret_cast<float2*>(part + size_t(row[r]) * D + col) = make_float2(o0, o1);
+            }
+        } else {
+          uint32_t o[32];
+          tc_ld32(o_lane + uint32_t(c), o);
+          if (act[0]) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              float f[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) f[z] = __uint_as_float(o[y + z]);
+              if (whole) {
+                *reinterpret_cast<uint4*>(A.o + orow[0] * D + c + y) =
+                    make_uint4(pack_bf16(f[0] * osc[0], f[1] * osc[0]), pack_bf16(f[2] * osc[0], f[3] * osc[0]),
+                               pack_bf16(f[4] * osc[0], f[5] * osc[0]), pack_bf16(f[6] * osc[0], f[7] * osc[0]));
+              } else {
+                float4* dst = reinterpret_cast<float4*>(part + size_t(row[0]) * D + c + y);
+                dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
   }
-  float m = -INFINITY, l = 0.f;
-  auto key = [&](const uint16_t* kr, const uint16_t* vr) {
-    float s = 0.f;
+
+  // Every query load has been issued: the last NQB of them (each the latest
+  // phase of its buffer) have landed before the CTA exits.
+  __syncthreads();
+  if (warp == kLoaderWarp0 && lane == 0) {
+    const int hi = *q_hi;
+    for (int x = hi - NQB < 0 ? 0 : hi - NQB; x < hi; ++x) mbar_drain(&q_full[x % NQB], uint32_t(x / NQB) & 1u, A.err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::cols) : "memory");
+}
+
+// Log-sum-exp merge of a unit's segments: one thread per four output columns.
+// A segment is (unnormalised O, log2-domain reference maximum m, sum l).
+constexpr int kMergeThreads = 128;
+
+struct Merge {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void merge_in(Merge& a, float m, float l, const float4& o) {
+  const float top = fmaxf(a.m, m);
+  const float ref = top == -INFINITY ? 0.f : top;
+  const float x = exp2f(a.m - ref), y = exp2f(m - ref);   // exp2(-inf) = 0
+  a.m = top;
+  a.l = a.l * x + l * y;
+  a.o.x = a.o.x * x + o.x * y;
+  a.o.y = a.o.y * x + o.y * y;
+  a.o.z = a.o.z * x + o.z * y;
+  a.o.w = a.o.w * x + o.w * y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendArgs A) {
+  pdl_launch_dependents();
+  pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
+  const int unit = blockIdx.y, T = A.T, GQ = A.hq / A.hkv, NQ = T * GQ;
+  const int c0 = A.seg_cta[2 * unit], c1 = A.seg_cta[2 * unit + 1];
+  if (A.direct && c0 == c1) return;   // written by its CTA
+  const int x = blockIdx.x * kMergeThreads + threadIdx.x;
+  if (x >= NQ * (D / 4)) return;
+  const int r = x / (D / 4), c4 = x - r * (D / 4);
+  const size_t mo = size_t(NQ) * D;
+  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const float* p = A.partial + (size_t(unit) + c0) * A.slot_floats;
+  for (int c = c0; c <= c1; c += 4) {   // four segments' loads in flight at once
+    float m[4], l[4];
+    float4 o[4];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) s = fmaf(q[c], __uint_as_float(uint32_t(kr[32 * c + lane]) << 16), s);
+    for (int y = 0; y < 4; ++y) {
+      m[y] = -INFINITY;
+      l[y] = 0.f;
+      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + y <= c1) {
+        const float* s = p + size_t(c - c0 + y) * A.slot_floats;
+        m[y] = __ldcg(s + mo + r);
+        l[y] = __ldcg(s + mo + NQ + r);
+        o[y] = __ldcg(reinterpret_cast<const float4*>(s + size_t(r) * D) + c4);
+      }
+    }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s);
-    const float a = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      o[c] = o[c] * a + w * __uint_as_float(uint32_t(vr[32 * c + lane]) << 16);
-  };
-  for (int j = 0; j < P; ++j)
-    key(A.pk + size_t(g) * A.pksh + size_t(j) * A.pksl, A.pv + size_t(g) * A.pvsh + size_t(j) * A.pvsl);
-  const long long i = (long long)L + t;
-  const int s_end = A.sinks < L ? A.sinks : L;
-  const long long lo = i - A.window + 1;
-  const uint16_t* kc = A.k + size_t(b) * A.ksb + size_t(g) * A.ksh;
-  const uint16_t* vc = A.v + size_t(b) * A.vsb + size_t(g) * A.vsh;
-  for (int j = 0; j < s_end; ++j) key(kc + size_t(j) * A.ksl, vc + size_t(j) * A.vsl);
-  for (long long j = lo > s_end ? lo : s_end; j < L; ++j)
-    key(kc + size_t(j) * A.ksl, vc + size_t(j) * A.vsl);
-  const size_t blk = (size_t(b) * A.hkv + g) * T * D;
-  for (int u = 0; u <= t; ++u)
-    if (t - u < A.window || L + u < A.sinks) key(A.kb + blk + size_t(u) * D, A.vb + blk + size_t(u) * D);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-    A.o[row * D + 32 * c + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * inv));
-  if (A.lse && lane == 0) A.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int y = 0; y < 4; ++y) merge_in(a, m[y], l[y], o[y]);
+  }
+  const int b = unit / A.hkv, g = unit % A.hkv;
+  const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
+  const float inv = a.l > 0.f ? 1.f / a.l : 0.f;
+  reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
+      make_uint2(pack_bf16(a.o.x * inv, a.o.y * inv), pack_bf16(a.o.z * inv, a.o.w * inv));
+  if (A.lse && c4 == 0) A.lse[orow] = a.l > 0.f ? (a.m + log2f(a.l)) * kLn2 : -INFINITY;
+}
+
+template <int D, int M, int CPS>
+cudaError_t launch_attend(const AttendArgs& a, int grid, size_t smem, cudaStream_t stream) {
+  auto kern = attend_kernel<D, M, CPS>;
+  static const cudaError_t attr = [&] {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess && CPS > 1)   // room for CPS CTAs' shared memory
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               int(cudaSharedmemCarveoutMaxShared));
+    return e;
+  }();
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(kern, dim3(grid), dim3(NTH), smem, stream, a);
+}
+
+template <int D>
+cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
+  const int NQ = a.T * (a.hq / a.hkv);
+  // 64-row MMAs while the query rows fit, two CTAs per SM while two fit
+  const bool two = NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
+  long long most = (long long)a.B * a.hkv * a.max_tiles;
+  int grid = (two ? 2 : 1) * num_sms;
+  if (grid > kAttendGridMax) grid = kAttendGridMax;
+  if (grid > most) grid = int(most);
+  cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
+                  : NQ <= 64 ? launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream)
+                             : launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
+  if (e != cudaSuccess) return e;
+  const dim3 mgrid((NQ * (D / 4) + kMergeThreads - 1) / kMergeThreads, unsigned(a.B * a.hkv));
+  return launch_pdl(attend_merge_kernel<D>, mgrid, dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace
 
-size_t attend_scratch_bytes(int, int, int, int, int, int) { return 0; }
-
-cudaError_t attend_launch(const AttendArgs& a, int D, cudaStream_t stream) {
-  const long long rows = (long long)a.B * a.T * a.hq;
-  const dim3 grid(unsigned((rows + kWarps - 1) / kWarps));
-  return D == 128 ? launch_pdl(attend_kernel<128>, grid, dim3(32 * kWarps), 0, stream, a)
-                  : launch_pdl(attend_kernel<64>, grid, dim3(32 * kWarps), 0, stream, a);
+cudaError_t attend_launch(const AttendArgs& a, int D, int num_sms, cudaStream_t stream) {
+  return D == 128 ? launch_d<128>(a, num_sms, stream) : launch_d<64>(a, num_sms, stream);
 }
 
 }  // namespace dustin

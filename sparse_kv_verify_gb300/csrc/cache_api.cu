@@ -2,7 +2,7 @@
 // accumulated attention weights, eviction): argument checks and launches.
 // Nothing here allocates device memory.  Workspace: the header of api.cu, then
 // the scratch of the one operator that runs.
-#include <climits>
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -28,6 +28,22 @@ int attend_shape(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d) {
   return DUSTIN_OK;
 }
 
+// Workspace of an attention call, after the fixed part: every unit's first and
+// last CTA, then the segment slots.
+struct AttendPlan {
+  int64_t slot_floats;
+  size_t seg_off, part_off, total;
+};
+AttendPlan attend_plan(int B, int hq, int hkv, int d, int T) {
+  AttendPlan pl;
+  const int64_t units = int64_t(B) * hkv, NQ = int64_t(T) * (hq / hkv);
+  pl.slot_floats = (NQ * d + 2 * NQ + 3) / 4 * 4;   // 16-byte aligned slots
+  pl.seg_off = kScratch;
+  pl.part_off = round256(pl.seg_off + size_t(units) * 2 * 4);
+  pl.total = round256(pl.part_off + size_t(units + kAttendGridMax) * size_t(pl.slot_floats) * 4);
+  return pl;
+}
+
 // pk == nullptr: windowed attention.
 int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_kv* pk, const dustin_kv* pv,
                int32_t prefix_cap, const int32_t* prefix_len, const dustin_kv& k, const dustin_kv& v,
@@ -45,16 +61,16 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
   }
   const int st = attend_shape(p, hq, k.hkv, k.d);
   if (st != DUSTIN_OK) return st;
-  const size_t need = kScratch + attend_scratch_bytes(p->B, hq, k.hkv, k.d, p->gamma + 1, pk ? prefix_cap : 0);
-  if (!ws_ok(ws, ws_bytes, need)) return DUSTIN_EWORKSPACE;
+  const AttendPlan pl = attend_plan(p->B, hq, k.hkv, k.d, p->gamma + 1);
+  if (!ws_ok(ws, ws_bytes, pl.total)) return DUSTIN_EWORKSPACE;
   AttendArgs a{};
   a.B = p->B;
   a.Lcap = p->Lcap;
   a.T = p->gamma + 1;
   a.hq = hq;
   a.hkv = k.hkv;
-  a.sinks = pk ? 0 : p->sinks;
-  a.window = pk ? INT_MAX : p->window;
+  a.sinks = pk ? 0 : std::min(p->sinks, kAttendFar);
+  a.window = pk ? kAttendFar : std::min(p->window, kAttendFar);
   a.Pcap = pk ? prefix_cap : 0;
   a.scale_log2 = scale_log2_of(k.d);
   a.q = static_cast<const uint16_t*>(q);
@@ -75,7 +91,19 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
   a.err = err_word(ws);
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  return attend_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+  if (pk) return prefix_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+  a.direct = 1;
+  const int tile = kAttendTile;
+  const auto tiles = [&](int rows) { return (std::min(rows, p->Lcap) + tile - 1) / tile; };
+  a.max_tiles = tiles(a.sinks) + tiles(a.window) + 1;
+  a.seg_cta = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + pl.seg_off);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.part_off);
+  a.slot_floats = pl.slot_floats;
+  if (!encode_query_map(&a.qmap, q, k.d, hq, p->B * a.T, hq / k.hkv, a.T)) return DUSTIN_ECUDA;
+  // caches that a tensor map cannot describe come row by row
+  a.tma = encode_cache_map(&a.kmap, k, p->Lcap, p->B, &a.krank, tile) &&
+          encode_cache_map(&a.vmap, v, p->Lcap, p->B, &a.vrank, tile);
+  return attend_launch(a, k.d, num_sms(), stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
 }
 
 }  // namespace
@@ -90,7 +118,7 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
   size_t need = kScratch;
   if (hq != 0) {
     if (attend_shape(p, hq, hkv, d) != DUSTIN_OK) return 0;
-    need = kScratch + attend_scratch_bytes(p->B, hq, hkv, d, p->gamma + 1, prefix_cap);
+    need = attend_plan(p->B, hq, hkv, d, p->gamma + 1).total;
   }
   if (n_layers != 0) {
     const size_t e = kScratch + evict_scratch_bytes(p->B, hkv, n_layers, p->k);

@@ -263,9 +263,14 @@ cudaError_t compact_launch(const CompactArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------- windowed / prefix attention
 
+constexpr int kAttendTile = 64;        // keys per tile
+constexpr int kAttendGridMax = 512;    // CTAs of the attention kernel at most
+constexpr int kAttendFar = 1 << 22;    // a window or sink count past every position
+constexpr float kLn2 = 0.69314718055994531f;
+
 struct AttendArgs {
   int B, Lcap, T, hq, hkv;
-  int sinks, window;         // shared-prefix attention: sinks = 0, window = INT32_MAX
+  int sinks, window;         // 0 .. kAttendFar; shared-prefix attention: 0 and kAttendFar
   int Pcap;                  // rows of the prefix caches (0: no prefix)
   float scale_log2;          // log2(e) / sqrt(D)
   const uint16_t* q;         // [B][T][hq][D]
@@ -281,9 +286,17 @@ struct AttendArgs {
   int* err;
   uint16_t* o;               // [B][T][hq][D] bf16
   float* lse;                // [B][T][hq], or nullptr
+  int direct;                // 1: a segment that covers its unit writes o and lse
+  int max_tiles;             // tiles of a unit at most
+  int32_t* seg_cta;          // [units][2]: first and last CTA of each unit's segments
+  float* partial;            // segment slots [units + grid][slot_floats]: O [NQ][D], m [NQ], l [NQ]
+  int64_t slot_floats;
+  int tma;                   // the caches have tensor maps (whole tiles come as TMA boxes)
+  int krank, vrank;          // 2: map over packed rows, 4: (d, Lcap, hkv, B)
+  CUtensorMap qmap, kmap, vmap;
 };
-size_t attend_scratch_bytes(int B, int hq, int hkv, int D, int T, int Pcap);
-cudaError_t attend_launch(const AttendArgs& a, int D, cudaStream_t stream);
+cudaError_t attend_launch(const AttendArgs& a, int D, int num_sms, cudaStream_t stream);
+cudaError_t prefix_launch(const AttendArgs& a, int D, cudaStream_t stream);
 
 // -------------------------------------------------------------- accumulate
 
