@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
       }
       if (!live) break;
       // ----------------------------------------------------------- epilogue
-      const bool whole = A.direct && w.n == w.s.n;
+      const bool whole = A.pgrid == 0 && w.n == w.s.n;
       const long long unit = (long long)w.b * A.hkv + w.g;
       if (tid == 0) {
         if (w.ta == 0) A.seg_cta[2 * unit] = int(blockIdx.x);
@@ -671,20 +671,10 @@ __device__ __forceinline__ void merge_in(Merge& a, float m, float l, const float
   a.o.w = a.o.w * x + o.w * y;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendArgs A) {
-  pdl_launch_dependents();
-  pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
-  const int unit = blockIdx.y, T = A.T, GQ = A.hq / A.hkv, NQ = T * GQ;
-  const int c0 = A.seg_cta[2 * unit], c1 = A.seg_cta[2 * unit + 1];
-  if (A.direct && c0 == c1) return;   // written by its CTA
-  const int x = blockIdx.x * kMergeThreads + threadIdx.x;
-  if (x >= NQ * (D / 4)) return;
-  const int r = x / (D / 4), c4 = x - r * (D / 4);
-  const size_t mo = size_t(NQ) * D;
-  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  const float* p = A.partial + (size_t(unit) + c0) * A.slot_floats;
-  for (int c = c0; c <= c1; c += 4) {   // four segments' loads in flight at once
+// segments p0, p0 + stride, ... (n of them); m at mo, l at mo + rows
+__device__ __forceinline__ void merge_segments(Merge& a, const float* p, size_t stride, int n, size_t at, size_t mo,
+                                               int rows) {
+  for (int c = 0; c < n; c += 4) {   // four segments' loads in flight at once
     float m[4], l[4];
     float4 o[4];
 #pragma unroll
@@ -692,17 +682,49 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
       m[y] = -INFINITY;
       l[y] = 0.f;
       o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + y <= c1) {
-        const float* s = p + size_t(c - c0 + y) * A.slot_floats;
-        m[y] = __ldcg(s + mo + r);
-        l[y] = __ldcg(s + mo + NQ + r);
-        o[y] = __ldcg(reinterpret_cast<const float4*>(s + size_t(r) * D) + c4);
+      if (c + y < n) {
+        const float* s = p + size_t(c + y) * stride;
+        m[y] = __ldcg(s + mo);
+        l[y] = __ldcg(s + mo + rows);
+        o[y] = __ldcg(reinterpret_cast<const float4*>(s + at));
       }
     }
 #pragma unroll
     for (int y = 0; y < 4; ++y) merge_in(a, m[y], l[y], o[y]);
   }
+}
+
+template <int D, bool PREFIX>
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendArgs A) {
+  pdl_launch_dependents();
+  pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
+  const int unit = blockIdx.y, T = A.T, GQ = A.hq / A.hkv, NQ = T * GQ;
+  const int c0 = A.seg_cta[2 * unit], c1 = A.seg_cta[2 * unit + 1];
+  if (!PREFIX && c0 == c1) return;   // written by its CTA
+  const int x = blockIdx.x * kMergeThreads + threadIdx.x;
+  if (x >= NQ * (D / 4)) return;
+  const int r = x / (D / 4), c4 = x - r * (D / 4);
   const int b = unit / A.hkv, g = unit % A.hkv;
+  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  merge_segments(a, A.partial + (size_t(unit) + c0) * A.slot_floats, size_t(A.slot_floats), c1 - c0 + 1,
+                 size_t(r) * D + 4 * c4, size_t(NQ) * D + r, NQ);
+  if constexpr (PREFIX) {
+    // the prefix segments of this row: unit pu's tiles [pu * n, (pu + 1) * n) of
+    // the flattened key tiles, CTA c holding [c * total / ctas, (c + 1) * total / ctas)
+    int P = *A.prefix_len;
+    if (P < 0 || P > A.Pcap) P = 0;
+    if (P > 0) {
+      const int tok = b * T + r / GQ, tile = tok / A.nt, pu = g * A.pairs + (tile >> 1);
+      const long long n = (P + kPrefixTile - 1) / kPrefixTile, total = n * A.hkv * A.pairs;
+      const long long ctas = total < A.pgrid ? total : A.pgrid;
+      auto cta_of = [&](long long t) { return int(((t + 1) * ctas + total - 1) / total) - 1; };
+      const int p0 = cta_of(pu * n), p1 = cta_of(pu * n + n - 1);
+      constexpr size_t kLane = size_t(kPrefixTile) * (D + 2);
+      const int row = (tok - tile * A.nt) * GQ + r % GQ;
+      merge_segments(a, A.ppartial + ((size_t(pu) + p0) * 2 + (tile & 1)) * kLane, 2 * kLane, p1 - p0 + 1,
+                     size_t(row) * D + 4 * c4, size_t(kPrefixTile) * D + row, kPrefixTile);
+    }
+  }
   const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
   const float inv = a.l > 0.f ? 1.f / a.l : 0.f;
   reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
@@ -736,9 +758,11 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
                   : NQ <= 64 ? launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream)
                              : launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
+  if (e == cudaSuccess && a.pgrid) e = prefix_launch(a, D, stream);
   if (e != cudaSuccess) return e;
   const dim3 mgrid((NQ * (D / 4) + kMergeThreads - 1) / kMergeThreads, unsigned(a.B * a.hkv));
-  return launch_pdl(attend_merge_kernel<D>, mgrid, dim3(kMergeThreads), 0, stream, a);
+  return a.pgrid ? launch_pdl(attend_merge_kernel<D, true>, mgrid, dim3(kMergeThreads), 0, stream, a)
+                 : launch_pdl(attend_merge_kernel<D, false>, mgrid, dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -29,18 +29,25 @@ int attend_shape(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d) {
 }
 
 // Workspace of an attention call, after the fixed part: every unit's first and
-// last CTA, then the segment slots.
+// last CTA, the segment slots of the sequences' own part, those of the prefix.
 struct AttendPlan {
   int64_t slot_floats;
-  size_t seg_off, part_off, total;
+  int nt, row_tiles, pairs;
+  size_t seg_off, part_off, ppart_off, total;
 };
-AttendPlan attend_plan(int B, int hq, int hkv, int d, int T) {
+AttendPlan attend_plan(int B, int hq, int hkv, int d, int T, bool prefix) {
   AttendPlan pl;
   const int64_t units = int64_t(B) * hkv, NQ = int64_t(T) * (hq / hkv);
   pl.slot_floats = (NQ * d + 2 * NQ + 3) / 4 * 4;   // 16-byte aligned slots
+  pl.nt = kPrefixTile / (hq / hkv);
+  pl.row_tiles = int((int64_t(B) * T + pl.nt - 1) / pl.nt);
+  pl.pairs = (pl.row_tiles + 1) / 2;
   pl.seg_off = kScratch;
   pl.part_off = round256(pl.seg_off + size_t(units) * 2 * 4);
-  pl.total = round256(pl.part_off + size_t(units + kAttendGridMax) * size_t(pl.slot_floats) * 4);
+  pl.ppart_off = round256(pl.part_off + size_t(units + kAttendGridMax) * size_t(pl.slot_floats) * 4);
+  pl.total = pl.ppart_off;
+  if (prefix)
+    pl.total += round256((size_t(hkv) * pl.pairs + kPrefixGridMax) * 2 * kPrefixTile * (size_t(d) + 2) * 4);
   return pl;
 }
 
@@ -61,7 +68,7 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
   }
   const int st = attend_shape(p, hq, k.hkv, k.d);
   if (st != DUSTIN_OK) return st;
-  const AttendPlan pl = attend_plan(p->B, hq, k.hkv, k.d, p->gamma + 1);
+  const AttendPlan pl = attend_plan(p->B, hq, k.hkv, k.d, p->gamma + 1, pk != nullptr);
   if (!ws_ok(ws, ws_bytes, pl.total)) return DUSTIN_EWORKSPACE;
   AttendArgs a{};
   a.B = p->B;
@@ -91,8 +98,6 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
   a.err = err_word(ws);
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  if (pk) return prefix_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
-  a.direct = 1;
   const int tile = kAttendTile;
   const auto tiles = [&](int rows) { return (std::min(rows, p->Lcap) + tile - 1) / tile; };
   a.max_tiles = tiles(a.sinks) + tiles(a.window) + 1;
@@ -103,7 +108,19 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
   // caches that a tensor map cannot describe come row by row
   a.tma = encode_cache_map(&a.kmap, k, p->Lcap, p->B, &a.krank, tile) &&
           encode_cache_map(&a.vmap, v, p->Lcap, p->B, &a.vrank, tile);
-  return attend_launch(a, k.d, num_sms(), stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+  const int sms = num_sms();
+  if (sms < 1) return DUSTIN_ECUDA;
+  if (pk) {
+    a.pgrid = std::min(sms, kPrefixGridMax);
+    a.nt = pl.nt;
+    a.row_tiles = pl.row_tiles;
+    a.pairs = pl.pairs;
+    a.ppartial = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.ppart_off);
+    if (!encode_query_map(&a.pqmap, q, k.d, hq, p->B * a.T, hq / k.hkv, pl.nt)) return DUSTIN_ECUDA;
+    a.ptma = encode_cache_map(&a.pkmap, *pk, prefix_cap, 1, &a.pkrank, kPrefixTile) &&
+             encode_cache_map(&a.pvmap, *pv, prefix_cap, 1, &a.pvrank, kPrefixTile);
+  }
+  return attend_launch(a, k.d, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
 }
 
 }  // namespace
@@ -118,7 +135,7 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
   size_t need = kScratch;
   if (hq != 0) {
     if (attend_shape(p, hq, hkv, d) != DUSTIN_OK) return 0;
-    need = attend_plan(p->B, hq, hkv, d, p->gamma + 1).total;
+    need = attend_plan(p->B, hq, hkv, d, p->gamma + 1, prefix_cap > 0).total;
   }
   if (n_layers != 0) {
     const size_t e = kScratch + evict_scratch_bytes(p->B, hkv, n_layers, p->k);

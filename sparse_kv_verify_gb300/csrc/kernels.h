@@ -265,6 +265,8 @@ cudaError_t compact_launch(const CompactArgs& a, cudaStream_t stream);
 
 constexpr int kAttendTile = 64;        // keys per tile
 constexpr int kAttendGridMax = 512;    // CTAs of the attention kernel at most
+constexpr int kPrefixTile = 128;       // keys, and query rows, per tile of the prefix kernel
+constexpr int kPrefixGridMax = 256;    // CTAs of the prefix kernel at most
 constexpr int kAttendFar = 1 << 22;    // a window or sink count past every position
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -286,15 +288,21 @@ struct AttendArgs {
   int* err;
   uint16_t* o;               // [B][T][hq][D] bf16
   float* lse;                // [B][T][hq], or nullptr
-  int direct;                // 1: a segment that covers its unit writes o and lse
   int max_tiles;             // tiles of a unit at most
   int32_t* seg_cta;          // [units][2]: first and last CTA of each unit's segments
   float* partial;            // segment slots [units + grid][slot_floats]: O [NQ][D], m [NQ], l [NQ]
   int64_t slot_floats;
   int tma;                   // the caches have tensor maps (whole tiles come as TMA boxes)
   int krank, vrank;          // 2: map over packed rows, 4: (d, Lcap, hkv, B)
-  CUtensorMap qmap, kmap, vmap;
+  // the prefix kernel (pgrid = 0: no prefix, and a segment of the attention
+  // kernel that covers its unit writes o and lse itself)
+  int pgrid;
+  int nt, row_tiles, pairs;  // tokens per row tile; row tiles of a KV head; pairs of them
+  float* ppartial;           // slots [(hkv * pairs + pgrid)][2][128 * (D + 2)]: O, m [128], l [128]
+  int ptma, pkrank, pvrank;
+  CUtensorMap qmap, kmap, vmap, pqmap, pkmap, pvmap;
 };
+// The attention kernel, the prefix kernel if there is a prefix, the merge.
 cudaError_t attend_launch(const AttendArgs& a, int D, int num_sms, cudaStream_t stream);
 cudaError_t prefix_launch(const AttendArgs& a, int D, cudaStream_t stream);
 
