@@ -37,6 +37,7 @@
 // and a second kernel merges them.
 #include "common.cuh"
 #include "kernels.h"
+#include "share.cuh"
 #include "tc.cuh"
 
 namespace dustin {
@@ -119,13 +120,13 @@ struct Walk {
   int b, g, ta, n;
   Tiles s;
 };
-__device__ __forceinline__ void walk_init(Walk& w, const AttendArgs& A, long long count, int b0, long long rem0) {
-  w.left = count;
-  w.b = b0;
-  if (count > 0) {
-    w.s = tiles_of(A, b0);
-    w.g = int(rem0 / w.s.n);
-    w.ta = int(rem0 - (long long)w.g * w.s.n);
+__device__ __forceinline__ void walk_init(Walk& w, const AttendArgs& A, const Share& sh) {
+  w.left = sh.count;
+  w.b = sh.b;
+  if (w.left > 0) {
+    w.s = tiles_of(A, w.b);
+    w.g = int(sh.offset / w.s.n);
+    w.ta = int(sh.offset - (long long)w.g * w.s.n);
     w.n = int(w.left < w.s.n - w.ta ? w.left : w.s.n - w.ta);
   }
 }
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly.misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly.misc_off + 8);
   int* q_hi = reinterpret_cast<int*>(smem + Ly.misc_off + 12);   // query loads issued: [0, q_hi)
-  long long* share = reinterpret_cast<long long*>(smem + Ly.misc_off + 16);   // tiles, offset in b0, b0
+  Share* share = reinterpret_cast<Share*>(smem + Ly.misc_off + 16);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -215,52 +216,18 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    // this CTA's share [t0, t1) of the batch's tiles and the sequence it starts in
-    long long total = 0;
-    for (int b0 = 0; b0 < A.B; b0 += 32) {
-      int n = b0 + lane < A.B ? tiles_of(A, b0 + lane).n * A.hkv : 0;
-      if (blockIdx.x == 0 && b0 + lane < A.B) {
-        const int L = A.seq_len[b0 + lane];
-        if (L < 0 || L > A.Lcap) flag_error(A.err, DUSTIN_DEV_SEQLEN);
-      }
-      total += __reduce_add_sync(0xffffffffu, unsigned(n));
-    }
-    // (at most as many CTAs as tiles: a unit's segments then lie in consecutive CTAs)
-    const long long ctas = total < gridDim.x ? total : gridDim.x;
-    const long long t0 = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-    const long long t1 = blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
-    long long before = 0;
-    int at = 0;
-    for (int b0 = 0; b0 < A.B; b0 += 32) {
-      const int n = b0 + lane < A.B ? tiles_of(A, b0 + lane).n * A.hkv : 0;
-      int inc = n;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, x);
-        if (lane >= x) inc += y;
-      }
-      const long long end = before + inc;
-      const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && t0 < end);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        at = b0 + src;
-        before = __shfl_sync(0xffffffffu, end - n, src);
-        break;
-      }
-      before = __shfl_sync(0xffffffffu, end, 31);
-    }
-    if (lane == 0) {
-      share[0] = t1 - t0;
-      share[1] = t0 - before;
-      share[2] = at;
-    }
+    const Share sh = share_of(A.B, [&](int b) { return tiles_of(A, b).n * A.hkv; });
+    if (lane == 0) *share = sh;
+    if (blockIdx.x == 0)
+      for (int b = lane; b < A.B; b += 32)
+        if (A.seq_len[b] < 0 || A.seq_len[b] > A.Lcap) flag_error(A.err, DUSTIN_DEV_SEQLEN);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk w;
-  walk_init(w, A, share[0], int(share[2]), share[1]);
+  walk_init(w, A, *share);
 
   if (warp >= kLoaderWarp0 && warp < kLoaderWarp0 + kLoaders) {
     // =============================================================== loaders

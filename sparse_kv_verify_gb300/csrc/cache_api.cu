@@ -51,6 +51,22 @@ AttendPlan attend_plan(int B, int hq, int hkv, int d, int T, bool prefix) {
   return pl;
 }
 
+// Workspace of an eviction, after the fixed part: rows to move per unit, then
+// their lists.
+struct EvictPlan {
+  int list_cap;
+  size_t moves_off, lists_off, total;
+};
+EvictPlan evict_plan(const dustin_params* p, int hkv, int n_layers) {
+  EvictPlan pl;
+  const size_t units = size_t(n_layers) * p->B * hkv;
+  pl.list_cap = std::max(0, std::min(p->k, p->Lcap - p->k));
+  pl.moves_off = kScratch;
+  pl.lists_off = round256(pl.moves_off + units * 4);
+  pl.total = round256(pl.lists_off + units * 2 * size_t(pl.list_cap) * 4);
+  return pl;
+}
+
 // pk == nullptr: windowed attention.
 int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_kv* pk, const dustin_kv* pv,
                int32_t prefix_cap, const int32_t* prefix_len, const dustin_kv& k, const dustin_kv& v,
@@ -138,7 +154,7 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
     need = attend_plan(p->B, hq, hkv, d, p->gamma + 1, prefix_cap > 0).total;
   }
   if (n_layers != 0) {
-    const size_t e = kScratch + evict_scratch_bytes(p->B, hkv, n_layers, p->k);
+    const size_t e = evict_plan(p, hkv, n_layers).total;
     need = e > need ? e : need;
   }
   return round256(need);
@@ -175,17 +191,18 @@ int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const f
   a.G = hq / k.hkv;
   a.hkv = k.hkv;
   a.scale_log2 = scale_log2_of(k.d);
-  a.q = static_cast<const uint16_t*>(q);
   a.lse = lse;
-  a.k = static_cast<const uint16_t*>(k.ptr);
-  a.ksb = k.sb; a.ksh = k.sh; a.ksl = k.sl;
   a.n_new = n_new;
   a.seq_len = seq_len;
   a.n_seen = n_seen;
   a.weight = weight;
   a.pos = pos;
   a.err = err_word(ws);
-  return accumulate_launch(a, k.d, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+  const int sms = num_sms();
+  if (sms < 1 || !encode_query_map(&a.qmap, q, k.d, hq, p->B * a.T, a.G, a.T) ||
+      !encode_cache_map(&a.kmap, k, p->Lcap, p->B, &a.krank, kAccumulateTile))
+    return DUSTIN_ECUDA;
+  return accumulate_launch(a, k.d, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
 }
 
 int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, const dustin_kv* v,
@@ -227,10 +244,15 @@ int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, c
     L.vsb = v[l].sb; L.vsh = v[l].sh; L.vsl = v[l].sl;
   }
   if (int64_t(p->B) * a.hkv > kVerifyUnitsMax) return DUSTIN_ERANGE;
-  if (!ws_ok(ws, ws_bytes, kScratch + evict_scratch_bytes(p->B, a.hkv, n_layers, p->k))) return DUSTIN_EWORKSPACE;
+  const EvictPlan pl = evict_plan(p, a.hkv, n_layers);
+  if (!ws_ok(ws, ws_bytes, pl.total)) return DUSTIN_EWORKSPACE;
   a.err = err_word(ws);
-  a.lists = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kScratch);
-  return evict_launch(a, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
+  a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + pl.moves_off);
+  a.lists = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + pl.lists_off);
+  a.list_cap = pl.list_cap;
+  const int sms = num_sms();
+  if (sms < 1) return DUSTIN_ECUDA;
+  return evict_launch(a, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
 }
 
 }  // extern "C"

@@ -4,136 +4,298 @@
 // them: those at positions below `sinks` or among the last `window` positions
 // seen, then the largest weights (equal weights: the lower row).  The rows it
 // drops below k, in order, take the rows it keeps at or beyond k, in order --
-// sources and destinations never overlap, and as few rows move as can.
+// sources and destinations never overlap, so the move is in place, needs no
+// order among its rows, and moves as few as can be.
 //
-// One CTA per unit: a radix select over the 32-bit keys finds the threshold
-// and how many rows that equal it stay, one ordered scan lists holes and
-// movers, then the warps copy them.
+// Two launches:
+//   select  one cluster of CTAs per unit.  Every row's 32-bit key (all ones for
+//           a protected row, else the weight's bits, which order like the
+//           weight) is formed once and kept in shared memory; three histogram
+//           passes of 11, 11 and 10 bits, summed over the cluster's CTAs, give
+//           the k-th largest key and how many rows that equal it stay.  With
+//           kept(j) = rows kept before row j, a hole j < k is the
+//           (j - kept(j))-th and a mover j >= k the (kept(j) - kept(k))-th of
+//           its list, so both lists are written from one ordered count of keys
+//           above and equal to the threshold.
+//   move    bound by the bytes of the rows: every warp moves eight rows at a
+//           time, a row's K and V by half a warp each, loads before stores.
+//           It also sets the lengths, which the first launch read.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
+
+namespace cg = cooperative_groups;
 
 namespace dustin {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarpsN = kThreads / 32;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeysMax = 48 * 1024;      // keys that a CTA keeps in shared memory
+constexpr int kMaxCluster = 8;
+constexpr int kSliceMin = 4096;          // rows per CTA below which more CTAs do not help
 
-// exclusive rank of this thread's flag within the block, and the block's count
-__device__ __forceinline__ int block_rank(bool f, int* warp_sum, int* total) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned bal = __ballot_sync(0xffffffffu, f);
-  __syncthreads();
-  if (lane == 0) warp_sum[w] = __popc(bal);
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int x = 0; x < kWarpsN; ++x) {
-    before += x < w ? warp_sum[x] : 0;
-    all += warp_sum[x];
-  }
-  *total = all;
-  return before + __popc(bal & ((1u << lane) - 1u));
-}
+struct Counts {
+  int gt, tie, gt_below, tie_below;      // keys above / at the threshold; of these the rows < k
+};
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs A) {
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs A) {
+  extern __shared__ uint32_t keys[];     // [min(slice, kKeysMax)]
+  __shared__ int hist[kBins];
+  __shared__ int warp_sum[kWarps];
+  __shared__ Counts warp_cnt[kWarps];
+  __shared__ Counts cta_cnt;
+  __shared__ int s_bin, s_need;
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int hist[256];
-  __shared__ int warp_sum[kWarpsN];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int unit = blockIdx.x, l = blockIdx.y;
-  const int b = unit / A.hkv, g = unit % A.hkv;
-  const EvictLayerDev& Ly = A.layer[l];
-  const int n = A.seq_len[b], k = A.k;
-  if (n < 0 || n > A.Lcap) {
-    if (threadIdx.x == 0 && g == 0 && l == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int cs = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int unit = blockIdx.x / cs, l = blockIdx.y;
+  const int b = unit / A.hkv, g = unit % A.hkv, k = A.k;
+  const size_t lu = size_t(l) * A.B * A.hkv + unit;
+  const int n = A.seq_len[b];
+  if (n < 0 || n > A.Lcap || n <= k) {   // the whole cluster leaves
+    if (rank == 0 && tid == 0) {
+      if ((n < 0 || n > A.Lcap) && g == 0 && l == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
+      A.moves[lu] = 0;
+    }
     return;
   }
-  if (n <= k) return;
-  float* weight = Ly.weight + size_t(unit) * A.Lcap;
-  int32_t* pos = Ly.pos + size_t(unit) * A.Lcap;
+  const float* weight = A.layer[l].weight + size_t(unit) * A.Lcap;
+  const int32_t* pos = A.layer[l].pos + size_t(unit) * A.Lcap;
   const int recent = A.n_seen[b] - A.window;
-  auto key_of = [&](int j) -> uint32_t {
-    const int p = pos[j];
-    return p < A.sinks || p >= recent ? 0xFFFFFFFFu : importance_key(weight[j], A.err);
+  // this CTA's rows [j0, j1), a whole number of warps' chunks
+  const int slice = ((n + cs - 1) / cs + 31) & ~31;
+  const int j0 = min(rank * slice, n), j1 = min(j0 + slice, n);
+  const bool cached = slice <= A.keys_cap;
+  auto fresh_key = [&](int j) -> uint32_t {
+    const int p = __ldcg(pos + j);
+    const float w = __ldcg(weight + j);
+    return p < A.sinks || p >= recent ? 0xFFFFFFFFu : importance_key(w, A.err);
   };
-  uint32_t prefix = 0, mask = 0;
-  int need = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int x = threadIdx.x; x < 256; x += kThreads) hist[x] = 0;
+  auto key_of = [&](int j) -> uint32_t { return cached ? keys[j - j0] : fresh_key(j); };
+
+  // the k-th largest key, digit by digit
+  uint32_t high = 0;      // digits so far
+  int need = k;           // rows still to take among the keys that share them
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int x = tid; x < kBins; x += kThreads) hist[x] = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kThreads) {
-      const uint32_t key = key_of(j);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+    for (int jb = j0 + 32 * warp; jb < j1; jb += kThreads) {   // whole warps
+      const int j = jb + lane;
+      uint32_t key = 0;
+      if (j < j1) {
+        key = pass == 0 ? fresh_key(j) : key_of(j);
+        if (pass == 0 && cached) keys[j - j0] = key;
+      }
+      const bool in = j < j1 && (pass == 0 || (key >> (shift + bits)) == high);
+      const int bin = int((key >> shift) & ((1u << bits) - 1u));
+      // rows of one key (a protected run, weights never touched) count as one
+      const unsigned live = __ballot_sync(0xffffffffu, in);
+      if (live) {
+        const int first = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
+        if (__all_sync(0xffffffffu, !in || bin == first)) {
+          if (lane == 0) atomicAdd(&hist[first], __popc(live));
+        } else if (in) {
+          atomicAdd(&hist[bin], 1);
+        }
+      }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int left = need, x = 255;
-      while (x > 0 && hist[x] < left) left -= hist[x--];
-      s_prefix = prefix | (uint32_t(x) << shift);
-      s_need = left;
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+    // from the top: thread t sums bins 2047 - 2 t and 2046 - 2 t over the cluster
+    int h0 = 0, h1 = 0;
+    for (int r = 0; r < cs; ++r) {
+      const int* h = cs > 1 ? cluster.map_shared_rank(hist, r) : hist;
+      h0 += h[kBins - 1 - 2 * tid];
+      h1 += h[kBins - 2 - 2 * tid];
     }
+    int inc = h0 + h1;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    prefix = s_prefix;
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    const int end = before + inc, begin = end - h0 - h1;
+    if (begin < need && need <= end) {
+      const bool top = need <= begin + h0;
+      s_bin = kBins - (top ? 1 : 2) - 2 * tid;
+      s_need = need - begin - (top ? 0 : h0);
+    }
+    if (cs > 1) cluster.sync();   // the other CTAs have read this histogram
+    else __syncthreads();
+    high = (high << bits) | uint32_t(s_bin);
     need = s_need;
-    mask |= 255u << shift;
-    __syncthreads();
   }
-  int32_t* dst = A.lists + (size_t(l) * A.B * A.hkv + unit) * 2 * k;
-  int32_t* src = dst + k;
-  int ties = 0, holes = 0, movers = 0;
-  for (int j0 = 0; j0 < n; j0 += kThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint32_t key = j < n ? key_of(j) : 0u;
-    const bool tie = j < n && key == prefix;
-    int all;
-    const int tr = ties + block_rank(tie, warp_sum, &all);
-    ties += all;
-    const bool keep = j < n && (key > prefix || (tie && tr < need));
-    const bool hole = j < k && !keep, move = j >= k && keep;
-    const int hr = block_rank(hole, warp_sum, &all);
-    if (hole) dst[holes + hr] = j;
-    holes += all;
-    const int mr = block_rank(move, warp_sum, &all);
-    if (move) src[movers + mr] = j;
-    movers += all;
+  const uint32_t thr = high;
+
+  // counts per warp: warp w has the rows [j0 + w * span, ...) of this CTA
+  const int span = ((j1 - j0 + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(j0 + warp * span, j1), w1 = min(w0 + span, j1);
+  Counts c{0, 0, 0, 0};
+  for (int jb = w0; jb < w1; jb += 32) {
+    const int j = jb + lane;
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    const unsigned gt = __ballot_sync(0xffffffffu, j < w1 && key > thr);
+    const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && key == thr);
+    const unsigned below = __ballot_sync(0xffffffffu, j < k);
+    c.gt += __popc(gt);
+    c.tie += __popc(tie);
+    c.gt_below += __popc(gt & below);
+    c.tie_below += __popc(tie & below);
   }
+  if (lane == 0) warp_cnt[warp] = c;
   __syncthreads();
-  const int chunks = A.D / 8;
-  uint16_t* kc = Ly.k + size_t(b) * Ly.ksb + size_t(g) * Ly.ksh;
-  uint16_t* vc = Ly.v + size_t(b) * Ly.vsb + size_t(g) * Ly.vsh;
-  for (int x = threadIdx.x; x < movers * chunks; x += kThreads) {
-    const int r = x / chunks, c = x % chunks;
-    const int to = dst[r], of = src[r];
-    reinterpret_cast<uint4*>(kc + size_t(to) * Ly.ksl)[c] = reinterpret_cast<const uint4*>(kc + size_t(of) * Ly.ksl)[c];
-    reinterpret_cast<uint4*>(vc + size_t(to) * Ly.vsl)[c] = reinterpret_cast<const uint4*>(vc + size_t(of) * Ly.vsl)[c];
-    if (c == 0) {
+  if (warp == 0) {
+    Counts t = warp_cnt[lane];
+    t.gt = __reduce_add_sync(0xffffffffu, t.gt);
+    t.tie = __reduce_add_sync(0xffffffffu, t.tie);
+    t.gt_below = __reduce_add_sync(0xffffffffu, t.gt_below);
+    t.tie_below = __reduce_add_sync(0xffffffffu, t.tie_below);
+    if (lane == 0) cta_cnt = t;
+  }
+  if (cs > 1) cluster.sync();
+  else __syncthreads();
+  int gt = 0, tie = 0, gt_k = 0, tie_k = 0;   // before this warp's rows; before row k
+  for (int r = 0; r < cs; ++r) {
+    const Counts* t = cs > 1 ? cluster.map_shared_rank(&cta_cnt, r) : &cta_cnt;
+    if (r < rank) {
+      gt += t->gt;
+      tie += t->tie;
+    }
+    gt_k += t->gt_below;
+    tie_k += t->tie_below;
+  }
+  for (int w = 0; w < warp; ++w) {
+    gt += warp_cnt[w].gt;
+    tie += warp_cnt[w].tie;
+  }
+  const int kept_k = gt_k + min(tie_k, need);
+  int32_t* dst = A.lists + lu * 2 * A.list_cap;
+  int32_t* src = dst + A.list_cap;
+  if (rank == 0 && tid == 0) A.moves[lu] = k - kept_k;
+  for (int jb = w0; jb < w1; jb += 32) {
+    const int j = jb + lane;
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    const unsigned mgt = __ballot_sync(0xffffffffu, j < w1 && key > thr);
+    const unsigned mtie = __ballot_sync(0xffffffffu, j < w1 && key == thr);
+    const unsigned lt = (1u << lane) - 1u;
+    const int tie_j = tie + __popc(mtie & lt);
+    const int kept = gt + __popc(mgt & lt) + min(tie_j, need);
+    if (j < w1) {
+      const bool keep = key > thr || (key == thr && tie_j < need);
+      if (j < k && !keep) dst[j - kept] = j;
+      if (j >= k && keep) src[kept - kept_k] = j;
+    }
+    gt += __popc(mgt);
+    tie += __popc(mtie);
+  }
+  if (cs > 1) cluster.sync();   // no CTA leaves while its counts are read
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kRows = 8;                 // rows a warp has in flight
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs A) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int CH = D / 8;              // 16-byte chunks per row
+  constexpr int RPW = 16 / CH;           // rows a half-warp covers at once
+  const int unit = blockIdx.y, l = blockIdx.z;
+  if (blockIdx.x == 0 && unit == 0 && l == 0)
+    for (int b = threadIdx.x; b < A.B; b += kMoveThreads) {
+      const int n = A.seq_len[b];
+      if (n > A.k && n <= A.Lcap) A.seq_len[b] = A.k;
+    }
+  const size_t lu = size_t(l) * A.B * A.hkv + unit;
+  const int m = A.moves[lu];
+  const int32_t* dst = A.lists + lu * 2 * A.list_cap;
+  const int32_t* src = dst + A.list_cap;
+  const EvictLayerDev& Ly = A.layer[l];
+  const int b = unit / A.hkv, g = unit % A.hkv;
+  const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & (CH - 1), sub = (lane & 15) / CH;
+  uint16_t* base = half ? Ly.v + size_t(b) * Ly.vsb + size_t(g) * Ly.vsh : Ly.k + size_t(b) * Ly.ksb + size_t(g) * Ly.ksh;
+  const int64_t sl = half ? Ly.vsl : Ly.ksl;
+  uint32_t* weight = reinterpret_cast<uint32_t*>(Ly.weight + size_t(unit) * A.Lcap);
+  int32_t* pos = Ly.pos + size_t(unit) * A.Lcap;
+  constexpr int STEP = kRows * RPW;      // rows of a warp at once
+  const int warps = gridDim.x * (kMoveThreads / 32);
+  for (int r0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * STEP; r0 < m; r0 += warps * STEP) {
+    // lane x holds the x-th pair of rows
+    int to = 0, of = 0;
+    const bool mine = lane < STEP && r0 + lane < m;
+    if (mine) {
+      to = __ldcg(dst + r0 + lane);
+      of = __ldcg(src + r0 + lane);
+    }
+    uint4 v[kRows];
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      const int x = y * RPW + sub;
+      const int row = __shfl_sync(0xffffffffu, of, x);
+      if (r0 + x < m) v[y] = __ldcs(reinterpret_cast<const uint4*>(base + size_t(row) * sl) + c);
+    }
+    if (mine) {
       weight[to] = weight[of];
       pos[to] = pos[of];
     }
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      const int x = y * RPW + sub;
+      const int row = __shfl_sync(0xffffffffu, to, x);
+      if (r0 + x < m) reinterpret_cast<uint4*>(base + size_t(row) * sl)[c] = v[y];
+    }
   }
-}
-
-__global__ void evict_length_kernel(const __grid_constant__ EvictArgs A) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= A.B) return;
-  const int n = A.seq_len[b];
-  if (n > A.k && n <= A.Lcap) A.seq_len[b] = A.k;
 }
 
 }  // namespace
 
-size_t evict_scratch_bytes(int B, int hkv, int n_layers, int k) {
-  return size_t(n_layers) * B * hkv * 2 * size_t(k) * 4;
-}
-
-cudaError_t evict_launch(const EvictArgs& a, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(evict_kernel, dim3(a.B * a.hkv, a.n_layers), dim3(kThreads), 0, stream, a);
+cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream) {
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+  if (attr != cudaSuccess) return attr;
+  const int units = a.B * a.hkv;
+  // CTAs per unit: as many as find an SM each, while a CTA keeps kSliceMin rows
+  int cs = 1;
+  while (cs < kMaxCluster && (long long)units * a.n_layers * cs * 2 <= num_sms && a.Lcap / (cs * 2) >= kSliceMin) cs *= 2;
+  a.keys_cap = std::min(((a.Lcap + cs - 1) / cs + 31) & ~31, kKeysMax);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(units * cs), unsigned(a.n_layers));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = size_t(a.keys_cap) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = unsigned(cs);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(evict_length_kernel, dim3((a.B + 127) / 128), dim3(128), 0, stream, a);
+  // about eight blocks of eight warps per SM over all units, none without rows
+  const int rows = std::min(a.k, a.Lcap - a.k);
+  if (rows < 1) return cudaSuccess;   // a cache of at most k rows never evicts
+  const long long want = std::max(1LL, 8LL * num_sms / ((long long)units * a.n_layers));
+  const int per = kMoveThreads / 32 * kRows * (a.D == 64 ? 2 : 1);
+  const dim3 grid(unsigned(std::min<long long>(want, (rows + per - 1) / per)), unsigned(units), unsigned(a.n_layers));
+  return a.D == 128 ? launch_pdl(evict_move_kernel<128>, grid, dim3(kMoveThreads), 0, stream, a)
+                    : launch_pdl(evict_move_kernel<64>, grid, dim3(kMoveThreads), 0, stream, a);
 }
 
 }  // namespace dustin

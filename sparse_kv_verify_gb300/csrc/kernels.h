@@ -308,26 +308,27 @@ cudaError_t prefix_launch(const AttendArgs& a, int D, cudaStream_t stream);
 
 // -------------------------------------------------------------- accumulate
 
+constexpr int kAccumulateTile = 128;   // cache rows per tile
+
 struct AccumulateArgs {
   int B, Lcap, T, G, hkv;
   float scale_log2;          // log2(e) / sqrt(D)
-  const uint16_t* q;         // [B][T][hkv * G][D]
   const float* lse;          // [B][T][hkv * G]
-  const uint16_t* k;
-  int64_t ksb, ksh, ksl;
   const int32_t* n_new;
   const int32_t* seq_len;
   const int32_t* n_seen;
   float* weight;             // [B][hkv][Lcap]
   int32_t* pos;              // [B][hkv][Lcap]
   int* err;
+  int krank;                 // 2: map over packed rows, 4: (d, Lcap, hkv, B)
+  CUtensorMap qmap, kmap;
 };
 // Whether sequence lengths (rows, new rows, positions seen) are consistent; a
 // sequence that fails is flagged and left as it was.
 __host__ __device__ inline bool accumulate_ok(const AccumulateArgs& a, int L, int n, int seen) {
   return L >= 0 && L <= a.Lcap && n >= 0 && n <= a.T && n <= L && seen >= L;
 }
-cudaError_t accumulate_launch(const AccumulateArgs& a, int D, cudaStream_t stream);
+cudaError_t accumulate_launch(const AccumulateArgs& a, int D, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------- evict
 
@@ -344,11 +345,13 @@ struct EvictArgs {
   const int32_t* n_seen;
   int32_t* seq_len;
   int* err;
-  int32_t* lists;            // [n_layers][B][hkv][2][k]: holes, movers
+  int32_t* moves;            // [n_layers][B][hkv]: rows to move
+  int32_t* lists;            // [n_layers][B][hkv][2][list_cap]: holes, movers
+  int list_cap;              // min(k, Lcap - k), the rows a unit can move
+  int keys_cap;              // set by evict_launch: keys a CTA keeps in shared memory
   EvictLayerDev layer[DUSTIN_MAX_LAYERS];
 };
-size_t evict_scratch_bytes(int B, int hkv, int n_layers, int k);
-cudaError_t evict_launch(const EvictArgs& a, cudaStream_t stream);
+cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------ wait self-test
 cudaError_t wait_selftest_launch(int* err, long long* waited, unsigned long long limit_ns,

@@ -361,6 +361,8 @@ EVICT = [
     ([40, 41], 1, 1, 0, 1, 64, 1),
     ([20000, 9000], 4096, 16, 100, 2, 64, 1),
     ([300] * 40, 200, 2, 30, 4, 64, 16),
+    ([9000 - 7 * b for b in range(10)], 500, 4, 64, 4, 64, 1),   # two CTAs per unit
+    ([410000, 7000], 5000, 16, 100, 1, 64, 1),                   # keys past a CTA's shared memory
 ]
 
 
