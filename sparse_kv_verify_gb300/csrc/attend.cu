@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
 // Log-sum-exp merge of a unit's segments: one thread per four output columns.
 // A segment is (unnormalised O, log2-domain reference maximum m, sum l).
 constexpr int kMergeThreads = 128;
+constexpr int kMergeDepth = 8;
 
 struct Merge {
   float m, l;
@@ -638,47 +639,28 @@ __device__ __forceinline__ void merge_in(Merge& a, float m, float l, const float
   a.o.w = a.o.w * x + o.w * y;
 }
 
-// segments p0, p0 + stride, ... (n of them); m at mo, l at mo + rows
-__device__ __forceinline__ void merge_segments(Merge& a, const float* p, size_t stride, int n, size_t at, size_t mo,
-                                               int rows) {
-  for (int c = 0; c < n; c += 4) {   // four segments' loads in flight at once
-    float m[4], l[4];
-    float4 o[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      m[y] = -INFINITY;
-      l[y] = 0.f;
-      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + y < n) {
-        const float* s = p + size_t(c + y) * stride;
-        m[y] = __ldcg(s + mo);
-        l[y] = __ldcg(s + mo + rows);
-        o[y] = __ldcg(reinterpret_cast<const float4*>(s + at));
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < 4; ++y) merge_in(a, m[y], l[y], o[y]);
-  }
-}
-
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendArgs A) {
   pdl_launch_dependents();
-  pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
   const int unit = blockIdx.y, T = A.T, GQ = A.hq / A.hkv, NQ = T * GQ;
-  const int c0 = A.seg_cta[2 * unit], c1 = A.seg_cta[2 * unit + 1];
-  if (!PREFIX && c0 == c1) return;   // written by its CTA
   const int x = blockIdx.x * kMergeThreads + threadIdx.x;
-  if (x >= NQ * (D / 4)) return;
   const int r = x / (D / 4), c4 = x - r * (D / 4);
   const int b = unit / A.hkv, g = unit % A.hkv;
-  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  merge_segments(a, A.partial + (size_t(unit) + c0) * A.slot_floats, size_t(A.slot_floats), c1 - c0 + 1,
-                 size_t(r) * D + 4 * c4, size_t(NQ) * D + r, NQ);
+  pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
+  const int c0 = __ldcg(A.seg_cta + 2 * unit), c1 = __ldcg(A.seg_cta + 2 * unit + 1);
+  if (!PREFIX && c0 == c1) return;   // written by its CTA
+  if (x >= NQ * (D / 4)) return;
+  // this thread's columns, m and l of own segment 0 and of prefix segment 0
+  const int own = c1 - c0 + 1;
+  const float* po = A.partial + (size_t(unit) + c0) * A.slot_floats;
+  const size_t ov = size_t(r) * D + 4 * c4, om = size_t(NQ) * D + r;
+  constexpr size_t kLane = size_t(kPrefixTile) * (D + 2);
+  const float* pp = nullptr;
+  int row = 0, all = own;
   if constexpr (PREFIX) {
-    // the prefix segments of this row: unit pu's tiles [pu * n, (pu + 1) * n) of
-    // the flattened key tiles, CTA c holding [c * total / ctas, (c + 1) * total / ctas)
-    int P = *A.prefix_len;
+    // prefix unit pu has tiles [pu * n, (pu + 1) * n) of the flattened key
+    // tiles, CTA c holds [c * total / ctas, (c + 1) * total / ctas)
+    int P = __ldcg(A.prefix_len);
     if (P < 0 || P > A.Pcap) P = 0;
     if (P > 0) {
       const int tok = b * T + r / GQ, tile = tok / A.nt, pu = g * A.pairs + (tile >> 1);
@@ -686,11 +668,32 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
       const long long ctas = total < A.pgrid ? total : A.pgrid;
       auto cta_of = [&](long long t) { return int(((t + 1) * ctas + total - 1) / total) - 1; };
       const int p0 = cta_of(pu * n), p1 = cta_of(pu * n + n - 1);
-      constexpr size_t kLane = size_t(kPrefixTile) * (D + 2);
-      const int row = (tok - tile * A.nt) * GQ + r % GQ;
-      merge_segments(a, A.ppartial + ((size_t(pu) + p0) * 2 + (tile & 1)) * kLane, 2 * kLane, p1 - p0 + 1,
-                     size_t(row) * D + 4 * c4, size_t(kPrefixTile) * D + row, kPrefixTile);
+      row = (tok - tile * A.nt) * GQ + r % GQ;
+      pp = A.ppartial + ((size_t(pu) + p0) * 2 + (tile & 1)) * kLane;
+      all += p1 - p0 + 1;
     }
+  }
+  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int c = 0; c < all; c += kMergeDepth) {   // that many segments' loads in flight
+    float m[kMergeDepth], l[kMergeDepth];
+    float4 o[kMergeDepth];
+#pragma unroll
+    for (int y = 0; y < kMergeDepth; ++y) {
+      const int z = c + y;
+      m[y] = -INFINITY;
+      l[y] = 0.f;
+      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (z < all) {
+        const bool mine = !PREFIX || z < own;
+        const float* s = mine ? po + size_t(z) * A.slot_floats : pp + size_t(z - own) * 2 * kLane;
+        const float* ml = s + (mine ? om : size_t(kPrefixTile) * D + row);
+        m[y] = __ldcg(ml);
+        l[y] = __ldcg(ml + (mine ? NQ : kPrefixTile));
+        o[y] = __ldcg(reinterpret_cast<const float4*>(s + (mine ? ov : size_t(row) * D + 4 * c4)));
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kMergeDepth; ++y) merge_in(a, m[y], l[y], o[y]);
   }
   const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
   const float inv = a.l > 0.f ? 1.f / a.l : 0.f;

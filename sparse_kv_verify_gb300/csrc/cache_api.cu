@@ -133,8 +133,8 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
     a.pairs = pl.pairs;
     a.ppartial = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.ppart_off);
     if (!encode_query_map(&a.pqmap, q, k.d, hq, p->B * a.T, hq / k.hkv, pl.nt)) return DUSTIN_ECUDA;
-    a.ptma = encode_cache_map(&a.pkmap, *pk, prefix_cap, 1, &a.pkrank, kPrefixTile) &&
-             encode_cache_map(&a.pvmap, *pv, prefix_cap, 1, &a.pvrank, kPrefixTile);
+    a.ptma = encode_prefix_map(&a.pkmap, *pk, prefix_cap, kPrefixTile) &&
+             encode_prefix_map(&a.pvmap, *pv, prefix_cap, kPrefixTile);
   }
   return attend_launch(a, k.d, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;
 }

@@ -45,7 +45,7 @@ struct Counts {
 };
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs A) {
-  extern __shared__ uint32_t keys[];     // [min(slice, kKeysMax)]
+  extern __shared__ __align__(16) uint32_t keys[];     // [keys_cap]
   __shared__ int hist[kBins];
   __shared__ int warp_sum[kWarps];
   __shared__ Counts warp_cnt[kWarps];
@@ -70,16 +70,35 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const float* weight = A.layer[l].weight + size_t(unit) * A.Lcap;
   const int32_t* pos = A.layer[l].pos + size_t(unit) * A.Lcap;
   const int recent = A.n_seen[b] - A.window;
-  // this CTA's rows [j0, j1), a whole number of warps' chunks
-  const int slice = ((n + cs - 1) / cs + 31) & ~31;
+  // this CTA's rows [j0, j1); a warp takes 128 of them at a time, four
+  // neighbours to a lane
+  const int slice = ((n + cs - 1) / cs + 127) & ~127;
   const int j0 = min(rank * slice, n), j1 = min(j0 + slice, n);
   const bool cached = slice <= A.keys_cap;
-  auto fresh_key = [&](int j) -> uint32_t {
-    const int p = __ldcg(pos + j);
-    const float w = __ldcg(weight + j);
+  auto key_of = [&](int p, float w) -> uint32_t {
     return p < A.sinks || p >= recent ? 0xFFFFFFFFu : importance_key(w, A.err);
   };
-  auto key_of = [&](int j) -> uint32_t { return cached ? keys[j - j0] : fresh_key(j); };
+  // keys of rows j .. j + 3 (j a multiple of 4; 0 for rows at or beyond j1)
+  auto fresh4 = [&](int j) -> uint4 {
+    uint4 key = make_uint4(0, 0, 0, 0);
+    if (A.vec4 && j + 4 <= j1) {
+      const int4 p = __ldcg(reinterpret_cast<const int4*>(pos + j));
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(weight + j));
+      key = make_uint4(key_of(p.x, w.x), key_of(p.y, w.y), key_of(p.z, w.z), key_of(p.w, w.w));
+    } else {
+      if (j < j1) key.x = key_of(__ldcg(pos + j), __ldcg(weight + j));
+      if (j + 1 < j1) key.y = key_of(__ldcg(pos + j + 1), __ldcg(weight + j + 1));
+      if (j + 2 < j1) key.z = key_of(__ldcg(pos + j + 2), __ldcg(weight + j + 2));
+      if (j + 3 < j1) key.w = key_of(__ldcg(pos + j + 3), __ldcg(weight + j + 3));
+    }
+    return key;
+  };
+  auto key4 = [&](int j) -> uint4 { return cached ? *reinterpret_cast<const uint4*>(keys + (j - j0)) : fresh4(j); };
+
+  if (cached) {   // (a thread reads back the keys that it wrote)
+#pragma unroll 4
+    for (int j = j0 + 4 * tid; j < j1; j += 4 * kThreads) *reinterpret_cast<uint4*>(keys + (j - j0)) = fresh4(j);
+  }
 
   // the k-th largest key, digit by digit
   uint32_t high = 0;      // digits so far
@@ -89,24 +108,28 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     for (int x = tid; x < kBins; x += kThreads) hist[x] = 0;
     __syncthreads();
-    for (int jb = j0 + 32 * warp; jb < j1; jb += kThreads) {   // whole warps
-      const int j = jb + lane;
-      uint32_t key = 0;
-      if (j < j1) {
-        key = pass == 0 ? fresh_key(j) : key_of(j);
-        if (pass == 0 && cached) keys[j - j0] = key;
+#pragma unroll 4
+    for (int jb = j0 + 128 * warp; jb < j1; jb += 4 * kThreads) {
+      const int j = jb + 4 * lane;
+      const uint4 q = key4(j);
+      const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+      int bin[4];
+      bool in[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        in[x] = j + x < j1 && (pass == 0 || (key[x] >> (shift + bits)) == high);
+        bin[x] = int((key[x] >> shift) & ((1u << bits) - 1u));
       }
-      const bool in = j < j1 && (pass == 0 || (key >> (shift + bits)) == high);
-      const int bin = int((key >> shift) & ((1u << bits) - 1u));
-      // rows of one key (a protected run, weights never touched) count as one
-      const unsigned live = __ballot_sync(0xffffffffu, in);
-      if (live) {
-        const int first = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
-        if (__all_sync(0xffffffffu, !in || bin == first)) {
-          if (lane == 0) atomicAdd(&hist[first], __popc(live));
-        } else if (in) {
-          atomicAdd(&hist[bin], 1);
-        }
+      // a warp whose rows share a bin (a protected run, weights that were never
+      // touched) counts them at once
+      const bool one = bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3] && in[0] && in[1] && in[2] && in[3];
+      const int first = __shfl_sync(0xffffffffu, bin[0], 0);   // by every lane
+      if (__all_sync(0xffffffffu, one && bin[0] == first)) {
+        if (lane == 0) atomicAdd(&hist[first], 128);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (in[x]) atomicAdd(&hist[bin[x]], 1);
       }
     }
     if (cs > 1) cluster.sync();
@@ -142,20 +165,27 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const uint32_t thr = high;
 
   // counts per warp: warp w has the rows [j0 + w * span, ...) of this CTA
-  const int span = ((j1 - j0 + kWarps - 1) / kWarps + 31) & ~31;
+  const int span = ((j1 - j0 + kWarps - 1) / kWarps + 127) & ~127;
   const int w0 = min(j0 + warp * span, j1), w1 = min(w0 + span, j1);
   Counts c{0, 0, 0, 0};
-  for (int jb = w0; jb < w1; jb += 32) {
-    const int j = jb + lane;
-    const uint32_t key = j < w1 ? key_of(j) : 0u;
-    const unsigned gt = __ballot_sync(0xffffffffu, j < w1 && key > thr);
-    const unsigned tie = __ballot_sync(0xffffffffu, j < w1 && key == thr);
-    const unsigned below = __ballot_sync(0xffffffffu, j < k);
-    c.gt += __popc(gt);
-    c.tie += __popc(tie);
-    c.gt_below += __popc(gt & below);
-    c.tie_below += __popc(tie & below);
+#pragma unroll 2
+  for (int jb = w0; jb < w1; jb += 128) {
+    const int j = jb + 4 * lane;
+    const uint4 q = key4(j);
+    const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int gt = j + x < w1 && key[x] > thr, tie = j + x < w1 && key[x] == thr;
+      c.gt += gt;
+      c.tie += tie;
+      c.gt_below += j + x < k ? gt : 0;
+      c.tie_below += j + x < k ? tie : 0;
+    }
   }
+  c.gt = __reduce_add_sync(0xffffffffu, c.gt);
+  c.tie = __reduce_add_sync(0xffffffffu, c.tie);
+  c.gt_below = __reduce_add_sync(0xffffffffu, c.gt_below);
+  c.tie_below = __reduce_add_sync(0xffffffffu, c.tie_below);
   if (lane == 0) warp_cnt[warp] = c;
   __syncthreads();
   if (warp == 0) {
@@ -186,21 +216,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   int32_t* dst = A.lists + lu * 2 * A.list_cap;
   int32_t* src = dst + A.list_cap;
   if (rank == 0 && tid == 0) A.moves[lu] = k - kept_k;
-  for (int jb = w0; jb < w1; jb += 32) {
-    const int j = jb + lane;
-    const uint32_t key = j < w1 ? key_of(j) : 0u;
-    const unsigned mgt = __ballot_sync(0xffffffffu, j < w1 && key > thr);
-    const unsigned mtie = __ballot_sync(0xffffffffu, j < w1 && key == thr);
-    const unsigned lt = (1u << lane) - 1u;
-    const int tie_j = tie + __popc(mtie & lt);
-    const int kept = gt + __popc(mgt & lt) + min(tie_j, need);
-    if (j < w1) {
-      const bool keep = key > thr || (key == thr && tie_j < need);
-      if (j < k && !keep) dst[j - kept] = j;
-      if (j >= k && keep) src[kept - kept_k] = j;
+#pragma unroll 2
+  for (int jb = w0; jb < w1; jb += 128) {
+    const int j = jb + 4 * lane;
+    const uint4 q = key4(j);
+    const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+    int mine = 0;                       // above in the high, ties in the low half
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      mine += j + x < w1 ? (key[x] > thr ? 1 << 16 : key[x] == thr ? 1 : 0) : 0;
+    int inc = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, x);
+      if (lane >= x) inc += y;
     }
-    gt += __popc(mgt);
-    tie += __popc(mtie);
+    const int ahead = inc - mine, all = __shfl_sync(0xffffffffu, inc, 31);
+    int gt_j = gt + (ahead >> 16), tie_j = tie + (ahead & 0xFFFF);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (j + x >= w1) break;
+      const bool above = key[x] > thr, equal = key[x] == thr;
+      const int kept = gt_j + min(tie_j, need);
+      const bool keep = above || (equal && tie_j < need);
+      if (j + x < k && !keep) dst[j + x - kept] = j + x;
+      if (j + x >= k && keep) src[kept - kept_k] = j + x;
+      gt_j += above;
+      tie_j += equal;
+    }
+    gt += all >> 16;
+    tie += all & 0xFFFF;
   }
   if (cs > 1) cluster.sync();   // no CTA leaves while its counts are read
 }
@@ -271,7 +316,10 @@ cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream) {
   // CTAs per unit: as many as find an SM each, while a CTA keeps kSliceMin rows
   int cs = 1;
   while (cs < kMaxCluster && (long long)units * a.n_layers * cs * 2 <= num_sms && a.Lcap / (cs * 2) >= kSliceMin) cs *= 2;
-  a.keys_cap = std::min(((a.Lcap + cs - 1) / cs + 31) & ~31, kKeysMax);
+  a.keys_cap = std::min(((a.Lcap + cs - 1) / cs + 127) & ~127, kKeysMax);
+  a.vec4 = a.Lcap % 4 == 0;   // a unit's weights and positions start on 16 bytes
+  for (int l = 0; l < a.n_layers; ++l)
+    a.vec4 = a.vec4 && ((reinterpret_cast<uintptr_t>(a.layer[l].weight) | reinterpret_cast<uintptr_t>(a.layer[l].pos)) & 15u) == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(units * cs), unsigned(a.n_layers));
   cfg.blockDim = dim3(kThreads);

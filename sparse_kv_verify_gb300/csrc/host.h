@@ -142,4 +142,20 @@ inline bool encode_query_map(CUtensorMap* m, const void* q, int d, int hq, int B
   return true;
 }
 
+// TMA map over a prefix cache [hkv][cap][d] that brings a whole tile of `rows`
+// rows of one KV head in one load: (64 columns, cap, d / 64, hkv) with box
+// (64, rows, d / 64, 1), so that a tile's 64-column panels follow one another in
+// shared memory, each with the 128-byte swizzle.
+inline bool encode_prefix_map(CUtensorMap* m, const dustin_kv& v, int cap, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, cuuint64_t(cap), cuuint64_t(v.d / 64), cuuint64_t(v.hkv)};
+  cuuint64_t strides[3] = {cuuint64_t(v.sl) * 2, 128, cuuint64_t(v.sh) * 2};
+  cuuint32_t box[4] = {64, cuuint32_t(rows), cuuint32_t(v.d / 64), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dustin

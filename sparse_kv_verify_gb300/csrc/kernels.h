@@ -299,7 +299,7 @@ struct AttendArgs {
   int pgrid;
   int nt, row_tiles, pairs;  // tokens per row tile; row tiles of a KV head; pairs of them
   float* ppartial;           // slots [(hkv * pairs + pgrid)][2][128 * (D + 2)]: O, m [128], l [128]
-  int ptma, pkrank, pvrank;
+  int ptma;                  // the prefix caches have tensor maps
   CUtensorMap qmap, kmap, vmap, pqmap, pkmap, pvmap;
 };
 // The attention kernel, the prefix kernel if there is a prefix, the merge.
@@ -349,6 +349,7 @@ struct EvictArgs {
   int32_t* lists;            // [n_layers][B][hkv][2][list_cap]: holes, movers
   int list_cap;              // min(k, Lcap - k), the rows a unit can move
   int keys_cap;              // set by evict_launch: keys a CTA keeps in shared memory
+  int vec4;                  // set by evict_launch: weights and positions read four at a time
   EvictLayerDev layer[DUSTIN_MAX_LAYERS];
 };
 cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream);

@@ -9,19 +9,32 @@
 // about 280 rows on the two products bound the kernel, not the bytes.
 //
 // Roles (handing over through mbarriers):
-//   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row:
-//                   128 scores in registers, P (bf16) stored over them; the
-//                   reference maximum moves only when a tile passes it by more
+//   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
+//                   step's scores in registers, P (bf16) stored over them; the
+//                   reference maximum moves only when a step passes it by more
 //                   than 2^8, and then the thread rescales its row of O;
-//   warps 8, 9       K and V tiles into a ring of 128-row stages: one thread
-//                   issues tiled TMA loads; the tile that ends the prefix comes
-//                   by cp.async, its rows past the end zero-filled (they may
-//                   hold anything, and 0 * NaN is not 0);
-//   warp 10         one thread issues the MMAs, per key tile i and lane:
-//                   O += P(i) V(i), then S(i + 1) = Q K(i + 1)^T over the S and
-//                   P that the first of the two has read (MMAs of one thread
-//                   run in the order of issue).  While one lane's softmax
-//                   works, the tensor core has the other lane's products.
+//   warp 9          K and V tiles into a ring of 128-row stages, one tiled TMA
+//                   load each;
+//   warp 8          the tile that ends the prefix, by cp.async with its rows past
+//                   the end zero-filled (they may hold anything, and 0 * NaN is
+//                   not 0);
+//   warp 10         one thread issues the MMAs, per step i and lane a batch
+//                   O += P(i) V(i), S(i + NB) = Q K(i + NB)^T over the S and P that
+//                   the first product has read (MMAs of one thread run in the
+//                   order of issue).
+//
+// Two shapes of the pipeline:
+//   two row tiles   steps of 128 keys, one S buffer per lane (NB = 1): while one
+//                   lane's softmax works the tensor core has the other lane's
+//                   products.  Bound by the chain of a lane, products (2 x 512
+//                   cycles) -> S -> softmax (about 1250) -> P; steps of 64 keys
+//                   keep the softmax fed but pay the hand-overs twice and an S
+//                   product that shared memory bounds (48 cycles for 32).
+//   one row tile    (at most 128 query rows in all) the products wait for nobody
+//                   else, so steps of 64 keys with two S buffers (NB = 2): S of
+//                   the next step is there when the softmax comes to it.
+// us at 64/8/128, the whole call, two-tile / one-tile shape: 32 rows over P = 8192
+// 34.2 / 28.3; 768 rows over 32 K 122 / 132; 1280 rows over 64 K 301 / 339.
 //
 // Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
 // [256, 256 + D) and [384, 384 + D).  Every segment (unit x CTA) writes its row
@@ -35,20 +48,21 @@ namespace dustin {
 
 namespace {
 
-constexpr int TK = 128;              // keys per tile
-constexpr int kLoaders = 2;
-constexpr int kLoaderWarp0 = 8, kMmaWarp = 10;
-constexpr int NTH = 384;             // 168 registers a thread (a softmax thread holds a row's 128 scores)
+constexpr int TK = kPrefixTile;      // keys per tile, and query rows per row tile
+constexpr int kGatherWarp = 8, kLoadWarp = 9, kMmaWarp = 10;
+constexpr int NTH = 384;             // 168 registers a thread (a softmax thread holds a row's scores)
 constexpr int kSCol = 0, kOCol = 256;                // lane 1: + 128
 
-template <int D>
+template <int D, int LANES>
 struct Cfg {
-  static constexpr int nst = D == 128 ? 5 : 8;       // K or V tiles in the ring
+  static constexpr int nb = LANES == 2 ? 1 : 2;      // S buffers per lane, and steps per tile
+  static constexpr int step = TK / nb;               // keys per step
+  static constexpr int nst = LANES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 6 : 12);   // K or V tiles in the ring
   static constexpr uint32_t panel = TK * 128;        // 64 columns of a K, V or Q tile
   static constexpr uint32_t stage = (D / 64) * panel;
-  static constexpr uint32_t ring_off = 2 * stage;    // after the two Q tiles
+  static constexpr uint32_t ring_off = LANES * stage;   // after the query tiles
   static constexpr uint32_t bar_off = ring_off + nst * stage;
-  static constexpr uint32_t misc_off = bar_off + (2 * nst + 11) * 8;   // barriers
+  static constexpr uint32_t misc_off = bar_off + (2 * nst + 13) * 8;   // barriers
   static constexpr uint32_t total = misc_off + 16 + 1024;
 };
 
@@ -79,6 +93,24 @@ __device__ __forceinline__ void tc_ld128(uint32_t taddr, uint32_t* r) {
         "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]),
         "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]),
         "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 64 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tc_ld64(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
@@ -124,10 +156,10 @@ __device__ __forceinline__ bool next_seg(Seg& s, long long& t, long long t1, int
   return true;
 }
 
-template <int D>
+template <int D, int LANES>
 __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ AttendArgs A) {
-  using C = Cfg<D>;
-  constexpr int NST = C::nst;
+  using C = Cfg<D, LANES>;
+  constexpr int NST = C::nst, NB = C::nb, SK = C::step;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -135,10 +167,9 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
   uint64_t* empty = full + NST;
   uint64_t* q_full = empty + NST;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;      // [2] S of the lane's next tile is in
-  uint64_t* p_full = s_full + 2;       // [2] P is stored
-  uint64_t* o_full = p_full + 2;       // [2] the segment's last P V is in
-  uint64_t* mma_done = o_full + 2;
+  uint64_t* s_full = q_empty + 1;      // [lane][buffer] a batch is done, S of its step in
+  uint64_t* p_full = s_full + 4;       // [lane][buffer] P is stored over S
+  uint64_t* mma_done = p_full + 4;
   uint64_t* go = mma_done + 1;         // a tile that comes by cp.async has a stage
   uint64_t* gathered = go + 1;         // its rows are in
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
@@ -154,14 +185,13 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < 4; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 32 * n_act);
-      mbar_init(&o_full[x], 1);
     }
     mbar_init(mma_done, 1);
     mbar_init(go, 1);
-    mbar_init(gathered, 32 * kLoaders);
+    mbar_init(gathered, 32);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -192,7 +222,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
   }
   Seg sg;
 
-  if (warp < 8) {
+  if (warp < 4 * LANES) {
     // =============================================================== softmax
     const int ln = warp >> 2;                       // lane (row tile of the pair)
     const int row = tid & 127;
@@ -200,31 +230,42 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
       const float scale = A.scale_log2;
       const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
       const uint32_t s_tmem = lane_base + uint32_t(kSCol + 128 * ln), o_tmem = lane_base + uint32_t(kOCol + 128 * ln);
-      int gi = 0, segs = 0;
+      // batch J of the lane completes phase J / NB of s_full[lane][J % NB].  With j0
+      // batches before the segment, S of its step i comes with batch j0 + i, and
+      // P V of step i is in once batch j0 + i + NB is.
+      auto wait_batch = [&](int J) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u, A.err, abort_flag)));
+      };
+      int j0 = 0;
       bool live = true;
       while (live && next_seg(sg, t, t1, tiles, A)) {
         if (ln == 1 && !sg.two) continue;
         const int tok = (2 * sg.pair + ln) * A.nt + row / G;
         const bool act = row < A.nt * G && tok < A.B * A.T;
+        const int n = NB * sg.n;                    // steps
         float mref = -INFINITY, lsum = 0.f;
-        for (int i = 0; i < sg.n; ++i, ++gi) {
-          const int nv = P - (sg.i0 + i) * TK;      // keys of this tile, if under TK
-          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[ln], uint32_t(gi) & 1u, A.err, abort_flag))) {
+        for (int i = 0; i < n; ++i) {
+          const int nv = P - (NB * sg.i0 + i) * SK;  // keys of this step, if under SK
+          const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
+          if (!wait_batch(j0 + i)) {
             live = false;
             break;
           }
           tc_fence_after();
-          float x[TK];
-          tc_ld128(s_tmem, reinterpret_cast<uint32_t*>(x));
-          if (nv < TK) {
+          float x[SK];
+          if constexpr (SK == 128) tc_ld128(sb, reinterpret_cast<uint32_t*>(x));
+          else tc_ld64(sb, reinterpret_cast<uint32_t*>(x));
+          if (nv < SK) {
 #pragma unroll
-            for (int j = 0; j < TK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
+            for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
           }
           float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int j = 4; j < TK; j += 8)
+          for (int j = 4; j + 8 <= SK; j += 8)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) m4[y] = j + 4 + y < TK ? fmaxf(m4[y], fmaxf(x[j + y], x[j + 4 + y])) : fmaxf(m4[y], x[j + y]);
+            for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], fmaxf(x[j + y], x[j + 4 + y]));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], x[SK - 4 + y]);
           const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           // (a row that is not in use never rescales O; its P and O are never read)
           const float mx = act ? top * scale : -INFINITY;
@@ -235,8 +276,13 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
             lsum *= alpha;
           }
           const float nb = mref == -INFINITY ? 0.f : -mref;
-          // rescale this row of O: S of this tile came after P V of the last one
+          // rescale this row of O once P V of the step before is in
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (NB > 1 && !wait_batch(j0 + i - 1 + NB)) {
+              live = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -248,7 +294,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
           }
           float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < SK / 32; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
@@ -261,16 +307,17 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
               pk[j / 2] = pack_bf16(p0, p1);
               pk[j / 2 + 1] = pack_bf16(p2, p3);
             }
-            tc_st16(s_tmem + uint32_t(16 * h), pk);
+            tc_st16(sb + uint32_t(16 * h), pk);
           }
           tc_wait_st();
           lsum += (l0 + l1) + (l2 + l3);
           tc_fence_before();
-          mbar_arrive(&p_full[ln]);
+          mbar_arrive(&p_full[2 * ln + (j0 + i) % NB]);
         }
         if (!live) break;
         // --------------------------------------------------------- epilogue
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[ln], uint32_t(segs++) & 1u, A.err, abort_flag))) break;
+        if (!wait_batch(j0 + n - 1 + NB)) break;
+        j0 += n + NB;
         tc_fence_after();
         float* part = A.ppartial + ((size_t(sg.u) + blockIdx.x) * 2 + ln) * (size_t(TK) * (D + 2));
 #pragma unroll 1
@@ -292,18 +339,14 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
         tc_fence_before();
       }
     }
-  } else if (warp < kLoaderWarp0 + kLoaders) {
-    // =============================================================== loaders
-    const int lw = warp - kLoaderWarp0;
-    constexpr int CH = D / 8;             // 16-byte chunks per row
-    constexpr int KPI = 32 / CH;          // rows per warp instruction
-    const int c = lane_id % CH, ksub = lane_id / CH;
-    const uint64_t pol = policy_evict_last();   // the other pairs of this head read it again
-    const bool lead = lw == 0 && lane_id == 0;
-    int gi = 0, segs = 0, q_issued = 0, gathers = 0;
-    bool live = true;
-    while (live && next_seg(sg, t, t1, tiles, A)) {
-      if (lead) {
+  } else if (warp == kLoadWarp) {
+    if (lane_id == 0) {
+      // ============================================================== loads
+      const uint64_t pol = policy_evict_last();   // the other pairs of this head read it again
+      int gi = 0, st = 0, segs = 0, gathers = 0;
+      uint32_t ph = 0;                            // of stage st
+      bool live = true;
+      while (live && next_seg(sg, t, t1, tiles, A)) {
         // this segment's query tiles, once the last one's S MMAs have read theirs
         if (segs > 0 && !mbar_wait(q_empty, uint32_t(segs - 1) & 1u, A.err, abort_flag)) break;
         const uint32_t bytes = uint32_t(A.nt * G) * D * 2;
@@ -313,43 +356,63 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
           for (int h = 0; h < D / 64; ++h)
             tma_load_3d(sbase + uint32_t(ln) * C::stage + uint32_t(h) * C::panel, &A.pqmap, h * 64, sg.g * G,
                         (2 * sg.pair + ln) * A.nt, q_full);
-        ++q_issued;
-      }
-      ++segs;
-      for (int i = 0; i < 2 * sg.n; ++i, ++gi) {   // K and V of each tile in turn
-        const int st = gi % NST;
-        const int base = (sg.i0 + (i >> 1)) * TK;
-        const bool is_v = i & 1, whole = base + TK <= P && A.ptma;
-        if (whole && !lead) continue;
-        if (lead && gi >= NST && !mbar_wait(&empty[st], uint32_t(gi / NST - 1) & 1u, A.err, abort_flag)) {
-          live = false;
-          break;
-        }
-        const uint32_t stage = sbase + C::ring_off + uint32_t(st) * C::stage;
-        if (whole) {
-          mbar_arrive_expect_tx(&full[st], C::stage);
-          const CUtensorMap* map = is_v ? &A.pvmap : &A.pkmap;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            const uint32_t dst = stage + uint32_t(h) * C::panel;
-            if ((is_v ? A.pvrank : A.pkrank) == 2) tma_load_2d_u32(dst, map, h * 64, sg.g * A.Pcap + base, &full[st], pol);
-            else tma_load_4d_u32(dst, map, h * 64, base, sg.g, 0, &full[st], pol);
+        ++segs;
+        for (int i = 0; i < 2 * sg.n; ++i) {      // K and V of each tile in turn
+          const int base = (sg.i0 + (i >> 1)) * TK;
+          if (gi >= NST && !mbar_wait(&empty[st], ph ^ 1u, A.err, abort_flag)) {
+            live = false;
+            break;
           }
-          continue;
+          if (base + TK <= P && A.ptma) {
+            mbar_arrive_expect_tx(&full[st], C::stage);
+            tma_load_4d_u32(sbase + C::ring_off + uint32_t(st) * C::stage, i & 1 ? &A.pvmap : &A.pkmap, 0, base, 0, sg.g,
+                            &full[st], pol);
+          } else {   // rows by the gathering warps
+            mbar_arrive(go);
+            if (!mbar_wait(gathered, uint32_t(gathers++) & 1u, A.err, abort_flag)) {
+              live = false;
+              break;
+            }
+            mbar_arrive(&full[st]);
+          }
+          ++gi;
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
-        // rows by every loader thread: the leading one, which alone follows the
-        // ring, lets the others start and waits for them before it goes on
-        if (lead) {
-          mbar_arrive(go);
-        } else if (!mbar_wait(go, uint32_t(gathers) & 1u, A.err, abort_flag)) {
+      }
+      // what is in flight has landed before the CTA may exit: the query tiles
+      // and the latest load of each stage
+      if (segs > 0) mbar_drain(q_full, uint32_t(segs - 1) & 1u, A.err);
+      for (int j = gi > NST ? gi - NST : 0; j < gi; ++j) mbar_drain(&full[j % NST], uint32_t(j / NST) & 1u, A.err);
+    }
+    __syncwarp();
+  } else if (warp == kGatherWarp) {
+    // ============================================================== gathers
+    // the tile that ends the prefix, row by row (or every tile, of caches that
+    // no tensor map describes); the loading thread, which alone follows the
+    // ring, lets these start and waits for them before it goes on
+    constexpr int CH = D / 8;             // 16-byte chunks per row
+    constexpr int KPI = 32 / CH;          // rows per warp instruction
+    const int c = lane_id % CH, ksub = lane_id / CH;
+    int gi = 0, gathers = 0;
+    bool live = true;
+    while (live && next_seg(sg, t, t1, tiles, A)) {
+      for (int i = 0; i < 2 * sg.n; ++i, ++gi) {
+        const int base = (sg.i0 + (i >> 1)) * TK;
+        if (base + TK <= P && A.ptma) continue;
+        if (!mbar_wait(go, uint32_t(gathers++) & 1u, A.err, abort_flag)) {
           live = false;
           break;
         }
+        const bool is_v = i & 1;
+        const uint32_t stage = sbase + C::ring_off + uint32_t(gi % NST) * C::stage;
         const uint16_t* src = is_v ? A.pv + size_t(sg.g) * A.pvsh : A.pk + size_t(sg.g) * A.pksh;
         const int64_t sl = is_v ? A.pvsl : A.pksl;
-#pragma unroll 4
-        for (int m = 0; m < TK / kLoaders / KPI; ++m) {
-          const int key = TK / kLoaders * lw + m * KPI + ksub;
+#pragma unroll 8
+        for (int m = 0; m < TK / KPI; ++m) {
+          const int key = m * KPI + ksub;
           const bool ok = base + key < P;
           cp_async16(stage + uint32_t(c >> 3) * C::panel + swz(key, c & 7), src + size_t(ok ? base + key : 0) * sl + c * 8,
                      ok ? 16u : 0u);
@@ -357,81 +420,78 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
         cp_async_wait_all();
         fence_proxy_async();
         mbar_arrive(gathered);
-        if (lead) {
-          if (!mbar_wait(gathered, uint32_t(gathers) & 1u, A.err, abort_flag)) {
-            live = false;
-            break;
-          }
-          mbar_arrive(&full[st]);
-        }
-        ++gathers;
       }
-    }
-    cp_async_wait_all();
-    // what is in flight has landed before the CTA may exit: the query tiles and
-    // the latest load of each stage
-    if (lead) {
-      if (q_issued > 0) mbar_drain(q_full, uint32_t(q_issued - 1) & 1u, A.err);
-      for (int j = gi > NST ? gi - NST : 0; j < gi; ++j) mbar_drain(&full[j % NST], uint32_t(j / NST) & 1u, A.err);
     }
     __syncwarp();
   } else {
     if (warp == kMmaWarp && lane_id == 0) {
       // ================================================================ MMAs
-      constexpr uint32_t kIdS = tc_idesc(128, TK, 0), kIdPV = tc_idesc(128, D, 1);
-      int gi = 0, segs = 0;            // ring position (K of the current tile), segments
-      uint32_t np[2] = {0, 0};         // tiles of each lane so far
+      constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
+      const uint64_t q_desc = tc_desc(sbase, 16, 1024);
+      const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, 1024), v_desc = tc_desc(sbase + C::ring_off, C::panel, 1024);
+      int st = 0, segs = 0;                 // ring stage to consume next; segments
+      uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
+      int j0 = 0, j1 = 0;                   // batches of each lane
       bool issued = false, live = true;
-      auto wait_full = [&](int x) { return mbar_wait(&full[x % NST], uint32_t(x / NST) & 1u, A.err, abort_flag); };
-      auto s_mma = [&](int ln, int x) {   // S = Q K^T with K in ring position x
-        const uint32_t q = sbase + uint32_t(ln) * C::stage, k = sbase + C::ring_off + uint32_t(x % NST) * C::stage;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = uint32_t(kk >> 2) * C::panel + uint32_t((kk & 3) * 32);
-          tc_mma_ss(tmem + uint32_t(kSCol + 128 * ln), tc_desc(q + off, 16, 1024), tc_desc(k + off, 16, 1024), kIdS, kk > 0);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, A.err, abort_flag); };
+      auto next_stage = [&] {
+        if (++st == NST) {
+          st = 0;
+          ph ^= 1u;
         }
-        tc_commit(&s_full[ln]);
-      };
-      auto pv_mma = [&](int ln, int x, bool acc) {   // O (+)= P V with V in ring position x
-        const uint32_t v = sbase + C::ring_off + uint32_t(x % NST) * C::stage;
-#pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk)
-          tc_mma_ts(tmem + uint32_t(kOCol + 128 * ln), tmem + uint32_t(kSCol + 128 * ln + kk * 8),
-                    tc_desc(v + uint32_t(kk * 2048), C::panel, 1024), kIdPV, (acc || kk > 0) ? 1 : 0);
       };
       while (live && next_seg(sg, t, t1, tiles, A)) {
-        const int lanes = sg.two ? 2 : 1;
-        if (!mbar_wait(q_full, uint32_t(segs++) & 1u, A.err, abort_flag) || !wait_full(gi)) break;
-        issued = true;
-        tc_fence_after();
-        for (int ln = 0; ln < lanes; ++ln) s_mma(ln, gi);
-        tc_commit(&empty[gi % NST]);
-        if (sg.n == 1) tc_commit(q_empty);
-        for (int i = 0; i < sg.n && live; ++i, gi += 2) {
-          const bool more = i + 1 < sg.n;
-          for (int ln = 0; ln < lanes; ++ln) {
-            if (!mbar_wait(&p_full[ln], np[ln]++ & 1u, A.err, abort_flag) || (ln == 0 && !wait_full(gi + 1))) {
-              live = false;
-              break;
+        live = wait(q_full, uint32_t(segs++) & 1u);
+        const int n = NB * sg.n;
+        int sv = 0, sk = 0;                 // stages of V and of K
+        for (int i = -NB; live && i < n; ++i) {
+          const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
+          const bool pv = i >= 0, s = i + NB < n;
+          if (pv && first) {
+            sv = st;
+            live = wait(&full[sv], ph);
+            next_stage();
+          }
+          if (live && s && first) {
+            sk = st;
+            live = wait(&full[sk], ph);
+            next_stage();
+          }
+#pragma unroll
+          for (int ln = 0; ln < LANES; ++ln) {
+            if (!live || (ln == 1 && !sg.two)) break;
+            const int buf = (ln ? j1 : j0) % NB;
+            if (pv) {
+              live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
+              if (!live) break;
+              pp ^= 1u << (2 * ln + buf);
             }
+            issued = true;
             tc_fence_after();
-            pv_mma(ln, gi + 1, i > 0);
-            if (more) {
-              if (ln == 0 && !wait_full(gi + 2)) {
-                live = false;
-                break;
-              }
-              s_mma(ln, gi + 2);
-            } else {
-              tc_commit(&o_full[ln]);
+            const uint32_t sp = tmem + uint32_t(kSCol + 128 * ln + buf * SK);
+            if (pv) {
+              const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+#pragma unroll
+              for (int kk = 0; kk < SK / 16; ++kk)
+                tc_mma_ts(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk * 128), kIdPV,
+                          (i > 0 || kk > 0) ? 1 : 0);
             }
+            if (s) {
+              const uint64_t q = q_desc + uint64_t(ln) * (C::stage >> 4);
+              const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2);
+                tc_mma_ss(sp, q + off, k + off, kIdS, kk > 0);
+              }
+            }
+            tc_commit(&s_full[2 * ln + buf]);
+            ++(ln ? j1 : j0);
           }
           if (!live) break;
-          tc_commit(&empty[(gi + 1) % NST]);
-          if (more) {
-            tc_commit(&empty[(gi + 2) % NST]);
-            if (i + 2 == sg.n) tc_commit(q_empty);   // the query tiles are no longer read
-          }
+          if (pv && last) tc_commit(&empty[sv]);
+          if (s && last) tc_commit(&empty[sk]);
+          if (i + NB + 1 == n) tc_commit(q_empty);   // the query tiles are no longer read
         }
       }
       if (issued) {   // every MMA has completed before tensor memory is freed
@@ -449,21 +509,21 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-template <int D>
-cudaError_t launch_d(const AttendArgs& a, cudaStream_t stream) {
-  auto kern = prefix_kernel<D>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<D>::total));
+template <int D, int LANES>
+cudaError_t launch_t(const AttendArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, LANES>;
+  static_assert(C::total <= 227 * 1024, "shared memory of a CTA");
+  auto kern = prefix_kernel<D, LANES>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::total));
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(kern, dim3(a.pgrid), dim3(NTH), Cfg<D>::total, stream, a);
+  return launch_pdl(kern, dim3(a.pgrid), dim3(NTH), C::total, stream, a);
 }
-
-static_assert(Cfg<128>::total <= 227 * 1024 && Cfg<64>::total <= 227 * 1024, "shared memory of a CTA");
 
 }  // namespace
 
 cudaError_t prefix_launch(const AttendArgs& a, int D, cudaStream_t stream) {
-  return D == 128 ? launch_d<128>(a, stream) : launch_d<64>(a, stream);
+  if (a.row_tiles == 1) return D == 128 ? launch_t<128, 1>(a, stream) : launch_t<64, 1>(a, stream);
+  return D == 128 ? launch_t<128, 2>(a, stream) : launch_t<64, 2>(a, stream);
 }
 
 }  // namespace dustin
