@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     }
     __syncwarp();
   } else {
-    if (warp == kMmaWarp && lane_id == 0) {
+    if (warp == kMmaWarp) {
       // ================================================================ MMAs
       constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
       const uint64_t q_desc = tc_desc(sbase, 16, 1024);
@@ -433,20 +433,26 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
       uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
       int j0 = 0, j1 = 0;                   // batches of each lane
       bool issued = false, live = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, A.err, abort_flag); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+      };
+      // the warp runs together and one elected lane issues; branches go by votes,
+      // so that the compiler too knows the warp as converged
+      auto uni = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };
       auto next_stage = [&] {
         if (++st == NST) {
           st = 0;
           ph ^= 1u;
         }
       };
-      while (live && next_seg(sg, t, t1, tiles, A)) {
+      while (live && uni(next_seg(sg, t, t1, tiles, A))) {
+        const bool two = uni(sg.two);
         live = wait(q_full, uint32_t(segs++) & 1u);
         const int n = NB * sg.n;
         int sv = 0, sk = 0;                 // stages of V and of K
-        for (int i = -NB; live && i < n; ++i) {
+        for (int i = -NB; live && uni(i < n); ++i) {
           const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
-          const bool pv = i >= 0, s = i + NB < n;
+          const bool pv = i >= 0, s = uni(i + NB < n);
           if (pv && first) {
             sv = st;
             live = wait(&full[sv], ph);
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
           }
 #pragma unroll
           for (int ln = 0; ln < LANES; ++ln) {
-            if (!live || (ln == 1 && !sg.two)) break;
+            if (!live || (ln == 1 && !two)) break;
             const int buf = (ln ? j1 : j0) % NB;
             if (pv) {
               live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
               const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
 #pragma unroll
               for (int kk = 0; kk < SK / 16; ++kk)
-                tc_mma_ts(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk * 128), kIdPV,
+                tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk * 128), kIdPV,
                           (i > 0 || kk > 0) ? 1 : 0);
             }
             if (s) {
@@ -482,21 +488,21 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2);
-                tc_mma_ss(sp, q + off, k + off, kIdS, kk > 0);
+                tc_mma_ss_elect(sp, q + off, k + off, kIdS, kk > 0);
               }
             }
-            tc_commit(&s_full[2 * ln + buf]);
+            tc_commit_elect(&s_full[2 * ln + buf]);
             ++(ln ? j1 : j0);
           }
           if (!live) break;
-          if (pv && last) tc_commit(&empty[sv]);
-          if (s && last) tc_commit(&empty[sk]);
-          if (i + NB + 1 == n) tc_commit(q_empty);   // the query tiles are no longer read
+          if (pv && last) tc_commit_elect(&empty[sv]);
+          if (s && last) tc_commit_elect(&empty[sk]);
+          if (uni(i + NB + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
         }
       }
       if (issued) {   // every MMA has completed before tensor memory is freed
-        tc_commit(mma_done);
-        mbar_drain(mma_done, 0, A.err);
+        tc_commit_elect(mma_done);
+        if (lane_id == 0) mbar_drain(mma_done, 0, A.err);
       }
     }
     __syncwarp();
