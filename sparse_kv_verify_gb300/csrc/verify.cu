@@ -284,9 +284,11 @@ __global__ void __launch_bounds__(NTH, CPS) verify_kernel(const __grid_constant_
         L = 0;
       }
       // this segment's query rows -> query buffer s % NQB, once the MMAs of the
-      // segment that used it last are done
+      // segment that used it last are done.  One warp does this for every segment:
+      // a wait by parity is only right for a thread that has seen the phase before
+      // (the last warp, so that the TMA loads of the first one run on).
       const int qb = s % NQB;
-      if (s % kLoaders == lw) {
+      if (lw == kLoaders - 1) {
         bool ok = true;
         if (lane == 0) {
           if (s >= NQB) ok = mbar_wait(&q_empty[qb], uint32_t(s / NQB - 1) & 1u, A.err, abort_flag);
