@@ -213,8 +213,10 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  pdl_launch_dependents();
   pdl_wait();
+  // (only now: the prefix kernel does not wait for this one before it reads its
+  // inputs, so what wrote them has to be over when it starts)
+  pdl_launch_dependents();
   if (warp == 0) {
     const Share sh = share_of(A.B, [&](int b) { return tiles_of(A, b).n * A.hkv; });
     if (lane == 0) *share = sh;
@@ -242,9 +244,11 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
     const uint64_t pol = policy_evict_first();
     for (; w.left > 0 && live; walk_next(w, A), ++s) {
       // this segment's query rows -> query buffer s % NQB, once the MMAs of the
-      // segment that used it last are done
+      // segment that used it last are done.  One warp does this for every segment:
+      // a wait by parity is only right for a thread that has seen the phase before
+      // (the last warp, so that the TMA loads of the first one run on).
       const int qb = s % NQB;
-      if (s % kLoaders == lw) {
+      if (lw == kLoaders - 1) {
         bool ok = true;
         if (lane == 0) {
           if (s >= NQB) ok = mbar_wait(&q_empty[qb], uint32_t(s / NQB - 1) & 1u, A.err, abort_flag);
@@ -647,7 +651,9 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
   const int r = x / (D / 4), c4 = x - r * (D / 4);
   const int b = unit / A.hkv, g = unit % A.hkv;
   pdl_wait();   // before any CTA leaves: this kernel completes after the one before it
-  const int c0 = __ldcg(A.seg_cta + 2 * unit), c1 = __ldcg(A.seg_cta + 2 * unit + 1);
+  // (within the slots whatever they hold: a kernel that gave up may not have set them)
+  const int c0 = min(max(__ldcg(A.seg_cta + 2 * unit), 0), kAttendGridMax - 1);
+  const int c1 = min(max(__ldcg(A.seg_cta + 2 * unit + 1), c0), kAttendGridMax - 1);
   if (!PREFIX && c0 == c1) return;   // written by its CTA
   if (x >= NQ * (D / 4)) return;
   // this thread's columns, m and l of own segment 0 and of prefix segment 0

@@ -62,40 +62,9 @@ struct Cfg {
   static constexpr uint32_t stage = (D / 64) * panel;
   static constexpr uint32_t ring_off = LANES * stage;   // after the query tiles
   static constexpr uint32_t bar_off = ring_off + nst * stage;
-  static constexpr uint32_t misc_off = bar_off + (2 * nst + 13) * 8;   // barriers
+  static constexpr uint32_t misc_off = bar_off + (2 * nst + 17) * 8;   // barriers
   static constexpr uint32_t total = misc_off + 16 + 1024;
 };
-
-// 128 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tc_ld128(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
-      "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
-      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,"
-      "%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,"
-      "%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-        "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-        "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-        "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-        "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-        "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]),
-        "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]),
-        "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]),
-        "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]),
-        "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
-      : "r"(taddr)
-      : "memory");
-}
 
 // 64 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tc_ld64(uint32_t taddr, uint32_t* r) {
@@ -123,6 +92,14 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The 128 rows from `row` on of KV head g of a prefix cache.
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* map, int row, int g, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(g), "r"(smem_u32(bar))
+      : "memory");
+}
 
 // (a, b) * (s, s) + (c, c), and (a, b) + (c, d), as one packed instruction each
 __device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
@@ -167,9 +144,10 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
   uint64_t* empty = full + NST;
   uint64_t* q_full = empty + NST;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;      // [lane][buffer] a batch is done, S of its step in
+  uint64_t* s_full = q_empty + 1;      // [lane][buffer] a batch with an S is done
   uint64_t* p_full = s_full + 4;       // [lane][buffer] P is stored over S
-  uint64_t* mma_done = p_full + 4;
+  uint64_t* o_full = p_full + 4;       // [lane][z] the z-th of a segment's last NB batches, without an S, is done
+  uint64_t* mma_done = o_full + 4;
   uint64_t* go = mma_done + 1;         // a tile that comes by cp.async has a stage
   uint64_t* gathered = go + 1;         // its rows are in
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
@@ -188,6 +166,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     for (int x = 0; x < 4; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 32 * n_act);
+      mbar_init(&o_full[x], 1);
     }
     mbar_init(mma_done, 1);
     mbar_init(go, 1);
@@ -195,8 +174,11 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // This kernel starts on the SMs that the sequences' own part (the launch before
+  // it) leaves; it shares no buffer with that launch, which let this one start
+  // only after its own wait for everything before.  The wait before exit makes
+  // this kernel end after it, for the merge.
   pdl_launch_dependents();
-  pdl_wait();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
                  : "memory");
@@ -207,7 +189,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  int P = *A.prefix_len;
+  int P = __ldcg(A.prefix_len);
   if (P < 0 || P > A.Pcap) {
     if (blockIdx.x == 0 && tid == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
     P = 0;
@@ -230,13 +212,17 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
       const float scale = A.scale_log2;
       const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
       const uint32_t s_tmem = lane_base + uint32_t(kSCol + 128 * ln), o_tmem = lane_base + uint32_t(kOCol + 128 * ln);
-      // batch J of the lane completes phase J / NB of s_full[lane][J % NB].  With j0
-      // batches before the segment, S of its step i comes with batch j0 + i, and
-      // P V of step i is in once batch j0 + i + NB is.
-      auto wait_batch = [&](int J) {
-        return bool(__all_sync(0xffffffffu, mbar_wait(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u, A.err, abort_flag)));
+      // S of the lane's J-th step completes phase J / NB of s_full[lane][J % NB], in
+      // one batch with P V of step J - NB; P V of step n - NB + z of a segment
+      // completes a phase of o_full[lane][z].  Every thread waits for every phase
+      // in turn, and the one after it needs a P that the thread stores later: no
+      // wait by parity can be lapped or pass early.
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
       };
-      int j0 = 0;
+      auto wait_s = [&](int J) { return wait_warp(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u); };
+      int j0 = 0, segs = 0;   // steps and segments of the lane before this segment
+      auto wait_o = [&](int z) { return wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
       bool live = true;
       while (live && next_seg(sg, t, t1, tiles, A)) {
         if (ln == 1 && !sg.two) continue;
@@ -247,14 +233,14 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
         for (int i = 0; i < n; ++i) {
           const int nv = P - (NB * sg.i0 + i) * SK;  // keys of this step, if under SK
           const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
-          if (!wait_batch(j0 + i)) {
+          if (!wait_s(j0 + i)) {
             live = false;
             break;
           }
           tc_fence_after();
           float x[SK];
-          if constexpr (SK == 128) tc_ld128(sb, reinterpret_cast<uint32_t*>(x));
-          else tc_ld64(sb, reinterpret_cast<uint32_t*>(x));
+#pragma unroll
+          for (int c = 0; c < SK; c += 64) tc_ld64(sb + uint32_t(c), reinterpret_cast<uint32_t*>(x + c));
           if (nv < SK) {
 #pragma unroll
             for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
@@ -276,9 +262,11 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
             lsum *= alpha;
           }
           const float nb = mref == -INFINITY ? 0.f : -mref;
-          // rescale this row of O once P V of the step before is in
+          // rescale this row of O once P V of the step before is in (NB = 1: it
+          // came with S of this step; NB = 2: it comes with S of the next one, or
+          // alone after the last)
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            if (NB > 1 && !wait_batch(j0 + i - 1 + NB)) {
+            if (NB > 1 && !(i + 1 < n ? wait_s(j0 + i + 1) : wait_o(0))) {
               live = false;
               break;
             }
@@ -316,8 +304,11 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
         }
         if (!live) break;
         // --------------------------------------------------------- epilogue
-        if (!wait_batch(j0 + n - 1 + NB)) break;
-        j0 += n + NB;
+#pragma unroll
+        for (int z = 0; z < NB; ++z) live = live && wait_o(z);
+        if (!live) break;
+        j0 += n;
+        ++segs;
         tc_fence_after();
         float* part = A.ppartial + ((size_t(sg.u) + blockIdx.x) * 2 + ln) * (size_t(TK) * (D + 2));
 #pragma unroll 1
@@ -342,7 +333,6 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
   } else if (warp == kLoadWarp) {
     if (lane_id == 0) {
       // ============================================================== loads
-      const uint64_t pol = policy_evict_last();   // the other pairs of this head read it again
       int gi = 0, st = 0, segs = 0, gathers = 0;
       uint32_t ph = 0;                            // of stage st
       bool live = true;
@@ -365,8 +355,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
           }
           if (base + TK <= P && A.ptma) {
             mbar_arrive_expect_tx(&full[st], C::stage);
-            tma_load_4d_u32(sbase + C::ring_off + uint32_t(st) * C::stage, i & 1 ? &A.pvmap : &A.pkmap, 0, base, 0, sg.g,
-                            &full[st], pol);
+            tma_load_tile(sbase + C::ring_off + uint32_t(st) * C::stage, i & 1 ? &A.pvmap : &A.pkmap, base, sg.g, &full[st]);
           } else {   // rows by the gathering warps
             mbar_arrive(go);
             if (!mbar_wait(gathered, uint32_t(gathers++) & 1u, A.err, abort_flag)) {
@@ -431,7 +420,6 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
       const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, 1024), v_desc = tc_desc(sbase + C::ring_off, C::panel, 1024);
       int st = 0, segs = 0;                 // ring stage to consume next; segments
       uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
-      int j0 = 0, j1 = 0;                   // batches of each lane
       bool issued = false, live = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
@@ -466,7 +454,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
 #pragma unroll
           for (int ln = 0; ln < LANES; ++ln) {
             if (!live || (ln == 1 && !two)) break;
-            const int buf = (ln ? j1 : j0) % NB;
+            const int buf = NB == 1 ? 0 : i & 1;   // of step i and of step i + NB
             if (pv) {
               live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
               if (!live) break;
@@ -491,8 +479,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
                 tc_mma_ss_elect(sp, q + off, k + off, kIdS, kk > 0);
               }
             }
-            tc_commit_elect(&s_full[2 * ln + buf]);
-            ++(ln ? j1 : j0);
+            tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
           }
           if (!live) break;
           if (pv && last) tc_commit_elect(&empty[sv]);
@@ -508,6 +495,7 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
     __syncwarp();
   }
 
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -86,6 +86,18 @@ def test_window_many_sequences_and_extreme_scores():
     check_window(x, 2, 150)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_many_short_units_per_cta(d):
+    """Units of one to three tiles, ten of them to a CTA: the query buffer is
+    handed from unit to unit faster than the ring of tiles goes round."""
+    rng = np.random.default_rng(d)
+    x = Block(rng.integers(0, 130, 260).tolist(), 2, 8, 8, d, seed=d)
+    for _ in range(3):
+        check_window(x, 1, 60)
+    pk, pv = prefix_of(40, 8, d)
+    check_prefix(x, pk, pv, 40)
+
+
 @pytest.mark.parametrize("layout", ["padded", "token_major"])
 def test_window_strided_caches(layout):
     x = Block([300, 97, 64], 4, 8, 2, 128, seed=5)
