@@ -11,7 +11,7 @@
 //   select  one cluster of CTAs per unit.  Every row's 32-bit key (all ones for
 //           a protected row, else the weight's bits, which order like the
 //           weight) is formed once and kept in shared memory; three histogram
-//           passes of 11, 11 and 10 bits, summed over the cluster's CTAs, give
+//           passes of 12, 10 and 10 bits, summed over the cluster's CTAs, give
 //           the k-th largest key and how many rows that equal it stay.  With
 //           kept(j) = rows kept before row j, a hole j < k is the
 //           (j - kept(j))-th and a mover j >= k the (kept(j) - kept(k))-th of
@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 4096;            // of the first histogram pass; the others use 1024
 constexpr int kKeysMax = 48 * 1024;      // keys that a CTA keeps in shared memory
 constexpr int kMaxCluster = 8;
 constexpr int kSliceMin = 4096;          // rows per CTA below which more CTAs do not help
@@ -44,6 +44,28 @@ struct Counts {
   int gt, tie, gt_below, tie_below;      // keys above / at the threshold; of these the rows < k
 };
 
+struct Rule {                            // what a row's key depends on
+  const float* weight;
+  const int32_t* pos;
+  int sinks, recent, last;               // last: the unit's last row
+  int* err;
+};
+__device__ __forceinline__ uint32_t key_of(const Rule& R, int p, float w) {
+  return p < R.sinks || p >= R.recent ? 0xFFFFFFFFu : importance_key(w, R.err);
+}
+// The keys of rows j .. j + 3; rows past the last one repeat it.
+__device__ __noinline__ uint4 keys_by_row(const Rule& R, int j) {
+  uint32_t key[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int y = min(j + x, R.last);
+    key[x] = key_of(R, __ldcg(R.pos + y), __ldcg(R.weight + y));
+  }
+  return make_uint4(key[0], key[1], key[2], key[3]);
+}
+
+// (One launch runs this code once, so its loops are kept short: at n = 2054 the
+// instruction fetches of unrolled passes took longer than their work.)
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs A) {
   extern __shared__ __align__(16) uint32_t keys[];     // [keys_cap]
   __shared__ int hist[kBins];
@@ -55,11 +77,15 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   pdl_wait();
   const cg::cluster_group cluster = cg::this_cluster();
   const int cs = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  auto sync_all = [&] {
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+  };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int unit = blockIdx.x / cs, l = blockIdx.y;
   const int b = unit / A.hkv, g = unit % A.hkv, k = A.k;
   const size_t lu = size_t(l) * A.B * A.hkv + unit;
-  const int n = A.seq_len[b];
+  const int n = A.seq_len[b], seen = A.n_seen[b];
   if (n < 0 || n > A.Lcap || n <= k) {   // the whole cluster leaves
     if (rank == 0 && tid == 0) {
       if ((n < 0 || n > A.Lcap) && g == 0 && l == 0) flag_error(A.err, DUSTIN_DEV_SEQLEN);
@@ -67,81 +93,94 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     }
     return;
   }
-  const float* weight = A.layer[l].weight + size_t(unit) * A.Lcap;
-  const int32_t* pos = A.layer[l].pos + size_t(unit) * A.Lcap;
-  const int recent = A.n_seen[b] - A.window;
+  const Rule R{A.layer[l].weight + size_t(unit) * A.Lcap, A.layer[l].pos + size_t(unit) * A.Lcap, A.sinks,
+               seen - A.window, n - 1, A.err};
   // this CTA's rows [j0, j1); a warp takes 128 of them at a time, four
   // neighbours to a lane
   const int slice = ((n + cs - 1) / cs + 127) & ~127;
   const int j0 = min(rank * slice, n), j1 = min(j0 + slice, n);
   const bool cached = slice <= A.keys_cap;
-  auto key_of = [&](int p, float w) -> uint32_t {
-    return p < A.sinks || p >= recent ? 0xFFFFFFFFu : importance_key(w, A.err);
-  };
-  // keys of rows j .. j + 3 (j a multiple of 4; 0 for rows at or beyond j1)
-  auto fresh4 = [&](int j) -> uint4 {
-    uint4 key = make_uint4(0, 0, 0, 0);
-    if (A.vec4 && j + 4 <= j1) {
-      const int4 p = __ldcg(reinterpret_cast<const int4*>(pos + j));
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(weight + j));
-      key = make_uint4(key_of(p.x, w.x), key_of(p.y, w.y), key_of(p.z, w.z), key_of(p.w, w.w));
-    } else {
-      if (j < j1) key.x = key_of(__ldcg(pos + j), __ldcg(weight + j));
-      if (j + 1 < j1) key.y = key_of(__ldcg(pos + j + 1), __ldcg(weight + j + 1));
-      if (j + 2 < j1) key.z = key_of(__ldcg(pos + j + 2), __ldcg(weight + j + 2));
-      if (j + 3 < j1) key.w = key_of(__ldcg(pos + j + 3), __ldcg(weight + j + 3));
-    }
-    return key;
-  };
-  auto key4 = [&](int j) -> uint4 { return cached ? *reinterpret_cast<const uint4*>(keys + (j - j0)) : fresh4(j); };
-
-  if (cached) {   // (a thread reads back the keys that it wrote)
+  if (cached) {
+    if (A.vec4) {   // (a unit's rows are a multiple of four, so none lies outside)
 #pragma unroll 4
-    for (int j = j0 + 4 * tid; j < j1; j += 4 * kThreads) *reinterpret_cast<uint4*>(keys + (j - j0)) = fresh4(j);
+      for (int j = j0 + 4 * tid; j < j1; j += 4 * kThreads) {
+        const int4 p = __ldcg(reinterpret_cast<const int4*>(R.pos + j));
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(R.weight + j));
+        uint4 key;
+        key.x = key_of(R, p.x, w.x);
+        key.y = j + 1 < j1 ? key_of(R, p.y, w.y) : 0u;   // rows past the last hold anything
+        key.z = j + 2 < j1 ? key_of(R, p.z, w.z) : 0u;
+        key.w = j + 3 < j1 ? key_of(R, p.w, w.w) : 0u;
+        *reinterpret_cast<uint4*>(keys + (j - j0)) = key;
+      }
+    } else {
+#pragma unroll 1
+      for (int j = j0 + 4 * tid; j < j1; j += 4 * kThreads) *reinterpret_cast<uint4*>(keys + (j - j0)) = keys_by_row(R, j);
+    }
   }
+  auto key4 = [&](int j, uint32_t* key) {
+    const uint4 q = cached ? *reinterpret_cast<const uint4*>(keys + (j - j0)) : keys_by_row(R, j);
+    key[0] = q.x;
+    key[1] = q.y;
+    key[2] = q.z;
+    key[3] = q.w;
+  };
 
   // the k-th largest key, digit by digit
   uint32_t high = 0;      // digits so far
   int need = k;           // rows still to take among the keys that share them
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    for (int x = tid; x < kBins; x += kThreads) hist[x] = 0;
+    const int shift = 20 - 10 * pass, bits = pass == 0 ? 12 : 10;
+    constexpr int kPer = kBins / kThreads;              // bins of a thread
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) hist[tid + x * kThreads] = 0;
     __syncthreads();
-#pragma unroll 4
+#pragma unroll 1
     for (int jb = j0 + 128 * warp; jb < j1; jb += 4 * kThreads) {
       const int j = jb + 4 * lane;
-      const uint4 q = key4(j);
-      const uint32_t key[4] = {q.x, q.y, q.z, q.w};
-      int bin[4];
-      bool in[4];
+      uint32_t key[4];
+      key4(j, key);
+      int live = 0;                      // rows that share the digits so far
+#pragma unroll
+      for (int x = 0; x < 4; ++x) live |= (j + x < j1 && (pass == 0 || (key[x] >> (shift + bits)) == high)) << x;
+      if (!__any_sync(0xffffffffu, live)) continue;
+      // a warp whose rows share a bin (a protected run, weights that were never
+      // touched) counts them at once, and the zeros of any warp go together:
+      // atomics on one bin run one after another
+      const uint32_t first = __shfl_sync(0xffffffffu, key[0] >> shift, 0);
+      const bool same = live == 15 && (key[0] >> shift) == first && (key[1] >> shift) == first &&
+                        (key[2] >> shift) == first && (key[3] >> shift) == first;
+      const int mask = (1 << bits) - 1;
+      if (__all_sync(0xffffffffu, same)) {
+        if (lane == 0) atomicAdd(&hist[first & mask], 128);
+        continue;
+      }
+      int zeros = 0;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        in[x] = j + x < j1 && (pass == 0 || (key[x] >> (shift + bits)) == high);
-        bin[x] = int((key[x] >> shift) & ((1u << bits) - 1u));
+        const int bin = int(key[x] >> shift) & mask;
+        const bool in = (live >> x) & 1;
+        zeros += in && bin == 0;
+        if (in && bin != 0) atomicAdd(&hist[bin], 1);
       }
-      // a warp whose rows share a bin (a protected run, weights that were never
-      // touched) counts them at once
-      const bool one = bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3] && in[0] && in[1] && in[2] && in[3];
-      const int first = __shfl_sync(0xffffffffu, bin[0], 0);   // by every lane
-      if (__all_sync(0xffffffffu, one && bin[0] == first)) {
-        if (lane == 0) atomicAdd(&hist[first], 128);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (in[x]) atomicAdd(&hist[bin[x]], 1);
-      }
+      zeros = __reduce_add_sync(0xffffffffu, zeros);
+      if (lane == 0 && zeros) atomicAdd(&hist[0], zeros);
     }
-    if (cs > 1) cluster.sync();
-    else __syncthreads();
-    // from the top: thread t sums bins 2047 - 2 t and 2046 - 2 t over the cluster
-    int h0 = 0, h1 = 0;
+    sync_all();
+    // from the top: thread t sums bins top - 4 t .. over the cluster
+    const int top = kBins - 1 - kPer * tid;
+    int h[kPer] = {};
+#pragma unroll 1
     for (int r = 0; r < cs; ++r) {
-      const int* h = cs > 1 ? cluster.map_shared_rank(hist, r) : hist;
-      h0 += h[kBins - 1 - 2 * tid];
-      h1 += h[kBins - 2 - 2 * tid];
+      const int4 v = *reinterpret_cast<const int4*>((cs > 1 ? cluster.map_shared_rank(hist, r) : hist) + top - 3);
+      h[0] += v.w;
+      h[1] += v.z;
+      h[2] += v.y;
+      h[3] += v.x;
     }
-    int inc = h0 + h1;
+    const int sum = (h[0] + h[1]) + (h[2] + h[3]);
+    int inc = sum;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, x);
@@ -149,16 +188,20 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    const int end = before + inc, begin = end - h0 - h1;
-    if (begin < need && need <= end) {
-      const bool top = need <= begin + h0;
-      s_bin = kBins - (top ? 1 : 2) - 2 * tid;
-      s_need = need - begin - (top ? 0 : h0);
+    int begin = int(__reduce_add_sync(0xffffffffu, unsigned(lane < warp ? warp_sum[lane] : 0))) + inc - sum;
+    if (begin < need && need <= begin + sum) {
+      // the bin that holds the need-th row from the top
+      int x = 0;
+#pragma unroll
+      for (int y = 0; y < kPer - 1; ++y)
+        if (x == y && begin + h[y] < need) {
+          begin += h[y];
+          ++x;
+        }
+      s_bin = top - x;
+      s_need = need - begin;
     }
-    if (cs > 1) cluster.sync();   // the other CTAs have read this histogram
-    else __syncthreads();
+    sync_all();   // (the other CTAs have read this histogram)
     high = (high << bits) | uint32_t(s_bin);
     need = s_need;
   }
@@ -168,11 +211,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const int span = ((j1 - j0 + kWarps - 1) / kWarps + 127) & ~127;
   const int w0 = min(j0 + warp * span, j1), w1 = min(w0 + span, j1);
   Counts c{0, 0, 0, 0};
-#pragma unroll 2
+#pragma unroll 1
   for (int jb = w0; jb < w1; jb += 128) {
     const int j = jb + 4 * lane;
-    const uint4 q = key4(j);
-    const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+    uint32_t key[4];
+    key4(j, key);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int gt = j + x < w1 && key[x] > thr, tie = j + x < w1 && key[x] == thr;
@@ -196,9 +239,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     t.tie_below = __reduce_add_sync(0xffffffffu, t.tie_below);
     if (lane == 0) cta_cnt = t;
   }
-  if (cs > 1) cluster.sync();
-  else __syncthreads();
+  sync_all();
   int gt = 0, tie = 0, gt_k = 0, tie_k = 0;   // before this warp's rows; before row k
+#pragma unroll 1
   for (int r = 0; r < cs; ++r) {
     const Counts* t = cs > 1 ? cluster.map_shared_rank(&cta_cnt, r) : &cta_cnt;
     if (r < rank) {
@@ -208,44 +251,50 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     gt_k += t->gt_below;
     tie_k += t->tie_below;
   }
-  for (int w = 0; w < warp; ++w) {
-    gt += warp_cnt[w].gt;
-    tie += warp_cnt[w].tie;
-  }
+  gt += int(__reduce_add_sync(0xffffffffu, unsigned(lane < warp ? warp_cnt[lane].gt : 0)));
+  tie += int(__reduce_add_sync(0xffffffffu, unsigned(lane < warp ? warp_cnt[lane].tie : 0)));
   const int kept_k = gt_k + min(tie_k, need);
   int32_t* dst = A.lists + lu * 2 * A.list_cap;
   int32_t* src = dst + A.list_cap;
   if (rank == 0 && tid == 0) A.moves[lu] = k - kept_k;
-#pragma unroll 2
+  const unsigned lt = (1u << lane) - 1u;
+#pragma unroll 1
   for (int jb = w0; jb < w1; jb += 128) {
     const int j = jb + 4 * lane;
-    const uint4 q = key4(j);
-    const uint32_t key[4] = {q.x, q.y, q.z, q.w};
-    int mine = 0;                       // above in the high, ties in the low half
+    uint32_t key[4];
+    key4(j, key);
+    // rows above and at the threshold before this lane's, in the warp
+    int above = 0, ties = 0, gt_j = gt, tie_j = tie;
+    bool some = false;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      mine += j + x < w1 ? (key[x] > thr ? 1 << 16 : key[x] == thr ? 1 : 0) : 0;
-    int inc = mine;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, x);
-      if (lane >= x) inc += y;
+    for (int x = 0; x < 4; ++x) {
+      const bool in = j + x < w1, eq = in && key[x] == thr;
+      const unsigned m = __ballot_sync(0xffffffffu, in && key[x] > thr);
+      above += __popc(m);
+      gt_j += __popc(m & lt);
+      some |= eq;
     }
-    const int ahead = inc - mine, all = __shfl_sync(0xffffffffu, inc, 31);
-    int gt_j = gt + (ahead >> 16), tie_j = tie + (ahead & 0xFFFF);
+    if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const unsigned m = __ballot_sync(0xffffffffu, j + x < w1 && key[x] == thr);
+        ties += __popc(m);
+        tie_j += __popc(m & lt);
+      }
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       if (j + x >= w1) break;
-      const bool above = key[x] > thr, equal = key[x] == thr;
+      const bool over = key[x] > thr, equal = key[x] == thr;
       const int kept = gt_j + min(tie_j, need);
-      const bool keep = above || (equal && tie_j < need);
+      const bool keep = over || (equal && tie_j < need);
       if (j + x < k && !keep) dst[j + x - kept] = j + x;
       if (j + x >= k && keep) src[kept - kept_k] = j + x;
-      gt_j += above;
+      gt_j += over;
       tie_j += equal;
     }
-    gt += all >> 16;
-    tie += all & 0xFFFF;
+    gt += above;
+    tie += ties;
   }
   if (cs > 1) cluster.sync();   // no CTA leaves while its counts are read
 }
