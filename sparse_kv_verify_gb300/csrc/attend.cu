@@ -30,11 +30,15 @@
 //                when a tile passes it by more than 2^8 (O is rarely rescaled).
 //                P is rounded to bf16 for the second MMA; the row sum adds the
 //                unrounded fp32 values, so lse keeps fp32 accuracy.
+// Where units are short or many (whole_units below) CTAs take whole units
+// instead, and nothing needs merging.
 //
 // A segment that covers a whole unit writes o and lse; otherwise its row
 // maxima, sums and unnormalised O go to slot unit + cta of the workspace (both
 // indices only grow along the flattened tiles, so no two segments share one),
 // and a second kernel merges them.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "share.cuh"
@@ -116,7 +120,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttendArgs& A, int b) {
 
 // Walks this CTA's segments: tiles [ta, ta + n) of unit (b, g).
 struct Walk {
-  long long left;     // tiles this CTA still has
+  long long left;     // tiles (A.whole: units) this CTA still has
   int b, g, ta, n;
   Tiles s;
 };
@@ -125,13 +129,19 @@ __device__ __forceinline__ void walk_init(Walk& w, const AttendArgs& A, const Sh
   w.b = sh.b;
   if (w.left > 0) {
     w.s = tiles_of(A, w.b);
+    if (A.whole) {
+      w.g = int(sh.offset);
+      w.ta = 0;
+      w.n = w.s.n;
+      return;
+    }
     w.g = int(sh.offset / w.s.n);
     w.ta = int(sh.offset - (long long)w.g * w.s.n);
     w.n = int(w.left < w.s.n - w.ta ? w.left : w.s.n - w.ta);
   }
 }
 __device__ __forceinline__ void walk_next(Walk& w, const AttendArgs& A) {
-  w.left -= w.n;
+  w.left -= A.whole ? 1 : w.n;
   if (w.left <= 0) return;
   if (++w.g == A.hkv) {
     w.g = 0;
@@ -139,7 +149,7 @@ __device__ __forceinline__ void walk_next(Walk& w, const AttendArgs& A) {
     w.s = tiles_of(A, w.b);
   }
   w.ta = 0;
-  w.n = int(w.left < w.s.n ? w.left : w.s.n);
+  w.n = A.whole || w.left > w.s.n ? w.s.n : int(w.left);
 }
 
 // First key position and number of rows of tile tt.
@@ -218,7 +228,15 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
   // inputs, so what wrote them has to be over when it starts)
   pdl_launch_dependents();
   if (warp == 0) {
-    const Share sh = share_of(A.B, [&](int b) { return tiles_of(A, b).n * A.hkv; });
+    Share sh;
+    if (A.whole) {   // units [c U / G, (c + 1) U / G), first one (b, offset)
+      const long long units = (long long)A.B * A.hkv, u0 = blockIdx.x * units / gridDim.x;
+      sh.count = (blockIdx.x + 1) * units / gridDim.x - u0;
+      sh.b = int(u0 / A.hkv);
+      sh.offset = u0 - (long long)sh.b * A.hkv;
+    } else {
+      sh = share_of(A.B, [&](int b) { return tiles_of(A, b).n * A.hkv; });
+    }
     if (lane == 0) *share = sh;
     if (blockIdx.x == 0)
       for (int b = lane; b < A.B; b += 32)
@@ -722,19 +740,34 @@ cudaError_t launch_attend(const AttendArgs& a, int grid, size_t smem, cudaStream
   return launch_pdl(kern, dim3(grid), dim3(NTH), smem, stream, a);
 }
 
+// Whole units per CTA or tiles split evenly: whole units save the merge and the
+// partials' traffic, worth about 4 tiles of a CTA's time for a few units and 11
+// from a hundred on, and cost the tiles that the busiest CTA has beyond its
+// share.  us whole / split, T = 1 or 5, 64/8/128, by units and window (tiles):
+//     8 units   128 (4) 7.8 /  7.9, 448 (9) 11.2 /  8.9
+//    32         448 (9) 12.1 / 12.3, 1024 (18) 18.6 / 13.4
+//   128         128 (4) 9.2 / 15.7, 1024 (18) 20.2 / 22.0, 2048 (34) 33.3 / 31.4
+//   512         128 (4) 18.5 / 30.2, 2048 (34) 88.6 / 93.3
+bool whole_units(long long units, int tiles, long long ctas) {
+  const long long busiest = (units + ctas - 1) / ctas * tiles;
+  const long long share = std::max(1LL, units * tiles / ctas);
+  return busiest - share <= std::min(11LL, 4 + units / 16);
+}
+
 template <int D>
-cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_d(AttendArgs& a, int num_sms, cudaStream_t stream) {
   const int NQ = a.T * (a.hq / a.hkv);
   // 64-row MMAs while the query rows fit, two CTAs per SM while two fit
   const bool two = NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
-  long long most = (long long)a.B * a.hkv * a.max_tiles;
-  int grid = (two ? 2 : 1) * num_sms;
-  if (grid > kAttendGridMax) grid = kAttendGridMax;
-  if (grid > most) grid = int(most);
+  const long long units = (long long)a.B * a.hkv;
+  const int ctas = std::min((two ? 2 : 1) * num_sms, kAttendGridMax);
+  a.whole = a.pgrid == 0 && whole_units(units, a.max_tiles, ctas);
+  const int grid = int(std::min<long long>(ctas, units * (a.whole ? 1 : a.max_tiles)));
   cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
                   : NQ <= 64 ? launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream)
                              : launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
-  if (e == cudaSuccess && a.pgrid) e = prefix_launch(a, D, stream);
+  if (e != cudaSuccess || a.whole) return e;
+  if (a.pgrid) e = prefix_launch(a, D, stream);
   if (e != cudaSuccess) return e;
   const dim3 mgrid((NQ * (D / 4) + kMergeThreads - 1) / kMergeThreads, unsigned(a.B * a.hkv));
   return a.pgrid ? launch_pdl(attend_merge_kernel<D, true>, mgrid, dim3(kMergeThreads), 0, stream, a)
@@ -743,7 +776,7 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t attend_launch(const AttendArgs& a, int D, int num_sms, cudaStream_t stream) {
+cudaError_t attend_launch(AttendArgs& a, int D, int num_sms, cudaStream_t stream) {
   return D == 128 ? launch_d<128>(a, num_sms, stream) : launch_d<64>(a, num_sms, stream);
 }
 

@@ -17,7 +17,7 @@
 //           (j - kept(j))-th and a mover j >= k the (kept(j) - kept(k))-th of
 //           its list, so both lists are written from one ordered count of keys
 //           above and equal to the threshold.
-//   move    bound by the bytes of the rows: every warp moves eight rows at a
+//   move    bound by the bytes of the rows: every warp moves four rows at a
 //           time, a row's K and V by half a warp each, loads before stores.
 //           It also sets the lengths, which the first launch read.
 #include <algorithm>
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kRows = 8;                 // rows a warp has in flight
+constexpr int kRows = 4;                 // rows a warp has in flight
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs A) {
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     for (int y = 0; y < kRows; ++y) {
       const int x = y * RPW + sub;
       const int row = __shfl_sync(0xffffffffu, to, x);
-      if (r0 + x < m) reinterpret_cast<uint4*>(base + size_t(row) * sl)[c] = v[y];
+      if (r0 + x < m) __stcs(reinterpret_cast<uint4*>(base + size_t(row) * sl) + c, v[y]);
     }
   }
 }
@@ -385,10 +385,10 @@ cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream) {
   cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
   if (e != cudaSuccess) return e;
-  // about eight blocks of eight warps per SM over all units, none without rows
+  // about sixteen blocks of eight warps per SM over all units, none without rows
   const int rows = std::min(a.k, a.Lcap - a.k);
   if (rows < 1) return cudaSuccess;   // a cache of at most k rows never evicts
-  const long long want = std::max(1LL, 8LL * num_sms / ((long long)units * a.n_layers));
+  const long long want = std::max(1LL, 16LL * num_sms / ((long long)units * a.n_layers));
   const int per = kMoveThreads / 32 * kRows * (a.D == 64 ? 2 : 1);
   const dim3 grid(unsigned(std::min<long long>(want, (rows + per - 1) / per)), unsigned(units), unsigned(a.n_layers));
   return a.D == 128 ? launch_pdl(evict_move_kernel<128>, grid, dim3(kMoveThreads), 0, stream, a)

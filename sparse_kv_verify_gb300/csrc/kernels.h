@@ -289,6 +289,7 @@ struct AttendArgs {
   uint16_t* o;               // [B][T][hq][D] bf16
   float* lse;                // [B][T][hq], or nullptr
   int max_tiles;             // tiles of a unit at most
+  int whole;                 // set by attend_launch: CTAs take whole units
   int32_t* seg_cta;          // [units][2]: first and last CTA of each unit's segments
   float* partial;            // segment slots [units + grid][slot_floats]: O [NQ][D], m [NQ], l [NQ]
   int64_t slot_floats;
@@ -303,7 +304,7 @@ struct AttendArgs {
   CUtensorMap qmap, kmap, vmap, pqmap, pkmap, pvmap;
 };
 // The attention kernel, the prefix kernel if there is a prefix, the merge.
-cudaError_t attend_launch(const AttendArgs& a, int D, int num_sms, cudaStream_t stream);
+cudaError_t attend_launch(AttendArgs& a, int D, int num_sms, cudaStream_t stream);
 cudaError_t prefix_launch(const AttendArgs& a, int D, cudaStream_t stream);
 
 // -------------------------------------------------------------- accumulate

@@ -14,40 +14,39 @@ struct Share {
 };
 
 // Called by one whole warp.  tiles(b): the tiles of sequence b (all its units
-// together, up to 2^31 / 32).  The batch is summed 32 sequences at a time and
-// cut into min(CTAs, tiles) equal runs, so that every run holds a tile and a
-// unit's runs lie in consecutive CTAs; later CTAs get count = 0.
+// together).  Each lane sums a run of neighbouring sequences, one scan over the
+// lanes finds the one whose run holds this CTA's first tile, and that lane looks
+// it up.  The batch is cut into min(CTAs, tiles) equal runs, so that every run
+// holds a tile and a unit's runs lie in consecutive CTAs; later CTAs get
+// count = 0.
 template <typename Tiles>
 __device__ __forceinline__ Share share_of(int B, Tiles tiles) {
   const int lane = threadIdx.x & 31;
-  long long total = 0;
-  for (int b0 = 0; b0 < B; b0 += 32) {
-    const int n = b0 + lane < B ? tiles(b0 + lane) : 0;
-    total += __reduce_add_sync(0xffffffffu, unsigned(n));
-  }
-  const long long ctas = total < gridDim.x ? total : gridDim.x;
-  const long long t0 = blockIdx.x < ctas ? blockIdx.x * total / ctas : total;
-  const long long t1 = blockIdx.x < ctas ? (blockIdx.x + 1) * total / ctas : total;
-  Share s{t1 - t0, 0, 0};
-  long long before = 0;
-  for (int b0 = 0; b0 < B && s.count > 0; b0 += 32) {
-    const int n = b0 + lane < B ? tiles(b0 + lane) : 0;
-    int inc = n;
+  const int per = (B + 31) / 32, b0 = lane * per, b1 = min(b0 + per, B);
+  long long mine = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) mine += tiles(b);
+  long long inc = mine;
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, x);
-      if (lane >= x) inc += y;
-    }
-    const long long end = before + inc;
-    const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && t0 < end);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      s.b = b0 + src;
-      s.offset = t0 - __shfl_sync(0xffffffffu, end - n, src);
-      break;
-    }
-    before = __shfl_sync(0xffffffffu, end, 31);
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, x);
+    if (lane >= x) inc += y;
   }
+  const long long total = __shfl_sync(0xffffffffu, inc, 31);
+  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  Share s{0, 0, 0};
+  if (blockIdx.x >= ctas) return s;
+  const long long t0 = blockIdx.x * total / ctas;
+  s.count = (blockIdx.x + 1) * total / ctas - t0;
+  const bool here = t0 < inc && t0 >= inc - mine;
+  if (here) {
+    s.b = b0;
+    s.offset = t0 - (inc - mine);
+    for (int n; s.offset >= (n = tiles(s.b)); ++s.b) s.offset -= n;
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  s.b = __shfl_sync(0xffffffffu, s.b, src);
+  s.offset = __shfl_sync(0xffffffffu, s.offset, src);
   return s;
 }
 
