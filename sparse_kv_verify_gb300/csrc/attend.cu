@@ -643,23 +643,6 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
 // Log-sum-exp merge of a unit's segments: one thread per four output columns.
 // A segment is (unnormalised O, log2-domain reference maximum m, sum l).
 constexpr int kMergeThreads = 128;
-constexpr int kMergeDepth = 8;
-
-struct Merge {
-  float m, l;
-  float4 o;
-};
-__device__ __forceinline__ void merge_in(Merge& a, float m, float l, const float4& o) {
-  const float top = fmaxf(a.m, m);
-  const float ref = top == -INFINITY ? 0.f : top;
-  const float x = exp2f(a.m - ref), y = exp2f(m - ref);   // exp2(-inf) = 0
-  a.m = top;
-  a.l = a.l * x + l * y;
-  a.o.x = a.o.x * x + o.x * y;
-  a.o.y = a.o.y * x + o.y * y;
-  a.o.z = a.o.z * x + o.z * y;
-  a.o.w = a.o.w * x + o.w * y;
-}
 
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendArgs A) {
@@ -697,12 +680,14 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
       all += p1 - p0 + 1;
     }
   }
-  Merge a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int c = 0; c < all; c += kMergeDepth) {   // that many segments' loads in flight
-    float m[kMergeDepth], l[kMergeDepth];
-    float4 o[kMergeDepth];
+  constexpr int kDepth = 8;   // segments whose loads are in flight
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < all; c += kDepth) {
+    float m[kDepth], l[kDepth];
+    float4 o[kDepth];
 #pragma unroll
-    for (int y = 0; y < kMergeDepth; ++y) {
+    for (int y = 0; y < kDepth; ++y) {
       const int z = c + y;
       m[y] = -INFINITY;
       l[y] = 0.f;
@@ -716,14 +701,29 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
         o[y] = __ldcg(reinterpret_cast<const float4*>(s + (mine ? ov : size_t(row) * D + 4 * c4)));
       }
     }
+    float ref = top;
 #pragma unroll
-    for (int y = 0; y < kMergeDepth; ++y) merge_in(a, m[y], l[y], o[y]);
+    for (int y = 0; y < kDepth; ++y) ref = fmaxf(ref, m[y]);
+    const float base = ref == -INFINITY ? 0.f : ref;
+    const float w0 = fast_exp2(top - base);   // 2^-inf = 0
+    top = ref;
+    sum *= w0;
+    acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
+#pragma unroll
+    for (int y = 0; y < kDepth; ++y) {
+      const float w = fast_exp2(m[y] - base);
+      sum = fmaf(l[y], w, sum);
+      acc.x = fmaf(o[y].x, w, acc.x);
+      acc.y = fmaf(o[y].y, w, acc.y);
+      acc.z = fmaf(o[y].z, w, acc.z);
+      acc.w = fmaf(o[y].w, w, acc.w);
+    }
   }
   const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
-  const float inv = a.l > 0.f ? 1.f / a.l : 0.f;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
   reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
-      make_uint2(pack_bf16(a.o.x * inv, a.o.y * inv), pack_bf16(a.o.z * inv, a.o.w * inv));
-  if (A.lse && c4 == 0) A.lse[orow] = a.l > 0.f ? (a.m + log2f(a.l)) * kLn2 : -INFINITY;
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (A.lse && c4 == 0) A.lse[orow] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D, int M, int CPS>
@@ -761,12 +761,12 @@ cudaError_t launch_d(AttendArgs& a, int num_sms, cudaStream_t stream) {
   const bool two = NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
   const long long units = (long long)a.B * a.hkv;
   const int ctas = std::min((two ? 2 : 1) * num_sms, kAttendGridMax);
-  a.whole = a.pgrid == 0 && whole_units(units, a.max_tiles, ctas);
+  a.whole = whole_units(units, a.max_tiles, ctas);
   const int grid = int(std::min<long long>(ctas, units * (a.whole ? 1 : a.max_tiles)));
   cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
                   : NQ <= 64 ? launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream)
                              : launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
-  if (e != cudaSuccess || a.whole) return e;
+  if (e != cudaSuccess || (a.whole && !a.pgrid)) return e;
   if (a.pgrid) e = prefix_launch(a, D, stream);
   if (e != cudaSuccess) return e;
   const dim3 mgrid((NQ * (D / 4) + kMergeThreads - 1) / kMergeThreads, unsigned(a.B * a.hkv));
