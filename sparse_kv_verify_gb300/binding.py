@@ -556,6 +556,7 @@ class _CacheCall:
         for t in self._tensors:
             if t.device != self.device:
                 raise ValueError(f"{fn}: tensors on {self.device} and {t.device}")
+        self._own_ws = ws is None
         if ws is None:
             with torch.cuda.device(self.device):
                 ws = Workspace(need, device=self.device,
@@ -572,6 +573,8 @@ class _CacheCall:
             raise ValueError(f"{self._name}: tensors on {self.device} and a stream on {stream.device}")
         else:
             s = stream.cuda_stream
+            if self._own_ws:   # it may be freed before that stream has come to the call
+                self.ws.buf.record_stream(stream)
         if torch.cuda.current_device() == self.device.index:
             st = self._fn(*self._args, s)
         else:

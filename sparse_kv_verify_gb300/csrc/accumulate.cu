@@ -287,13 +287,14 @@ __global__ void __launch_bounds__(NTH, 2) accumulate_kernel(const __grid_constan
 template <int D>
 cudaError_t launch_d(const AccumulateArgs& a, int num_sms, cudaStream_t stream) {
   auto kern = accumulate_kernel<D>;
-  static const cudaError_t attr = [&] {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [&] {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMax));
     if (e == cudaSuccess)   // room for two CTAs' shared memory
       e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                                int(cudaSharedmemCarveoutMaxShared));
     return e;
-  }();
+  });
   if (attr != cudaSuccess) return attr;
   const long long most = (long long)a.B * a.hkv * ((a.Lcap + TK - 1) / TK);
   const int grid = int(std::min<long long>(2LL * num_sms, most));

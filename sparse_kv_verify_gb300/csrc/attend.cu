@@ -13,7 +13,7 @@
 // the block tile are partial; a row's own window start and the causal rule are
 // masks inside a tile.  How many tiles a unit has depends on its sequence's
 // length, which only the device knows: every CTA sums the tile counts of the
-// batch (one warp, 32 sequences at a time) and takes its equal share of the
+// batch (one warp) and takes its equal share of the
 // flattened tiles (stream-K), so that ragged lengths and any B and hkv load the
 // SMs alike.
 //
@@ -729,13 +729,14 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
 template <int D, int M, int CPS>
 cudaError_t launch_attend(const AttendArgs& a, int grid, size_t smem, cudaStream_t stream) {
   auto kern = attend_kernel<D, M, CPS>;
-  static const cudaError_t attr = [&] {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [&] {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e == cudaSuccess && CPS > 1)   // room for CPS CTAs' shared memory
       e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                                int(cudaSharedmemCarveoutMaxShared));
     return e;
-  }();
+  });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(kern, dim3(grid), dim3(NTH), smem, stream, a);
 }

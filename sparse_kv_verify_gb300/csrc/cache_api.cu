@@ -73,7 +73,7 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
                const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse, void* ws,
                size_t ws_bytes, cudaStream_t stream) {
   if (!params_ok(p)) return DUSTIN_EINVAL;
-  if (!q || !kb || !vb || !o || !seq_len || o == q) return DUSTIN_EINVAL;
+  if (!q || !kb || !vb || !o || !seq_len || o == q || o == lse) return DUSTIN_EINVAL;
   if (!aligned16(q) || !aligned16(kb) || !aligned16(vb) || !aligned16(o) || !aligned4(lse)) return DUSTIN_EINVAL;
   if (!kv_ok(k, p->Lcap) || !kv_ok(v, p->Lcap) || k.hkv != v.hkv || k.d != v.d) return DUSTIN_EINVAL;
   if (pk) {

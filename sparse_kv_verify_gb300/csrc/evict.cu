@@ -358,8 +358,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 }  // namespace
 
 cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+  });
   if (attr != cudaSuccess) return attr;
   const int units = a.B * a.hkv;
   // CTAs per unit: as many as find an SM each, while a CTA keeps kSliceMin rows

@@ -1,6 +1,7 @@
 // Internal launch interface between the C-ABI layer (api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -8,6 +9,20 @@
 #include "../../include/dustin.h"
 
 namespace dustin {
+
+// Runs set() once per device (function attributes belong to the current one).
+// done: one word of device bits per call site.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Launches kern<<<grid, block, smem, stream>>>(args) with programmatic stream
 // serialisation, so that it may begin while the previous kernel in the stream

@@ -508,7 +508,9 @@ cudaError_t launch_t(const AttendArgs& a, cudaStream_t stream) {
   using C = Cfg<D, LANES>;
   static_assert(C::total <= 227 * 1024, "shared memory of a CTA");
   auto kern = prefix_kernel<D, LANES>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::total));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(
+      done, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::total)); });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(kern, dim3(a.pgrid), dim3(NTH), C::total, stream, a);
 }

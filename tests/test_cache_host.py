@@ -150,7 +150,7 @@ def test_window_refusals(L):
         a.update(o)
         return lib.dustin_window_attn(ctypes.byref(p or _params(bd)), *a.values(), ws, nbytes, None)
     for o in [dict(q=None), dict(q=0x1008), dict(kb=None), dict(vb=0x3004), dict(sl=None), dict(o=None),
-              dict(o=0x6008), dict(o=0x1000), dict(lse=0x7002), dict(hq=60), dict(hq=0)]:
+              dict(o=0x6008), dict(o=0x1000), dict(lse=0x6000), dict(lse=0x7002), dict(hq=60), dict(hq=0)]:
         assert call(**o) == -1, o
     for bad in BAD_KV:
         assert call(k=_kv(bd, **bad)) == -1, bad

@@ -52,6 +52,8 @@ WINDOW = [
     ([260, 40], 19, 3, 1, 64, 1, 129),          # 57 query rows
     ([400], 7, 8, 1, 128, 16, 256),             # 56 query rows at d = 128
     ([5], 2, 1, 1, 64, 2, 2),
+    ([150, 20], 1, 128, 1, 64, 3, 70),          # 128 query heads on one KV head
+    ([150], 1, 65, 1, 128, 0, 200),
 ]
 
 
@@ -167,6 +169,8 @@ PREFIX = [
     (257, [5] * 11, 3, 3, 1, 64),                 # G = 3
     (190, [30, 20], 64, 2, 1, 64),                # the largest block
     (500, [17, 0, 90], 2, 5, 1, 128),             # G = 5: tiles that whole tokens do not fill
+    (140, [30, 20, 0], 1, 128, 1, 64),            # one token fills a row tile
+    (140, [30, 20, 0], 1, 65, 1, 128),
 ]
 
 
@@ -530,6 +534,24 @@ def test_graph_replay_on_side_stream_follows_lengths():
             for a, b in zip(snapshot(), want):
                 assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
     assert dk.check(ws) == 0
+
+
+def test_explicit_stream_owns_its_workspace():
+    """A call on a stream that is not the current one, with a workspace of its
+    own that is freed at once and other work that would take its memory."""
+    x = Block([900, 30, 333], 4, 8, 2, 128, seed=23)
+    p = params(x, 4, 600)
+    ref = [t.clone() for t in dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+        o, lse = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq, stream=side)
+        junk = [torch.full((1 << 20,), 3.0e38, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        del junk
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
 def test_deterministic():
