@@ -755,13 +755,37 @@ bool whole_units(long long units, int tiles, long long ctas) {
   return busiest - share <= std::min(11LL, 4 + units / 16);
 }
 
+// The own parts and the prefix one after the other on all SMs, or side by side,
+// the own parts with one CTA on each of x SMs?  us that an SM needs, measured at
+// 64/8/128 (lengths by their capacities, as the host knows no more): an own tile
+// of 64 rows 0.6 and a unit 2 alone on the SM, a tile 0.7 of all SMs' time when
+// the whole GPU streams them; a prefix tile of 128 rows 1.1 with one row tile,
+// 1.75 with two; one after the other costs about 5 us more.  Long calls stay one
+// after the other: there the own parts' CTAs came to share SMs and held the call
+// up (768 rows over 32 K 120 -> 146 us).  Returns x, or 0.
+int beside_sms(long long units, long long own_tiles, long long prefix_tiles, bool two, int num_sms) {
+  const double own = 0.6 * double(own_tiles) + 2.0 * double(units), prefix = (two ? 1.75 : 1.1) * double(prefix_tiles);
+  const int x = std::min(std::max(int(num_sms * own / (own + prefix) + 0.5), 1), num_sms / 2);
+  const double after = (0.7 * double(own_tiles) + prefix) / num_sms + 5;
+  const double beside = std::max(own / x, prefix / (num_sms - x));
+  return after <= 40 && beside < after ? x : 0;
+}
+
 template <int D>
 cudaError_t launch_d(AttendArgs& a, int num_sms, cudaStream_t stream) {
   const int NQ = a.T * (a.hq / a.hkv);
   // 64-row MMAs while the query rows fit, two CTAs per SM while two fit
   const bool two = NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
   const long long units = (long long)a.B * a.hkv;
-  const int ctas = std::min((two ? 2 : 1) * num_sms, kAttendGridMax);
+  int ctas = std::min((two ? 2 : 1) * num_sms, kAttendGridMax);
+  if (a.pgrid) {
+    const int x = beside_sms(units, units * a.max_tiles, (a.Pcap + kPrefixTile - 1) / kPrefixTile * (long long)a.hkv * a.pairs,
+                             a.row_tiles > 1, num_sms);
+    if (x) {
+      ctas = x;
+      a.pgrid = std::min(num_sms - x, kPrefixGridMax);
+    }
+  }
   a.whole = whole_units(units, a.max_tiles, ctas);
   const int grid = int(std::min<long long>(ctas, units * (a.whole ? 1 : a.max_tiles)));
   cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
