@@ -665,16 +665,11 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
   const float* pp = nullptr;
   int row = 0, all = own;
   if constexpr (PREFIX) {
-    // prefix unit pu has tiles [pu * n, (pu + 1) * n) of the flattened key
-    // tiles, CTA c holds [c * total / ctas, (c + 1) * total / ctas)
-    int P = __ldcg(A.prefix_len);
-    if (P < 0 || P > A.Pcap) P = 0;
-    if (P > 0) {
+    const int P = __ldcg(A.prefix_len);
+    if (P > 0 && P <= A.Pcap) {
       const int tok = b * T + r / GQ, tile = tok / A.nt, pu = g * A.pairs + (tile >> 1);
-      const long long n = (P + kPrefixTile - 1) / kPrefixTile, total = n * A.hkv * A.pairs;
-      const long long ctas = total < A.pgrid ? total : A.pgrid;
-      auto cta_of = [&](long long t) { return int(((t + 1) * ctas + total - 1) / total) - 1; };
-      const int p0 = cta_of(pu * n), p1 = cta_of(pu * n + n - 1);
+      const int p0 = min(max(__ldcg(A.pseg_cta + 2 * pu), 0), kPrefixGridMax - 1);
+      const int p1 = min(max(__ldcg(A.pseg_cta + 2 * pu + 1), p0), kPrefixGridMax - 1);
       row = (tok - tile * A.nt) * GQ + r % GQ;
       pp = A.ppartial + ((size_t(pu) + p0) * 2 + (tile & 1)) * kLane;
       all += p1 - p0 + 1;

@@ -29,11 +29,12 @@ int attend_shape(const dustin_params* p, int32_t hq, int32_t hkv, int32_t d) {
 }
 
 // Workspace of an attention call, after the fixed part: every unit's first and
-// last CTA, the segment slots of the sequences' own part, those of the prefix.
+// last CTA and the segment slots of the sequences' own part, then those of the
+// prefix.
 struct AttendPlan {
   int64_t slot_floats;
   int nt, row_tiles, pairs;
-  size_t seg_off, part_off, ppart_off, total;
+  size_t seg_off, part_off, pseg_off, ppart_off, total;
 };
 AttendPlan attend_plan(int B, int hq, int hkv, int d, int T, bool prefix) {
   AttendPlan pl;
@@ -44,7 +45,8 @@ AttendPlan attend_plan(int B, int hq, int hkv, int d, int T, bool prefix) {
   pl.pairs = (pl.row_tiles + 1) / 2;
   pl.seg_off = kScratch;
   pl.part_off = round256(pl.seg_off + size_t(units) * 2 * 4);
-  pl.ppart_off = round256(pl.part_off + size_t(units + kAttendGridMax) * size_t(pl.slot_floats) * 4);
+  pl.pseg_off = round256(pl.part_off + size_t(units + kAttendGridMax) * size_t(pl.slot_floats) * 4);
+  pl.ppart_off = round256(pl.pseg_off + (prefix ? size_t(hkv) * pl.pairs * 2 * 4 : 0));
   pl.total = pl.ppart_off;
   if (prefix)
     pl.total += round256((size_t(hkv) * pl.pairs + kPrefixGridMax) * 2 * kPrefixTile * (size_t(d) + 2) * 4);
@@ -131,6 +133,7 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
     a.nt = pl.nt;
     a.row_tiles = pl.row_tiles;
     a.pairs = pl.pairs;
+    a.pseg_cta = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + pl.pseg_off);
     a.ppartial = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.ppart_off);
     if (!encode_query_map(&a.pqmap, q, k.d, hq, p->B * a.T, hq / k.hkv, pl.nt)) return DUSTIN_ECUDA;
     a.ptma = encode_prefix_map(&a.pkmap, *pk, prefix_cap, kPrefixTile) &&

@@ -315,6 +315,7 @@ struct AttendArgs {
   int pgrid;
   int nt, row_tiles, pairs;  // tokens per row tile; row tiles of a KV head; pairs of them
   float* ppartial;           // slots [(hkv * pairs + pgrid)][2][128 * (D + 2)]: O, m [128], l [128]
+  int32_t* pseg_cta;         // [hkv * pairs][2]: first and last CTA of each prefix unit
   int ptma;                  // the prefix caches have tensor maps
   CUtensorMap qmap, kmap, vmap, pqmap, pkmap, pvmap;
 };

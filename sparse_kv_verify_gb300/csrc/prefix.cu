@@ -310,6 +310,10 @@ __global__ void __launch_bounds__(NTH, 1) prefix_kernel(const __grid_constant__ 
         j0 += n;
         ++segs;
         tc_fence_after();
+        if (tid == 0) {   // (lane 0 has a row tile in every unit)
+          if (sg.i0 == 0) A.pseg_cta[2 * sg.u] = int(blockIdx.x);
+          if (sg.i0 + sg.n == tiles) A.pseg_cta[2 * sg.u + 1] = int(blockIdx.x);
+        }
         float* part = A.ppartial + ((size_t(sg.u) + blockIdx.x) * 2 + ln) * (size_t(TK) * (D + 2));
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
