@@ -18,6 +18,9 @@
 // sum (thread = cache row), warp 4 issues the TMA loads of K tiles into a ring
 // and of each unit's query rows, warp 5 issues the MMAs into one of two S
 // buffers.
+//
+// B = 16, L = 24 K .. 32 K, T = 6, 64/8/128: 141 us for 970 MB, 6.9 TB/s, which is
+// the rate of a plain copy; one token over 4097 rows 5.3 us, latency of one launch.
 #include <algorithm>
 
 #include "common.cuh"

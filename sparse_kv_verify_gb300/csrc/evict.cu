@@ -20,6 +20,11 @@
 //   move    bound by the bytes of the rows: every warp moves four rows at a
 //           time, a row's K and V by half a warp each, loads before stores.
 //           It also sets the lengths, which the first launch read.
+//
+// Cold caches, 128 units (16 sequences x 8 KV heads), d = 128: 32 K rows to 2048:
+// select 34 us, move 45 us for 252 MB (5.6 TB/s); 2054 rows to 2048: select 9.4,
+// move 5.5.  The first with eight rows in flight instead of four takes 4.8 us
+// more, with plain instead of streaming stores 6.7 us more.
 #include <algorithm>
 
 #include <cooperative_groups.h>

@@ -33,8 +33,14 @@
 //   one row tile    (at most 128 query rows in all) the products wait for nobody
 //                   else, so steps of 64 keys with two S buffers (NB = 2): S of
 //                   the next step is there when the softmax comes to it.
-// us at 64/8/128, the whole call, two-tile / one-tile shape: 32 rows over P = 8192
-// 34.2 / 28.3; 768 rows over 32 K 122 / 132; 1280 rows over 64 K 301 / 339.
+// us of the whole call, one row tile in the one-tile / two-tile shape: 32 rows
+// over P = 8192 at 64/8/128 20.1 / 21.6; 14/2/64 behind 3001 rows 13.0 / 13.4.
+// Two row tiles with steps of 128 / 64 keys (runs on two machines, which differ
+// by up to 5 %): 1280 rows over 64 K 301 / 339.
+//
+// 1280 rows over 64 K: this kernel 243 to 254 us, 1.35 to 1.42 PFLOP/s (0.71 to
+// 0.75 of cuBLAS's measured rate): 1.8 us per 128 keys and two row tiles.  Over
+// 16 K the tensor pipe is active 47 % of the time and DRAM 12 %.
 //
 // Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
 // [256, 256 + D) and [384, 384 + D).  Every segment (unit x CTA) writes its row
