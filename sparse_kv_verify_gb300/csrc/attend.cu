@@ -579,11 +579,11 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
         }
         const int rr = act[r] ? row[r] : 0;
         orow[r] = (size_t(w.b) * T + rr / GQ) * A.hq + size_t(w.g) * GQ + rr % GQ;
-        osc[r] = lsum[r] > 0.f ? 1.f / lsum[r] : 0.f;
+        osc[r] = lsum[r] != 0.f ? 1.f / lsum[r] : 0.f;   // (a NaN stays one)
         if (act[r] && (M == 128 || q4 == 0)) {
           if (whole) {
             if (A.lse)
-              A.lse[orow[r]] = lsum[r] > 0.f ? (mref[r] + log2f(lsum[r])) * kLn2 : -INFINITY;
+              A.lse[orow[r]] = lsum[r] != 0.f ? (mref[r] + log2f(lsum[r])) * kLn2 : -INFINITY;
           } else {
             part[size_t(NQ) * D + row[r]] = mref[r];
             part[size_t(NQ) * D + NQ + row[r]] = lsum[r];
@@ -720,10 +720,10 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     }
   }
   const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a NaN stays one)
   reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (A.lse && c4 == 0) A.lse[orow] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (A.lse && c4 == 0) A.lse[orow] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D, int M, int CPS>

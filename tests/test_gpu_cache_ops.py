@@ -472,6 +472,26 @@ def test_evict_bad_length_flagged_and_untouched():
         assert seq.tolist() == [bad, 40] and torch.equal(k0, ks[0]) and torch.equal(w0, w[0])
 
 
+@pytest.mark.parametrize("lens, d", [([40, 9], 64), ([3000, 5], 128)])   # whole units; units split and merged
+@pytest.mark.parametrize("prefix", [False, True])
+def test_query_that_is_not_finite_shows(lens, d, prefix):
+    """NaN in one query row comes out in that row, never as an empty one, and
+    every other row keeps its bits."""
+    x = Block(lens, 3, 8, 2, d, seed=24)
+    p = params(x, 0, 0 if prefix else 2500)
+    pk, pv = prefix_of(300, 2, d)
+    def run():
+        if prefix:
+            return dk.dustin_prefix_attn(p, x.q, pk, pv, i32([300]), x.k, x.v, x.kb, x.vb, x.seq)
+        return dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    o0, l0 = run()
+    x.q[1, 1, 3, 5] = float("nan")
+    o1, l1 = run()
+    assert o1[1, 1, 3].isnan().all() and l1[1, 1, 3].isnan()
+    o1[1, 1, 3], l1[1, 1, 3] = o0[1, 1, 3], l0[1, 1, 3]
+    assert torch.equal(o1, o0) and torch.equal(l1, l0)
+
+
 # ------------------------------------------------ streams, graphs, all together
 
 
