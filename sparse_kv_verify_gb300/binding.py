@@ -8,6 +8,7 @@ a call returns an error status, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_int32, c_int64, c_size_t, c_void_p
@@ -549,21 +550,26 @@ class _CacheCall:
     once and keeps them alive; calling it enqueues the operator on ``stream``
     (default: the current stream of the tensors' device)."""
 
-    def __init__(self, fn: str, p: Params, tensors, ws, need: int, stream):
+    def __init__(self, fn: str, p: Params, tensors, ws, need: int, stream, own=()):
         self._name, self._p = fn, p.c()
+        self._own = list(own)   # what the call has allocated, on the stream self._home
         self._tensors = [t for t in tensors if t is not None]
         self.device = self._tensors[0].device
         for t in self._tensors:
             if t.device != self.device:
                 raise ValueError(f"{fn}: tensors on {self.device} and {t.device}")
-        self._own_ws = ws is None
+        with torch.cuda.device(self.device):
+            self._home = stream or torch.cuda.current_stream(self.device)
+        if self._home.device != self.device:
+            raise ValueError(f"{fn}: tensors on {self.device} and a stream on {self._home.device}")
         if ws is None:
-            with torch.cuda.device(self.device):
-                ws = Workspace(need, device=self.device,
-                               stream=stream or torch.cuda.current_stream(self.device))
+            with torch.cuda.stream(self._home):
+                ws = Workspace(need, device=self.device, stream=self._home)
+            self._own.append(ws.buf)
         elif ws.buf.device != self.device:
             raise ValueError(f"{fn}: tensors on {self.device} and a workspace on {ws.buf.device}")
         self.ws = ws
+        self._home = self._home.cuda_stream
         self._fn = getattr(lib(), fn)
 
     def __call__(self, stream=None):
@@ -573,8 +579,9 @@ class _CacheCall:
             raise ValueError(f"{self._name}: tensors on {self.device} and a stream on {stream.device}")
         else:
             s = stream.cuda_stream
-            if self._own_ws:   # it may be freed before that stream has come to the call
-                self.ws.buf.record_stream(stream)
+        if s != self._home:   # its own buffers may be freed before that stream has come to the call
+            for t in self._own:
+                t.record_stream(stream or torch.cuda.current_stream(self.device))
         if torch.cuda.current_device() == self.device.index:
             st = self._fn(*self._args, s)
         else:
@@ -585,8 +592,9 @@ class _CacheCall:
         return self._result
 
 
-def _block_args(p: Params, q, k, v, kb, vb, seq_len, o, lse):
-    """Checks the tensors of an attention call and allocates its outputs."""
+def _block_args(p: Params, q, k, v, kb, vb, seq_len, o, lse, stream):
+    """Checks the tensors of an attention call and allocates its outputs (on
+    the stream that the call is for); returns the allocated ones last."""
     T = p.gamma + 1
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B][gamma+1][hq][d] and the caches [B][hkv][Lcap][d]")
@@ -597,25 +605,29 @@ def _block_args(p: Params, q, k, v, kb, vb, seq_len, o, lse):
     _shape("kb", kb, p.B, hkv, T, d)
     _shape("vb", vb, p.B, hkv, T, d)
     _shape("seq_len", seq_len, p.B)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    own = []
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        if o is None:
+            o = torch.empty_like(q)
+            own.append(o)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            own.append(lse)
     _shape("o", o, p.B, T, hq, d)
     _shape("lse", lse, p.B, T, hq)
-    return hq, hkv, d, o, lse
+    return hq, hkv, d, o, lse, own
 
 
 class WindowCall(_CacheCall):
     """Pre-marshalled ``dustin_window_attn``; calling it returns ``(o, lse)``."""
 
     def __init__(self, p: Params, q, k, v, kb, vb, seq_len, o=None, lse=None, ws=None, stream=None):
-        hq, hkv, d, o, lse = _block_args(p, q, k, v, kb, vb, seq_len, o, lse)
+        hq, hkv, d, o, lse, own = _block_args(p, q, k, v, kb, vb, seq_len, o, lse, stream)
         bf = torch.bfloat16
         args = (hq, _ptr(q, bf), kv_view(k), kv_view(v), _ptr(kb, bf), _ptr(vb, bf),
                 _ptr(seq_len, torch.int32), _ptr(o, bf), _ptr(lse, torch.float32))
         super().__init__("dustin_window_attn", p, (q, k, v, kb, vb, seq_len, o, lse), ws,
-                         0 if ws is not None else cache_workspace_bytes(p, hq, hkv, d), stream)
+                         0 if ws is not None else cache_workspace_bytes(p, hq, hkv, d), stream, own)
         self._args = (ctypes.byref(self._p),) + args + (self.ws.ptr, self.ws.nbytes)
         self._result = (o, lse)
 
@@ -625,7 +637,7 @@ class PrefixCall(_CacheCall):
 
     def __init__(self, p: Params, q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o=None, lse=None,
                  ws=None, stream=None):
-        hq, hkv, d, o, lse = _block_args(p, q, k, v, kb, vb, seq_len, o, lse)
+        hq, hkv, d, o, lse, own = _block_args(p, q, k, v, kb, vb, seq_len, o, lse, stream)
         if pk.dim() != 4:
             raise ValueError("the prefix caches must be [1][hkv][prefix_cap][d]")
         cap = pk.shape[2]
@@ -638,7 +650,7 @@ class PrefixCall(_CacheCall):
                 _ptr(lse, torch.float32))
         super().__init__("dustin_prefix_attn", p, (q, pk, pv, prefix_len, k, v, kb, vb, seq_len, o, lse),
                          ws, 0 if ws is not None else cache_workspace_bytes(p, hq, hkv, d, prefix_cap=cap),
-                         stream)
+                         stream, own)
         self._args = (ctypes.byref(self._p),) + args + (self.ws.ptr, self.ws.nbytes)
         self._result = (o, lse)
 

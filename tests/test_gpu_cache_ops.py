@@ -574,6 +574,38 @@ def test_explicit_stream_owns_its_workspace():
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
+@pytest.mark.parametrize("how", ["current", "explicit"])
+def test_own_buffers_belong_to_the_stream_that_uses_them(how, monkeypatch):
+    """What a call allocated is recorded on another stream that it runs on, the
+    current one or a given one; on its own stream nothing is."""
+    x = Block([70, 30], 2, 8, 2, 64, seed=25)
+    p = params(x, 4, 60)
+    side = torch.cuda.Stream()
+    call = dk.WindowCall(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    own = {t.data_ptr() for t in (call.ws.buf, *call._result)}
+    torch.cuda.synchronize()
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append((t.data_ptr(), s.cuda_stream)))
+    ref = [t.clone() for t in call()]
+    assert not seen
+    side.wait_stream(torch.cuda.current_stream())
+    if how == "current":
+        with torch.cuda.stream(side):
+            call()
+    else:
+        call(side)
+    side.synchronize()
+    assert sorted(seen) == sorted((a, side.cuda_stream) for a in own)
+    assert all(torch.equal(a, b) for a, b in zip(call._result, ref))
+    # built for a stream: its buffers are that stream's, and a user's are left alone
+    seen.clear()
+    dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq, stream=side)
+    o, lse = (torch.empty_like(t) for t in ref)
+    dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq, o, lse, ws=call.ws)
+    torch.cuda.synchronize()
+    assert not seen and torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
 def test_deterministic():
     x = Block([700, 30, 333], 5, 8, 2, 128, seed=21)
     pk, pv = prefix_of(900, 2, 128)
