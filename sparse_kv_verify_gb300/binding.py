@@ -686,6 +686,8 @@ class EvictCall(_CacheCall):
         n = len(ks)
         if n < 1 or not (len(vs) == len(weights) == len(poss) == n):
             raise ValueError("ks, vs, weights and poss must hold one tensor per layer")
+        if ks[0].dim() != 4:
+            raise ValueError("caches must be [B][hkv][Lcap][d]")
         hkv, d = ks[0].shape[1], ks[0].shape[3]
         for l in range(n):
             _shape(f"ks[{l}]", ks[l], p.B, hkv, p.Lcap, d)

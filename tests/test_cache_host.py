@@ -246,3 +246,12 @@ def test_binding_refuses_wrong_tensors(L):
         L.dustin_evict(p, [k], [k, k], [w], [pos], sl, sl)
     with pytest.raises(ValueError):
         L.dustin_evict(p, [], [], [], [], sl, sl)
+
+
+def test_evict_call_refuses_caches_of_other_ranks(L):
+    p = L.Params(1, 8, 0, 0, 0, 0, 4)
+    flat, w, i = torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 8), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        L.EvictCall(p, [flat], [flat], [w], [w.int()], i, i)
+    with pytest.raises(ValueError):
+        L.EvictCall(p, [flat[0]], [flat[0]], [w], [w.int()], i, i)
