@@ -288,7 +288,7 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
  * the query's own position, and the first p->sinks positions stay visible.
  * Cache rows that no query of the block sees are never read (they may hold
  * anything); keys and values that some query sees must be finite.  A query row
- * that is not finite gives NaN in its own o and lse.
+ * that is not finite and sees a key gives NaN in its own o and lse.
  *   o    device, bf16 [B][gamma+1][hq][d], not q: softmax(q.k/sqrt(d)) v over the
  *        visible keys, 0 where there is none (window = 0)
  *   lse  device, fp32 [B][gamma+1][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf

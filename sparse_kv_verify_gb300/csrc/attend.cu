@@ -63,6 +63,7 @@ constexpr int NTH = 32 * (kPvWarp + 1);
 constexpr int kSCol = 0;            // S buffers: columns [0, 64) and [64, 128)
 constexpr int kPCol = 128;          // P buffers (bf16 pairs) with one CTA per SM
 constexpr uint32_t kSmemPerSm = 228 * 1024;
+constexpr float kNaN = __builtin_nanf("");
 static_assert(TK == DUSTIN_MAX_BLOCK, "the draft block must fit one tile");
 
 // Tensor memory, query buffers and K/V stages per head dimension and CTAs per
@@ -97,6 +98,18 @@ __host__ __device__ inline Lay make_lay(int NQ) {
   L.misc_off = L.bar_off + uint32_t(2 * C::nst + 4 + 2 * C::nqb + 2) * 8;
   L.total = L.misc_off + 48 + 1024;
   return L;
+}
+
+// Where a row's sum of weights is 0 either it sees no key, or every score that it
+// sees is -inf (a query with an infinite element), which is NaN like the 0 / 0 it
+// stands for.  A query sees position 0 as a sink and itself in its window, so the
+// call's parameters tell the two apart.
+__device__ __forceinline__ bool sees_a_key(const AttendArgs& A) { return A.window > 0 || A.sinks > 0; }
+__device__ __forceinline__ float row_scale(const AttendArgs& A, float sum) {
+  return sum != 0.f ? 1.f / sum : sees_a_key(A) ? kNaN : 0.f;   // (a NaN stays one)
+}
+__device__ __forceinline__ float row_lse(const AttendArgs& A, float top, float sum) {
+  return sum != 0.f ? (top + log2f(sum)) * kLn2 : sees_a_key(A) ? kNaN : -INFINITY;
 }
 
 // The tiles of one sequence's units.
@@ -579,11 +592,10 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
         }
         const int rr = act[r] ? row[r] : 0;
         orow[r] = (size_t(w.b) * T + rr / GQ) * A.hq + size_t(w.g) * GQ + rr % GQ;
-        osc[r] = lsum[r] != 0.f ? 1.f / lsum[r] : 0.f;   // (a NaN stays one)
+        osc[r] = row_scale(A, lsum[r]);
         if (act[r] && (M == 128 || q4 == 0)) {
           if (whole) {
-            if (A.lse)
-              A.lse[orow[r]] = lsum[r] != 0.f ? (mref[r] + log2f(lsum[r])) * kLn2 : -INFINITY;
+            if (A.lse) A.lse[orow[r]] = row_lse(A, mref[r], lsum[r]);
           } else {
             part[size_t(NQ) * D + row[r]] = mref[r];
             part[size_t(NQ) * D + NQ + row[r]] = lsum[r];
@@ -720,10 +732,10 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     }
   }
   const size_t orow = (size_t(b) * T + r / GQ) * A.hq + size_t(g) * GQ + r % GQ;
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a NaN stays one)
+  const float inv = row_scale(A, sum);
   reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (A.lse && c4 == 0) A.lse[orow] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (A.lse && c4 == 0) A.lse[orow] = row_lse(A, top, sum);
 }
 
 template <int D, int M, int CPS>

@@ -1,0 +1,78 @@
+"""Corners of the cache operators."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU too
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import sparse_kv_verify_gb300 as dk  # noqa: E402
+
+from _cache_cases import Block, i32, normal  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__ as g
+    g.build()
+
+
+def params(x, sinks=0, window=0):
+    return dk.Params(x.B, x.cap, x.T - 1, sinks, window, 0, max(1, sinks + window))
+
+
+# ------------------------------------------------------- infinite queries
+
+INFINITE = [
+    # lens, T, hq, hkv, d, sinks, window
+    ([40, 9], 1, 8, 2, 64, 0, 1),           # each query sees its own position alone
+    ([40, 9], 1, 8, 2, 128, 0, 1),
+    ([40, 9], 2, 8, 2, 64, 3, 20),
+    ([3000, 5], 3, 8, 2, 128, 0, 2500),     # units split over CTAs and merged
+    ([200, 90], 9, 16, 2, 64, 4, 60),       # 72 query rows
+    ([40, 0], 2, 8, 2, 64, 2, 0),           # sinks alone, of the block itself in an empty cache
+]
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("lens,T,hq,hkv,d,sinks,window", INFINITE)
+def test_window_query_with_an_infinite_element_gives_nan(lens, T, hq, hkv, d, sinks, window, sign):
+    """Every score of the row is an infinity of one sign: 0 / 0 of the softmax,
+    never the 0 and -inf of a row without keys.  Other rows keep their bits."""
+    x = Block(lens, T, hq, hkv, d, seed=31)
+    x.k[..., 5] = x.k[..., 5].abs() + 0.125
+    x.kb[..., 5] = x.kb[..., 5].abs() + 0.125
+    p = params(x, sinks, window)
+    o0, l0 = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    x.q[1, T - 1, 3, 5] = sign * math.inf
+    o1, l1 = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    assert o1[1, T - 1, 3].isnan().all() and l1[1, T - 1, 3].isnan()
+    o1[1, T - 1, 3], l1[1, T - 1, 3] = o0[1, T - 1, 3], l0[1, T - 1, 3]
+    assert torch.equal(o1, o0) and torch.equal(l1, l0)
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("P,lens,T,hq,hkv,d", [(0, [0, 0], 1, 2, 2, 64), (300, [40, 9], 3, 8, 2, 64),
+                                               (700, [900, 0], 2, 8, 2, 128)])
+def test_prefix_query_with_an_infinite_element_gives_nan(P, lens, T, hq, hkv, d, sign):
+    x = Block(lens, T, hq, hkv, d, seed=32)
+    pk, pv = normal(7, 1, hkv, P + 5, d), normal(8, 1, hkv, P + 5, d)
+    for t in (x.k, x.kb, pk):
+        t[..., 5] = t[..., 5].abs() + 0.125
+    p, n = params(x), i32([P])
+    o0, l0 = dk.dustin_prefix_attn(p, x.q, pk, pv, n, x.k, x.v, x.kb, x.vb, x.seq)
+    x.q[0, T - 1, 1, 5] = sign * math.inf
+    o1, l1 = dk.dustin_prefix_attn(p, x.q, pk, pv, n, x.k, x.v, x.kb, x.vb, x.seq)
+    assert o1[0, T - 1, 1].isnan().all() and l1[0, T - 1, 1].isnan()
+    o1[0, T - 1, 1], l1[0, T - 1, 1] = o0[0, T - 1, 1], l0[0, T - 1, 1]
+    assert torch.equal(o1, o0) and torch.equal(l1, l0)
+
+
+def test_infinite_query_that_sees_nothing_is_an_empty_row():
+    x = Block([40, 9], 2, 4, 2, 64, seed=33)
+    x.q[0, 0, 0, 5] = -math.inf
+    o, lse = dk.dustin_window_attn(params(x), x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
