@@ -286,8 +286,8 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
  * position j, block row u position seq_len[b] + u.  A key at position j is
  * visible iff j <= i and (i - j < p->window or j < p->sinks): the window counts
  * the query's own position, and the first p->sinks positions stay visible.
- * Cache rows that no query of the block sees are never read (they may hold
- * anything); keys and values that some query sees must be finite.  A query row
+ * Cache and block rows that no query of the block sees are never read (they may
+ * hold anything); keys and values that some query sees must be finite.  A query row
  * that is not finite and sees a key gives NaN in its own o and lse.
  *   o    device, bf16 [B][gamma+1][hq][d], not q: softmax(q.k/sqrt(d)) v over the
  *        visible keys, 0 where there is none (window = 0)

@@ -117,6 +117,7 @@ struct Tiles {
   int L, w0;      // rows; start of the window range
   int nA, nB, n;  // tiles of the first and the window range; all, the block tile included
   int a_end;      // rows of the first range
+  int nblk;       // block rows that some query sees: all, or without a window the sinks among them
 };
 __device__ __forceinline__ Tiles tiles_of(const AttendArgs& A, int b) {
   Tiles s;
@@ -133,6 +134,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttendArgs& A, int b) {
   s.nA = (s.a_end + TK - 1) / TK;
   s.nB = (L - w0 + TK - 1) / TK;
   s.n = s.nA + s.nB + 1;
+  s.nblk = A.window > 0 ? A.T : min(max(A.sinks - L, 0), A.T);
   return s;
 }
 
@@ -171,12 +173,12 @@ __device__ __forceinline__ void walk_next(Walk& w, const AttendArgs& A) {
 }
 
 // First key position and number of rows of tile tt.
-__device__ __forceinline__ void tile_rows(const Walk& w, int T, int tt, int& base, int& nv, bool& blk) {
+__device__ __forceinline__ void tile_rows(const Walk& w, int tt, int& base, int& nv, bool& blk) {
   const Tiles& s = w.s;
   blk = tt == s.n - 1;
   if (blk) {
     base = s.L;
-    nv = T;
+    nv = s.nblk;
   } else if (tt < s.nA) {
     base = tt * TK;
     nv = min(TK, s.a_end - base);
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
       for (int i = 0; i < w.n; ++i, ++gi) {
         int base, nv;
         bool blk;
-        tile_rows(w, T, w.ta + i, base, nv, blk);
+        tile_rows(w, w.ta + i, base, nv, blk);
         const int st = gi % NST;
         if (gi >= NST &&
             !__all_sync(0xffffffffu, mbar_wait(&empty[st], uint32_t(gi / NST - 1) & 1u, A.err, abort_flag))) {
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(NTH, CPS) attend_kernel(const __grid_constant_
       for (int i = 0; i < w.n; ++i, ++gi) {
         int base, nv;
         bool blk;
-        tile_rows(w, T, w.ta + i, base, nv, blk);
+        tile_rows(w, w.ta + i, base, nv, blk);
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[gi & 1], uint32_t(gi >> 1) & 1u, A.err, abort_flag))) {
           live = false;
           break;

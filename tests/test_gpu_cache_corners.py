@@ -76,3 +76,21 @@ def test_infinite_query_that_sees_nothing_is_an_empty_row():
     x.q[0, 0, 0, 5] = -math.inf
     o, lse = dk.dustin_window_attn(params(x), x.q, x.k, x.v, x.kb, x.vb, x.seq)
     assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
+# ------------------------------------------- block rows that nobody sees
+
+
+@pytest.mark.parametrize("lens,T,hq,hkv,d,sinks", [([90, 3, 0], 4, 4, 2, 64, 5), ([90, 3, 0], 4, 4, 2, 128, 0),
+                                                   ([90, 60, 1], 9, 16, 2, 64, 64)])
+def test_without_a_window_unseen_block_rows_may_hold_anything(lens, T, hq, hkv, d, sinks):
+    """With a window of 0 a query sees sinks alone, not even its own position:
+    block rows at or beyond the sinks are no query's."""
+    x = Block(lens, T, hq, hkv, d, seed=34)
+    p = params(x, sinks, 0)
+    o0, l0 = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    for b, L in enumerate(lens):
+        x.kb[b, :, max(0, sinks - L):] = float("nan")
+        x.vb[b, :, max(0, sinks - L):] = float("nan")
+    o1, l1 = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    assert torch.equal(o1, o0) and torch.equal(l1, l0)
