@@ -548,7 +548,11 @@ def _shape(name: str, t: torch.Tensor, *want: int):
 class _CacheCall:
     """A pre-marshalled call: checks its tensors' shapes, types and devices
     once and keeps them alive; calling it enqueues the operator on ``stream``
-    (default: the current stream of the tensors' device)."""
+    (default: the current stream of the tensors' device).  The outputs and the
+    workspace that it allocates are ready on any stream: the first call on
+    another one than it was built for waits for that one's work up to then.
+    (Not in a graph capture, which can wait for nothing outside: whoever
+    captures orders the streams, as ``torch.cuda.graph`` does.)"""
 
     def __init__(self, fn: str, p: Params, tensors, ws, need: int, stream, own=()):
         self._name, self._p = fn, p.c()
@@ -569,8 +573,22 @@ class _CacheCall:
         elif ws.buf.device != self.device:
             raise ValueError(f"{fn}: tensors on {self.device} and a workspace on {ws.buf.device}")
         self.ws = ws
-        self._home = self._home.cuda_stream
+        self._built_on, self._home = self._home, self._home.cuda_stream
+        self._joined = set()   # streams that have waited for that one
         self._fn = getattr(lib(), fn)
+
+    def _join(self, other):
+        """Lets ``other`` use the buffers that the call has allocated."""
+        for t in self._own:   # they may be freed before that stream has come to the call
+            t.record_stream(other)
+        if other.cuda_stream in self._joined:
+            return
+        for x in (self._built_on, other):
+            with torch.cuda.stream(x):
+                if torch.cuda.is_current_stream_capturing():
+                    return
+        other.wait_stream(self._built_on)
+        self._joined.add(other.cuda_stream)
 
     def __call__(self, stream=None):
         if stream is None:   # (the stream's handle without an object around it: 2 us less)
@@ -579,9 +597,8 @@ class _CacheCall:
             raise ValueError(f"{self._name}: tensors on {self.device} and a stream on {stream.device}")
         else:
             s = stream.cuda_stream
-        if s != self._home:   # its own buffers may be freed before that stream has come to the call
-            for t in self._own:
-                t.record_stream(stream or torch.cuda.current_stream(self.device))
+        if s != self._home and self._own:
+            self._join(stream or torch.cuda.current_stream(self.device))
         if torch.cuda.current_device() == self.device.index:
             st = self._fn(*self._args, s)
         else:

@@ -94,3 +94,33 @@ def test_without_a_window_unseen_block_rows_may_hold_anything(lens, T, hq, hkv, 
         x.vb[b, :, max(0, sinks - L):] = float("nan")
     o1, l1 = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
     assert torch.equal(o1, o0) and torch.equal(l1, l0)
+
+
+# ------------------------------------------------------- another stream
+
+
+@pytest.mark.parametrize("how", ["current", "explicit"])
+def test_call_on_another_stream_waits_for_its_own_buffers(how):
+    """What a call allocates is its home stream's: the workspace is initialised
+    there, and the memory may have been another tensor's that work there still
+    uses.  On another stream the call comes after that."""
+    x = Block([70, 30], 2, 8, 2, 64, seed=35)
+    p = params(x, 4, 60)
+    ref = [t.clone() for t in dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)]
+    home, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(home):   # (memory of that stream, so that nothing is allocated behind the delay)
+        dk.WindowCall(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(home):
+        torch.cuda._sleep(400_000_000)
+        call = dk.WindowCall(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    assert not home.query()
+    if how == "current":
+        with torch.cuda.stream(side):
+            call()
+    else:
+        call(side)
+    side.synchronize()
+    assert home.query()
+    assert all(torch.equal(a, b) for a, b in zip(call._result, ref))
+    assert dk.check(call.ws) == 0
