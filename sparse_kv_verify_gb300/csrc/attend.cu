@@ -13,9 +13,10 @@
 // the block tile are partial; a row's own window start and the causal rule are
 // masks inside a tile.  How many tiles a unit has depends on its sequence's
 // length, which only the device knows: every CTA sums the tile counts of the
-// batch (one warp) and takes its equal share of the
-// flattened tiles (stream-K), so that ragged lengths and any B and hkv load the
-// SMs alike.
+// batch (one warp) and takes its equal share of the flattened tiles (stream-K),
+// so that ragged lengths and any B and hkv load the SMs alike.  Where units are
+// short, CTAs take whole units instead and nothing needs merging (whole_units
+// below).
 //
 // Roles inside a CTA (warp specialised, handing over through mbarriers):
 //   warps 4-7    loaders: a whole tile comes as tiled TMA loads (a K and a V
@@ -30,8 +31,6 @@
 //                when a tile passes it by more than 2^8 (O is rarely rescaled).
 //                P is rounded to bf16 for the second MMA; the row sum adds the
 //                unrounded fp32 values, so lse keeps fp32 accuracy.
-// Where units are short or many (whole_units below) CTAs take whole units
-// instead, and nothing needs merging.
 //
 // A segment that covers a whole unit writes o and lse; otherwise its row
 // maxima, sums and unnormalised O go to slot unit + cta of the workspace (both
@@ -758,15 +757,27 @@ cudaError_t launch_attend(const AttendArgs& a, int grid, size_t smem, cudaStream
 // Whole units per CTA or tiles split evenly: whole units save the merge and the
 // partials' traffic, worth about 4 tiles of a CTA's time for a few units and 11
 // from a hundred on, and cost the tiles that the busiest CTA has beyond its
-// share.  us whole / split, T = 1 or 5, 64/8/128, by units and window (tiles):
-//     8 units   128 (4) 7.8 /  7.9, 448 (9) 11.2 /  8.9
-//    32         448 (9) 12.1 / 12.3, 1024 (18) 18.6 / 13.4
-//   128         128 (4) 9.2 / 15.7, 1024 (18) 20.2 / 22.0, 2048 (34) 33.3 / 31.4
-//   512         128 (4) 18.5 / 30.2, 2048 (34) 88.6 / 93.3
+// share.  The host knows no lengths, so the rule takes every unit to be as long as
+// it can be; where one sequence is long and the others short, whole units leave
+// their CTAs all of its tiles, so no CTA gets more than kWholeTiles in that way.
+// us whole / split, T = 1, 64/8/128, calls in a graph, by units and window (tiles),
+// with every sequence longer than the window, and with one that long among
+// sequences of 60 rows:
+//     8 units   128 (3)  6.9 /  7.9,   448 (8) 10.0 / 8.2
+//    32         448 (8) 10.3 /  9.8,  1024 (17) 15.8 / 11.9
+//   128         448 (8) 11.3 / 14.1,  one long: 10.8 / 10.0
+//   128        1024 (17) 17.8 / 16.9, one long: 16.4 / 12.9
+//   304        1024 (17) 27.1 / 29.3, one long: 17.5 / 13.8
+//   304        2048 (33) 49.5 / 51.7, one long: 27.4 / 14.6
+//   304        4096 (65) 94.0 / 95.7, one long: 47.5 / 18.4
+//   608         448 (8) 24.5 / 27.4,  one long: 19.4 / 17.7
+//   608        1024 (17) 49.7 / 52.8, one long: 31.0 / 18.5
+// (14/2/64, 304 units: 1024 15.4 / 17.2 and 14.6 / 12.1, 2048 28.7 / 30.6 and 22.9 / 12.6).
+constexpr int kWholeTiles = 20;
 bool whole_units(long long units, int tiles, long long ctas) {
   const long long busiest = (units + ctas - 1) / ctas * tiles;
   const long long share = std::max(1LL, units * tiles / ctas);
-  return busiest - share <= std::min(11LL, 4 + units / 16);
+  return busiest <= kWholeTiles && busiest - share <= std::min(11LL, 4 + units / 16);
 }
 
 // The own parts and the prefix one after the other on all SMs, or side by side,

@@ -124,3 +124,40 @@ def test_call_on_another_stream_waits_for_its_own_buffers(how):
     assert home.query()
     assert all(torch.equal(a, b) for a, b in zip(call._result, ref))
     assert dk.check(call.ws) == 0
+
+
+# --------------------------------------------------------- ragged batches
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_one_long_sequence_among_short_ones_is_shared_among_the_sms(prefix):
+    """As many rows in all, most of them one sequence's or spread evenly, for a
+    batch with one unit per CTA: a long unit left to one CTA takes three to
+    seven times as long, so a factor of 2.5 tells."""
+    B = torch.cuda.get_device_properties(0).multi_processor_count * 2 // 8
+    cap = 8192
+    q, k, v = normal(1, B, 1, 64, 128), normal(2, B, 8, cap, 128), normal(3, B, 8, cap, 128)
+    kb, vb = normal(4, B, 8, 1, 128), normal(5, B, 8, 1, 128)
+    pk, pv = normal(6, 1, 8, 64, 128), normal(7, 1, 8, 64, 128)
+    seq = i32([64] * B)
+    p = dk.Params(B, cap, 0, 0, cap, 0, cap)
+    call = (dk.PrefixCall(p, q, pk, pv, i32([64]), k, v, kb, vb, seq) if prefix
+            else dk.WindowCall(p, q, k, v, kb, vb, seq))
+
+    def best(lens):
+        seq.copy_(i32(lens))
+        times = []
+        for _ in range(30):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    long = [64] * (B - 1) + [cap]
+    even = best([sum(long) // B] * B)
+    assert best(long) < 2.5 * even
+    o, lse = (t.clone() for t in call())
+    assert bool(o.isfinite().all()) and bool(lse.isfinite().all()) and dk.check(call.ws) == 0
