@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU too
 
 import sparse_kv_verify_gb300 as dk  # noqa: E402
 
-from _cache_cases import Block, i32, normal  # noqa: E402
+from _cache_cases import Block, assert_attended, attend64, i32, logit_error, normal  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -161,3 +161,49 @@ def test_one_long_sequence_among_short_ones_is_shared_among_the_sms(prefix):
     assert best(long) < 2.5 * even
     o, lse = (t.clone() for t in call())
     assert bool(o.isfinite().all()) and bool(lse.isfinite().all()) and dk.check(call.ws) == 0
+
+
+# ------------------------------------------------ shapes of the attention kernel
+
+ROWS = [
+    # T, hq, hkv: query rows per KV head
+    (5, 12, 1),      # 60
+    (8, 16, 2),      # 64
+    (5, 13, 1),      # 65
+    (9, 16, 2),      # 72
+    (8, 32, 2),      # 128
+]
+
+
+def check_rows(x, o, lse, keys_of, sinks, window):
+    """o and lse of every (sequence, KV head) against float64."""
+    G = x.hq // x.hkv
+    for b in range(x.B):
+        for g in range(x.hkv):
+            keys, vals = keys_of(b, g)
+            n = keys.shape[0]
+            i = n - x.T + torch.arange(x.T, device="cuda").repeat_interleave(G).view(-1, 1)
+            j = torch.arange(n, device="cuda")
+            seen = (j <= i) & ((i - j < window) | (j < sinks))
+            pick = lambda a: a[b, :, g * G:(g + 1) * G].reshape(x.T * G, -1)
+            ro, rl, ra = attend64(pick(x.q), keys, vals, seen)
+            assert_attended(pick(o), pick(lse).squeeze(-1), ro.cpu().numpy(), rl.cpu().numpy(), ra.cpu().numpy(),
+                            logit_error(x.q, keys), n)
+
+
+@pytest.mark.parametrize("lens", [[60, 5], [5003, 300, 0]])   # whole units; units split and merged
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,hq,hkv", ROWS)
+def test_query_rows_whole_and_split(T, hq, hkv, d, lens):
+    """57 to 64 rows take one CTA per SM at d = 128, more take 128-row products;
+    each over units of one CTA and of several, alone and behind a prefix."""
+    x = Block(lens, T, hq, hkv, d, seed=T * hq)
+    p = params(x, 7, 2900)
+    o, lse = dk.dustin_window_attn(p, x.q, x.k, x.v, x.kb, x.vb, x.seq)
+    own = lambda c, blk, b, g: torch.cat([c[b, g, :lens[b]], blk[b, g]])
+    check_rows(x, o, lse, lambda b, g: (own(x.k, x.kb, b, g), own(x.v, x.vb, b, g)), 7, 2900)
+    P = 333
+    pk, pv = normal(77, 1, hkv, P, d), normal(78, 1, hkv, P, d)
+    o, lse = dk.dustin_prefix_attn(p, x.q, pk, pv, i32([P]), x.k, x.v, x.kb, x.vb, x.seq)
+    check_rows(x, o, lse, lambda b, g: (torch.cat([pk[0, g], own(x.k, x.kb, b, g)]),
+                                        torch.cat([pv[0, g], own(x.v, x.vb, b, g)])), 0, 1 << 30)
