@@ -86,9 +86,9 @@ struct Lay {
 };
 
 template <int D, int CPS>
-__host__ __device__ inline Lay make_lay(int NQ) {
+__host__ __device__ constexpr Lay make_lay(int NQ) {
   using C = Cfg<D, CPS>;
-  Lay L;
+  Lay L{};
   const int q_rows = NQ < 8 ? 8 : (NQ + 7) & ~7;
   L.q_panel = uint32_t(q_rows) * 128;
   L.q_buf = (D / 64) * L.q_panel;
@@ -796,13 +796,25 @@ int beside_sms(long long units, long long own_tiles, long long prefix_tiles, boo
   return after <= 40 && beside < after ? x : 0;
 }
 
+// 64-row MMAs while the query rows fit, two CTAs per SM while two fit (at d = 64
+// for every count of rows, so the shape between has no kernel there).
+template <int D>
+constexpr bool two_fit(int NQ) {
+  return NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
+}
+template <int D>
+cudaError_t launch_own(const AttendArgs& a, int NQ, int grid, cudaStream_t stream) {
+  if (two_fit<D>(NQ)) return launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream);
+  if constexpr (!two_fit<D>(64))
+    if (NQ <= 64) return launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
+  return launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
+}
+
 template <int D>
 cudaError_t launch_d(AttendArgs& a, int num_sms, cudaStream_t stream) {
   const int NQ = a.T * (a.hq / a.hkv);
-  // 64-row MMAs while the query rows fit, two CTAs per SM while two fit
-  const bool two = NQ <= 64 && 2 * (make_lay<D, 2>(NQ).total + 1024) <= kSmemPerSm;
   const long long units = (long long)a.B * a.hkv;
-  int ctas = std::min((two ? 2 : 1) * num_sms, kAttendGridMax);
+  int ctas = std::min((two_fit<D>(NQ) ? 2 : 1) * num_sms, kAttendGridMax);
   if (a.pgrid) {
     const int x = beside_sms(units, units * a.max_tiles, (a.Pcap + kPrefixTile - 1) / kPrefixTile * (long long)a.hkv * a.pairs,
                              a.row_tiles > 1, num_sms);
@@ -813,9 +825,7 @@ cudaError_t launch_d(AttendArgs& a, int num_sms, cudaStream_t stream) {
   }
   a.whole = whole_units(units, a.max_tiles, ctas);
   const int grid = int(std::min<long long>(ctas, units * (a.whole ? 1 : a.max_tiles)));
-  cudaError_t e = two        ? launch_attend<D, 64, 2>(a, grid, make_lay<D, 2>(NQ).total, stream)
-                  : NQ <= 64 ? launch_attend<D, 64, 1>(a, grid, make_lay<D, 1>(NQ).total, stream)
-                             : launch_attend<D, 128, 1>(a, grid, make_lay<D, 1>(NQ).total, stream);
+  cudaError_t e = launch_own<D>(a, NQ, grid, stream);
   if (e != cudaSuccess || (a.whole && !a.pgrid)) return e;
   if (a.pgrid) e = prefix_launch(a, D, stream);
   if (e != cudaSuccess) return e;
