@@ -289,11 +289,12 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
  * Cache and block rows that no query of the block sees are never read (they may
  * hold anything); keys and values that some query sees must be finite.  A query row
  * that is not finite and sees a key gives NaN in its own o and lse.
- *   o    device, bf16 [B][gamma+1][hq][d], not q: softmax(q.k/sqrt(d)) v over the
+ *   o    device, bf16 [B][gamma+1][hq][d]: softmax(q.k/sqrt(d)) v over the
  *        visible keys, 0 where there is none (window = 0)
  *   lse  device, fp32 [B][gamma+1][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf
  *        where no key is visible
- * q, k, v, kb, vb as in dustin_verify_layer; hkv * B <= 16384 (DUSTIN_ERANGE).
+ * o and lse share memory with each other and with no input (an input given as
+ * either: DUSTIN_EINVAL).  q, k, v, kb, vb as in dustin_verify_layer; hkv * B <= 16384 (DUSTIN_ERANGE).
  * p->m and p->k are not used beyond their checks.  A sequence whose seq_len is
  * outside [0, Lcap] is flagged (DUSTIN_DEV_SEQLEN) and taken as empty. */
 int dustin_window_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv k, dustin_kv v,
@@ -326,8 +327,9 @@ int dustin_prefix_attn(const dustin_params* p, int32_t hq, const void* q, dustin
  *   q, lse         of the attention call that verified the block
  *   n_seen         device int32 [B]: tokens the sequence has had so far, the new
  *                  ones included (n_seen[b] >= seq_len[b]; more once rows were evicted)
- *   weight, pos    device fp32 / int32 [B][hkv][Lcap]; rows at or beyond
- *                  seq_len[b] are left as they were
+ *   weight, pos    device fp32 / int32 [B][hkv][Lcap], no input's memory
+ *                  (DUSTIN_EINVAL); rows at or beyond seq_len[b] are left as
+ *                  they were
  * A sequence whose n is outside [0, min(gamma+1, L)], L outside [0, Lcap] or
  * n_seen below L is left untouched and flagged (DUSTIN_DEV_APPEND). */
 int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const float* lse, dustin_kv k,

@@ -75,7 +75,12 @@ int run_attend(const dustin_params* p, int32_t hq, const void* q, const dustin_k
                const void* kb, const void* vb, const int32_t* seq_len, void* o, float* lse, void* ws,
                size_t ws_bytes, cudaStream_t stream) {
   if (!params_ok(p)) return DUSTIN_EINVAL;
-  if (!q || !kb || !vb || !o || !seq_len || o == q || o == lse) return DUSTIN_EINVAL;
+  if (!q || !kb || !vb || !o || !seq_len || o == lse) return DUSTIN_EINVAL;
+  // (units are written while others are still read)
+  for (const void* in : {q, kb, vb, static_cast<const void*>(k.ptr), static_cast<const void*>(v.ptr),
+                         static_cast<const void*>(seq_len), static_cast<const void*>(prefix_len),
+                         static_cast<const void*>(pk ? pk->ptr : nullptr), static_cast<const void*>(pv ? pv->ptr : nullptr)})
+    if (in && (in == o || in == lse)) return DUSTIN_EINVAL;
   if (!aligned16(q) || !aligned16(kb) || !aligned16(vb) || !aligned16(o) || !aligned4(lse)) return DUSTIN_EINVAL;
   if (!kv_ok(k, p->Lcap) || !kv_ok(v, p->Lcap) || k.hkv != v.hkv || k.d != v.d) return DUSTIN_EINVAL;
   if (pk) {
@@ -182,7 +187,10 @@ int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const f
   if (!params_ok(p)) return DUSTIN_EINVAL;
   if (!q || !lse || !n_new || !seq_len || !n_seen || !weight || !pos) return DUSTIN_EINVAL;
   if (!aligned16(q) || !aligned4(lse) || !aligned4(weight) || !aligned4(pos)) return DUSTIN_EINVAL;
-  if (static_cast<const void*>(weight) == pos || weight == lse) return DUSTIN_EINVAL;
+  if (static_cast<const void*>(weight) == pos) return DUSTIN_EINVAL;
+  for (const void* in : {q, static_cast<const void*>(lse), static_cast<const void*>(k.ptr), static_cast<const void*>(n_new),
+                         static_cast<const void*>(seq_len), static_cast<const void*>(n_seen)})
+    if (in == weight || in == pos) return DUSTIN_EINVAL;
   if (!kv_ok(k, p->Lcap)) return DUSTIN_EINVAL;
   const int st = attend_shape(p, hq, k.hkv, k.d);
   if (st != DUSTIN_OK) return st;

@@ -255,3 +255,22 @@ def test_evict_call_refuses_caches_of_other_ranks(L):
         L.EvictCall(p, [flat], [flat], [w], [w.int()], i, i)
     with pytest.raises(ValueError):
         L.EvictCall(p, [flat[0]], [flat[0]], [w], [w.int()], i, i)
+
+
+def test_outputs_that_are_inputs_are_refused(L):
+    """Units write their rows while others still read: no input can be an output."""
+    bd, lib = L.binding, L.lib()
+    k, v = _kv(bd, ptr=0x10000), _kv(bd, ptr=0x20000)
+    pk, pv = _kv(bd, ptr=0x30000), _kv(bd, ptr=0x40000)
+    ws = (0x100000, 1 << 30, None)
+    p = ctypes.byref(_params(bd))
+    for out in (0x1000, 0x2000, 0x3000, 0x5000, 0x10000, 0x20000):
+        assert lib.dustin_window_attn(p, 64, 0x1000, k, v, 0x2000, 0x3000, 0x5000, out, 0x7000, *ws) == -1, hex(out)
+        assert lib.dustin_window_attn(p, 64, 0x1000, k, v, 0x2000, 0x3000, 0x5000, 0x6000, out, *ws) == -1, hex(out)
+    for out in (0x1000, 0x2000, 0x3000, 0x5000, 0x8000, 0x10000, 0x20000, 0x30000, 0x40000):
+        for o, lse in ((out, 0x7000), (0x6000, out)):
+            assert lib.dustin_prefix_attn(p, 64, 0x1000, pk, pv, 1024, 0x8000, k, v, 0x2000, 0x3000, 0x5000, o, lse,
+                                          *ws) == -1, hex(out)
+    for out in (0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x10000):
+        for w, pos in ((out, 0x7000), (0x6000, out)):
+            assert lib.dustin_accumulate(p, 64, 0x1000, 0x2000, k, 0x3000, 0x4000, 0x5000, w, pos, *ws) == -1, hex(out)
