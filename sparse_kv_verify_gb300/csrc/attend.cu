@@ -787,13 +787,24 @@ bool whole_units(long long units, int tiles, long long ctas) {
 // the whole GPU streams them; a prefix tile of 128 rows 1.1 with one row tile,
 // 1.75 with two; one after the other costs about 5 us more.  Long calls stay one
 // after the other: there the own parts' CTAs came to share SMs and held the call
-// up (768 rows over 32 K 120 -> 146 us).  Returns x, or 0.
+// up (768 rows over 32 K 120 -> 146 us).  So do calls whose one part would get so
+// few SMs that it takes more than 20 us longer on them than on all: where the
+// other part is much shorter than its cache, that is what the call waits for.
+// us side by side / one after the other, single tokens of 4 sequences in a graph,
+// with lengths as the caches have room for, and with a prefix of 100 rows:
+//   prefix cache  8 K, own  576   18.0 / 24.1, 15.4 / 17.2   side by side
+//                32 K       576   36.9 / 45.5, 24.2 / 17.2   side by side
+//                32 K      2048   43.5 / 47.9, 32.0 / 19.3   side by side
+//                64 K       576   56.8 / 63.1, 41.4 / 17.3   one after the other
+//                64 K      2048   66.9 / 66.0, 49.4 / 19.3   one after the other
+// Returns x, or 0.
 int beside_sms(long long units, long long own_tiles, long long prefix_tiles, bool two, int num_sms) {
   const double own = 0.6 * double(own_tiles) + 2.0 * double(units), prefix = (two ? 1.75 : 1.1) * double(prefix_tiles);
   const int x = std::min(std::max(int(num_sms * own / (own + prefix) + 0.5), 1), num_sms / 2);
-  const double after = (0.7 * double(own_tiles) + prefix) / num_sms + 5;
-  const double beside = std::max(own / x, prefix / (num_sms - x));
-  return after <= 40 && beside < after ? x : 0;
+  const double own_all = 0.7 * double(own_tiles) / num_sms, prefix_all = prefix / num_sms;
+  const double own_few = own / x, prefix_few = prefix / (num_sms - x), after = own_all + prefix_all + 5;
+  if (after > 40 || std::max(own_few, prefix_few) >= after) return 0;
+  return std::max(own_few - own_all, prefix_few - prefix_all) <= 20 ? x : 0;
 }
 
 // 64-row MMAs while the query rows fit, two CTAs per SM while two fit (at d = 64

@@ -126,7 +126,21 @@ def test_call_on_another_stream_waits_for_its_own_buffers(how):
     assert dk.check(call.ws) == 0
 
 
-# --------------------------------------------------------- ragged batches
+# --------------------------------------- lengths far from what a launch is planned for
+
+
+def best_us(call):
+    """The shortest time of a call among others, in us."""
+    times = []
+    for _ in range(30):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            call()
+        b.record()
+        b.synchronize()
+        times.append(100 * a.elapsed_time(b))
+    return min(times)
 
 
 @pytest.mark.parametrize("prefix", [False, True])
@@ -146,21 +160,38 @@ def test_one_long_sequence_among_short_ones_is_shared_among_the_sms(prefix):
 
     def best(lens):
         seq.copy_(i32(lens))
-        times = []
-        for _ in range(30):
-            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            a.record()
-            for _ in range(10):
-                call()
-            b.record()
-            b.synchronize()
-            times.append(a.elapsed_time(b))
-        return min(times)
+        return best_us(call)
     long = [64] * (B - 1) + [cap]
     even = best([sum(long) // B] * B)
     assert best(long) < 2.5 * even
     o, lse = (t.clone() for t in call())
     assert bool(o.isfinite().all()) and bool(lse.isfinite().all()) and dk.check(call.ws) == 0
+
+
+def test_short_prefix_in_a_large_cache_does_not_wait_for_its_own_parts():
+    """The launch is planned by capacities.  A large prefix cache must not leave
+    the own parts so few SMs that, behind a short prefix, the call takes two and
+    a half times as long as with a small cache."""
+    B, rows = 4, 512
+    q, k, v = normal(1, B, 1, 64, 128), normal(2, B, 8, 576, 128), normal(3, B, 8, 576, 128)
+    kb, vb, seq, n = normal(4, B, 8, 1, 128), normal(5, B, 8, 1, 128), i32([rows] * B), i32([100])
+    p = dk.Params(B, 576, 0, 0, 0, 0, 1)
+    us, out = [], []
+    for cap in (128, 65536):
+        pk, pv = normal(6, 1, 8, cap, 128), normal(7, 1, 8, cap, 128)
+        if out:
+            pk[:, :, :100], pv[:, :, :100] = first[0][:, :, :100], first[1][:, :, :100]
+        else:
+            first = pk, pv
+        call = dk.PrefixCall(p, q, pk, pv, n, k, v, kb, vb, seq)
+        us.append(best_us(call))
+        out.append([t.clone() for t in call()])
+    assert us[1] < 1.8 * us[0]
+    # cut among other numbers of CTAs: two sums of the same terms, off by 2^-24 a
+    # term, their exponentials by 2^-21, and the logarithms' rounding
+    lse = [x[1] for x in out]
+    bound = 2 * ((rows + 101) * 2.0 ** -24 + 2.0 ** -21) + 2.0 ** -22 * float(lse[0].abs().max())
+    assert float((lse[0] - lse[1]).abs().max()) <= bound
 
 
 # ------------------------------------------------ shapes of the attention kernel
