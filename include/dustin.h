@@ -293,8 +293,11 @@ size_t dustin_cache_workspace_bytes(const dustin_params* p, int32_t hq, int32_t 
  *        visible keys, 0 where there is none (window = 0)
  *   lse  device, fp32 [B][gamma+1][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf
  *        where no key is visible
- * o and lse share memory with each other and with no input (an input given as
- * either: DUSTIN_EINVAL).  q, k, v, kb, vb as in dustin_verify_layer; hkv * B <= 16384 (DUSTIN_ERANGE).
+ * o and lse share memory neither with each other nor with an input (the same
+ * pointer twice: DUSTIN_EINVAL).  The softmax weights are rounded to bf16 for the
+ * product with v, each by at most 2^-8 of itself, and o once more; their sum, and
+ * so lse, takes them unrounded in fp32.  q, k, v, kb, vb as in
+ * dustin_verify_layer; hkv * B <= 16384 (DUSTIN_ERANGE).
  * p->m and p->k are not used beyond their checks.  A sequence whose seq_len is
  * outside [0, Lcap] is flagged (DUSTIN_DEV_SEQLEN) and taken as empty. */
 int dustin_window_attn(const dustin_params* p, int32_t hq, const void* q, dustin_kv k, dustin_kv v,
@@ -323,7 +326,8 @@ int dustin_prefix_attn(const dustin_params* p, int32_t hq, const void* q, dustin
  *   weight[b][g][j] += sum over t < n with j <= L - n + t, over the query heads
  *                      of g, of exp(q.k_j/sqrt(d) - lse[b][t][h]),
  * with weight taken as 0 and pos[b][g][j] set to n_seen[b] - (L - j) for the new
- * rows j >= L - n.  A row whose lse is -inf adds nothing.
+ * rows j >= L - n.  A row whose lse is -inf adds nothing, one whose lse is NaN
+ * makes the weights that it counts in NaN (which dustin_evict flags).
  *   q, lse         of the attention call that verified the block
  *   n_seen         device int32 [B]: tokens the sequence has had so far, the new
  *                  ones included (n_seen[b] >= seq_len[b]; more once rows were evicted)
@@ -344,9 +348,21 @@ int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const f
  * ascending, take the kept rows at or beyond k, ascending -- K and V rows,
  * weight and pos -- so that as few rows move as can; rows at or beyond k keep
  * their old contents.  Then seq_len[b] = min(seq_len[b], k).  A NaN or negative
- * weight ranks as 0 and sets DUSTIN_DEV_NAN.  Every buffer may be given once
- * only (DUSTIN_EINVAL); a sequence whose seq_len is outside [0, Lcap] is left
- * untouched and flagged (DUSTIN_DEV_SEQLEN). */
+ * weight of a row that is not protected ranks as 0 and sets DUSTIN_DEV_NAN.  Every
+ * buffer may be given once only (DUSTIN_EINVAL); a sequence whose seq_len is
+ * outside [0, Lcap] is left untouched and flagged (DUSTIN_DEV_SEQLEN).
+ *
+ * More than DUSTIN_MAX_LAYERS layers take a call per group of layers, each with
+ * the lengths from before: give every call but the last a copy of seq_len.  A
+ * group that is given lengths already lowered to k moves nothing and keeps its
+ * first k rows whatever their weight, and no flag tells.
+ *
+ * Afterwards row j of a cache is no longer position j, and not the same position
+ * in every KV head; pos tells which.  What takes the order of rows for that of
+ * positions, or rows of all heads together, is not for such caches:
+ * dustin_window_attn, dustin_score, dustin_select and the rows it selects.  The
+ * rest is: the own part of dustin_prefix_attn, dense_verify_attn,
+ * dustin_kv_append, dustin_accumulate and dustin_evict again. */
 int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, const dustin_kv* v,
                  float* const* weight, int32_t* const* pos, const int32_t* n_seen, int32_t* seq_len,
                  void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -746,5 +746,7 @@ def dustin_accumulate(p: Params, q, lse, k, n_new, seq_len, n_seen, weight, pos,
 
 def dustin_evict(p: Params, ks, vs, weights, poss, n_seen, seq_len, ws=None, stream=None):
     """Evicts, in place, down to ``p.k`` rows per layer, sequence and KV head,
-    keeping sinks, the recent window and the largest weights."""
+    keeping sinks, the recent window and the largest weights, and lowers
+    ``seq_len``.  More than ``MAX_LAYERS`` layers go in groups, every group but
+    the last with a copy of ``seq_len``: lengths already lowered move nothing."""
     return EvictCall(p, ks, vs, weights, poss, n_seen, seq_len, ws, stream)(stream)

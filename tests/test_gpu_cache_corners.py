@@ -1,6 +1,7 @@
 """Corners of the cache operators."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -10,6 +11,8 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU too
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import sparse_kv_verify_gb300 as dk  # noqa: E402
+from oracle import cache_oracle as O  # noqa: E402
+from synth import to_bits  # noqa: E402
 
 from _cache_cases import Block, assert_attended, attend64, i32, logit_error, normal  # noqa: E402
 
@@ -238,3 +241,47 @@ def test_query_rows_whole_and_split(T, hq, hkv, d, lens):
     o, lse = dk.dustin_prefix_attn(p, x.q, pk, pv, i32([P]), x.k, x.v, x.kb, x.vb, x.seq)
     check_rows(x, o, lse, lambda b, g: (torch.cat([pk[0, g], own(x.k, x.kb, b, g)]),
                                         torch.cat([pv[0, g], own(x.v, x.vb, b, g)])), 0, 1 << 30)
+
+
+# ------------------------------------------------ more layers than a call takes
+
+
+def test_evict_in_groups_of_layers():
+    """Twenty layers in two calls, the first with a copy of the lengths."""
+    B, hkv, d, cap, n, k, layers = 2, 2, 64, 160, 140, 100, 20
+    ks, vs = ([normal(50 + 2 * l + x, B, hkv, cap, d) for l in range(layers)] for x in (0, 1))
+    g = torch.Generator("cuda").manual_seed(5)
+    w = [torch.rand((B, hkv, cap), device="cuda", generator=g) for _ in range(layers)]
+    pos = [torch.arange(cap, dtype=torch.int32, device="cuda").expand(B, hkv, cap).contiguous() for _ in range(layers)]
+    before = [[to_bits(a), to_bits(b), c.cpu().numpy(), e.cpu().numpy()] for a, b, c, e in zip(ks, vs, w, pos)]
+    lens = [n, 120]
+    seq, seen = i32(lens), i32(lens)
+    p = dk.Params(B, cap, 0, 2, 10, 0, k)
+    first = seq.clone()
+    for at, lengths in ((slice(0, 16), first), (slice(16, layers), seq)):
+        dk.dustin_evict(p, ks[at], vs[at], w[at], pos[at], seen, lengths)
+    assert seq.tolist() == first.tolist() == [k, k]
+    for l, old in enumerate(before):
+        ref = O.evict(*old, lens, np.asarray(lens), k, 2, 10)
+        for a, r in zip((to_bits(ks[l]), to_bits(vs[l]), w[l].cpu().numpy(), pos[l].cpu().numpy()), ref):
+            assert np.array_equal(a, r), l
+
+
+def test_accumulate_nan_lse_shows_in_the_rows_that_it_counts_in():
+    """A query that is not finite (lse NaN) is not passed over like an empty one."""
+    L, T, n = 200, 3, 2
+    x = Block([L, L], T, 8, 2, 64, seed=36)
+    p = params(x)
+    seen, new = i32([L, L]), i32([n, n])
+    runs = []
+    for bad in (False, True):
+        w, pos = torch.ones((2, 2, x.cap), device="cuda"), torch.zeros((2, 2, x.cap), dtype=torch.int32, device="cuda")
+        lse = torch.full((2, T, 8), 5.0, device="cuda")
+        if bad:
+            lse[1, 0, 6] = float("nan")
+        dk.dustin_accumulate(p, x.q, lse, x.k, new, x.seq, seen, w, pos)
+        runs.append(w)
+    # query 0 of sequence 1 sits at row L - n; head 6 is KV head 1's
+    assert runs[1][1, 1, :L - n + 1].isnan().all()
+    runs[1][1, 1, :L - n + 1] = runs[0][1, 1, :L - n + 1]
+    assert torch.equal(runs[0], runs[1])
