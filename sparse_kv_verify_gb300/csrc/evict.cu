@@ -10,13 +10,14 @@
 // Two launches:
 //   select  one cluster of CTAs per unit.  Every row's 32-bit key (all ones for
 //           a protected row, else the weight's bits, which order like the
-//           weight) is formed once and kept in shared memory; three histogram
-//           passes of 12, 10 and 10 bits, summed over the cluster's CTAs, give
-//           the k-th largest key and how many rows that equal it stay.  With
-//           kept(j) = rows kept before row j, a hole j < k is the
-//           (j - kept(j))-th and a mover j >= k the (kept(j) - kept(k))-th of
-//           its list, so both lists are written from one ordered count of keys
-//           above and equal to the threshold.
+//           weight) is formed once and kept in shared memory (a CTA with more than
+//           kKeysMax rows forms it anew in every pass); three histogram passes of
+//           12, 10 and 10 bits, summed over the cluster's CTAs, give the k-th
+//           largest key and how many rows that equal it stay.  With kept(j) =
+//           rows kept before row j, a hole j < k is the (j - kept(j))-th and a
+//           mover j >= k the (kept(j) - kept(k))-th of its list, so both lists
+//           are written from one ordered count of keys above and equal to the
+//           threshold.
 //   move    bound by the bytes of the rows: every warp moves four rows at a
 //           time, a row's K and V by half a warp each, loads before stores.
 //           It also sets the lengths, which the first launch read.
