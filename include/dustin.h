@@ -21,7 +21,8 @@
  * Beside them, not in the pages: attention through a sliding window with sinks
  * (dustin_window_attn) and behind a prefix that a batch shares
  * (dustin_prefix_attn), and caches bounded by accumulated attention weight
- * (dustin_accumulate, dustin_evict).
+ * (dustin_accumulate, dustin_evict); and a cache in pages for ragged batches
+ * (dustin_page_map, dustin_norm_rope, dustin_paged_attn).
  *
  * Conventions (all calls):
  *  - The caller owns every buffer.  Pointers named "device" are CUDA device
@@ -66,6 +67,7 @@ typedef enum {
 #define DUSTIN_DEV_APPEND  4   /* n_accept outside [0, gamma+1] or append past Lcap (skipped) */
 #define DUSTIN_DEV_TIMEOUT 8   /* a bounded wait on an on-chip barrier gave up */
 #define DUSTIN_DEV_SEQLEN 16   /* seq_len[b] outside [0, Lcap] (sequence skipped) */
+#define DUSTIN_DEV_PAGES  32   /* a pool with too few free pages, or whose counts are inconsistent */
 
 /* Limits. */
 #define DUSTIN_MAX_SRH 32           /* SRH entries per call */
@@ -74,6 +76,8 @@ typedef enum {
 #define DUSTIN_MAX_QROWS 128        /* (gamma+1) * (Hq/Hkv) verify query rows per KV head */
 #define DUSTIN_MAX_BLOCK 64         /* gamma+1 draft-block rows per verify call */
 #define DUSTIN_MAX_LCAP (1 << 20)   /* positions per cache */
+#define DUSTIN_MAX_REQUESTS 8192    /* requests per paged-cache call */
+#define DUSTIN_MAX_TOKENS (1 << 20) /* packed token rows per paged-cache call */
 
 /* A bf16 KV-cache view, element (b, g, pos, j) at
  *   ptr + b*sb + g*sh + pos*sl + j          (strides in elements).
@@ -366,6 +370,137 @@ int dustin_accumulate(const dustin_params* p, int32_t hq, const void* q, const f
 int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, const dustin_kv* v,
                  float* const* weight, int32_t* const* pos, const int32_t* n_seen, int32_t* seq_len,
                  void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- paged cache ------------------------------------------------------------
+ * A cache in pages for a server whose batch mixes requests of any length, with
+ * one or many new tokens each: single tokens, draft blocks, chunks of prompts.
+ * The pages have no counterpart.  A pass, all of it on the GPU and without a host
+ * copy of any length, so that it can be captured into one graph:
+ *   dustin_page_map   pages for the new tokens, where each of them goes
+ *   per layer:        dustin_norm_rope (rotates, writes K and V) -> dustin_paged_attn
+ *   seq_len[b] += the tokens that stay; the next dustin_page_map takes back the
+ *                     pages that rejected tokens and finished requests held.
+ * The new tokens of all requests are packed: request b has rows cu[b] ..
+ * cu[b+1]-1 of the N rows of every token array; rows at or beyond cu[B] belong to
+ * no request (padding of a captured batch).  One table serves all layers, each
+ * of which has a cache of its own. */
+
+/* A pool of n_pages pages of `page` rows: element (id, g, r, j) at
+ *   ptr + id*sp + g*sh + r*sl + j         (strides in elements).
+ * d is 64 or 128, rows are contiguous, ptr is 16-byte aligned, sp, sh and sl are
+ * positive multiples of 8, and n_pages * page < 2^31.  Row `pos` of request b is
+ * row pos % page of page table[b][pos / page]. */
+typedef struct {
+  void* ptr;
+  int32_t hkv, d;
+  int32_t n_pages, page;
+  int64_t sp, sh, sl;
+} dustin_paged_kv;
+
+/* Shape of a ragged batch. */
+typedef struct {
+  int32_t B;          /* requests, 1..DUSTIN_MAX_REQUESTS */
+  int32_t N;          /* rows of the packed token arrays, 1..DUSTIN_MAX_TOKENS */
+  int32_t max_new;    /* new tokens of one request at most, 1..DUSTIN_MAX_TOKENS */
+  int32_t max_pages;  /* entries of a request's row of the table, >= 1;
+                         max_pages * page <= DUSTIN_MAX_LCAP (DUSTIN_ERANGE) */
+} dustin_batch;
+
+/* What dustin_norm_rope does to heads. */
+typedef struct {
+  int32_t N;            /* token rows, 1..DUSTIN_MAX_TOKENS */
+  int32_t hq;           /* query heads */
+  int32_t rot;          /* rotated elements of a head, the first ones: a multiple of 16, 0..d */
+  int32_t interleaved;  /* 0: pairs (j, j + rot/2), 1: pairs (2j, 2j + 1) */
+  float eps;            /* >= 0, finite */
+} dustin_rope;
+
+/* Bytes of workspace that dustin_paged_attn needs with these arguments.
+ * dustin_page_map and dustin_norm_rope need the same call's with hq = 0.
+ * Returns 0 if the arguments are invalid. */
+size_t dustin_paged_workspace_bytes(const dustin_batch* bt, int32_t hq, int32_t hkv, int32_t d);
+
+/* Pages, block tables and slots of a batch.  Request b has seq_len[b] rows in the
+ * cache and n_new[b] new tokens, together need = ceil((seq_len + n_new) / page)
+ * pages, and holds held[b]: entries 0..held[b]-1 of its row of the table.  The
+ * pool of free pages is the stack free_list[0..*n_free).
+ *  1. A request with held > need gives back entries need..held-1 of its row: all
+ *     these pages are pushed, in the order of requests and, within one, of its row.
+ *  2. A request with held < need takes need - held pages, popped one by one into
+ *     entries held..need-1, in the same order.  From the first request that the
+ *     pool has too few pages for on, no request gets any (DUSTIN_DEV_PAGES).
+ * A request that holds the pages that it needs afterwards is served.
+ *   table      device int32 [B][max_pages], in and out; entries at or beyond
+ *              held[b] are left as they were
+ *   held       device int32 [B], in and out (not served: unchanged)
+ *   free_list  device int32 [n_pages], in and out; n_free device int32, in and out.
+ *              Entries at or beyond *n_free are left as the pushes wrote them.
+ *   cu         device int32 [B+1], out: cu[b] = min(N, sum of n_new before b)
+ *   kv_len     device int32 [B], out: seq_len + n_new, or 0 if not served
+ *   slot       device int32 [N], out: for a served request's token at position
+ *              p = seq_len + t, table[b][p / page] * page + p % page; else -1
+ *   pos        device int32 [N], out: p, also if not served; 0 for padding rows
+ * A request whose numbers are inconsistent (negative, n_new > max_new, more rows
+ * than max_pages pages hold, tokens past row N, held outside [0, max_pages]) is
+ * flagged (DUSTIN_DEV_SEQLEN), not served, and keeps its pages.  A pool whose
+ * count is outside [0, n_pages] or would pass n_pages with the pages given back
+ * is flagged (DUSTIN_DEV_PAGES) and left alone: nothing is given back or taken.
+ * A table entry outside [0, n_pages) gives slot -1 and DUSTIN_DEV_INDEX.  A page
+ * belongs to one request: tables that share pages are not for this call, which
+ * would give such a page back twice.  `page` is any positive number.  No two of
+ * the buffers may be the same (DUSTIN_EINVAL). */
+int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const int32_t* seq_len,
+                    const int32_t* n_new, int32_t* table, int32_t* held, int32_t* free_list,
+                    int32_t* n_free, int32_t* cu, int32_t* kv_len, int32_t* slot, int32_t* pos, void* ws,
+                    size_t ws_bytes, cudaStream_t stream);
+
+/* Norm of each head, position rotation and cache write of one layer's new tokens.
+ *   y = x / sqrt(mean(x^2) + eps) * w          (w NULL: y = x)
+ * for each head x of q (w = q_w) and k (w = k_w), then for each pair (a, b) of
+ * the first rot elements, the j-th one turned by t = pos[i] * inv_freq[j]:
+ *   (a cos t - b sin t, b cos t + a sin t).
+ * q goes to q_out; k and v (v as it is) go to the caches at slot[i].
+ *   q, k, v   device, bf16 rows of hq, hkv, hkv heads of d: row i at
+ *             ptr + i * stride (elements, a multiple of 8, at least the row), as the
+ *             slices of one projection's output are
+ *   q_w, k_w  device bf16 [d], 16-byte aligned, or NULL
+ *   inv_freq  device fp32 [rot/2], finite, or NULL with rot = 0
+ *   pos, slot device int32 [N].  slot -1: the row's k and v are not written (its q
+ *             is); any other value outside [0, n_pages * page) as well, with
+ *             DUSTIN_DEV_INDEX.  No slot may occur twice.
+ *   q_out     device bf16 rows of hq heads; may be q itself with the same stride
+ *   kc, vc    caches of the same hkv, d, n_pages and page; `page` is any positive
+ *             number, so that a contiguous cache [B][hkv][Lcap][d] is a pool of B
+ *             pages of Lcap rows, with slot = b * Lcap + position
+ * Everything is fp32 with one rounding at the end; turns are reduced exactly (64-bit
+ * fractions of a turn), so that far positions lose nothing. */
+int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const void* q_w, const void* k_w,
+                     const float* inv_freq, const int32_t* pos, const int32_t* slot, void* q_out,
+                     int64_t q_out_stride, dustin_paged_kv kc, dustin_paged_kv vc, void* ws,
+                     size_t ws_bytes, cudaStream_t stream);
+
+/* Attention of a ragged batch's new tokens over a paged cache that holds their own
+ * rows already.  Request b has n = cu[b+1] - cu[b] query rows; row t is at position
+ * p = kv_len[b] - n + t and sees the cache rows 0..p:
+ *   o    device bf16 [N][hq][d]: softmax(q.k/sqrt(d)) v, 0 where p < 0
+ *   lse  device fp32 [N][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf where p < 0
+ *   q    device bf16 [N][hq][d];  hq / hkv <= 128
+ *   table, cu, kv_len  of dustin_page_map (or of the caller's own)
+ * Rows at or beyond cu[B] are left as they were.  A request whose numbers are
+ * inconsistent (cu not ascending within [0, N], n > max_new, kv_len outside
+ * [0, max_pages * page]) is flagged (DUSTIN_DEV_SEQLEN) and its rows are left as
+ * they were.  A table entry that is needed and outside [0, n_pages) is flagged
+ * (DUSTIN_DEV_INDEX); its rows count as rows of zeros.  Cache rows at or beyond
+ * kv_len[b] may hold anything; keys and values below it must be finite.  A query
+ * row that is not finite and sees a key gives NaN in its own o and lse.  Softmax
+ * weights are rounded to bf16 for the product with v, each by at most 2^-8 of
+ * itself, and o once more; their sum, and so lse, takes them unrounded in fp32.
+ * `page` is 16, 32, 64 or a multiple of 128 (DUSTIN_EINVAL).  o and lse are no
+ * input's memory (DUSTIN_EINVAL). */
+int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_paged_kv kc,
+                      dustin_paged_kv vc, const int32_t* table, const int32_t* cu, const int32_t* kv_len,
+                      void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Self-test of the bounded waits (no counterpart in the pages).  Every
  * on-chip wait of the kernels above gives up after 2 s, sets

@@ -11,5 +11,7 @@ from .binding import (  # noqa: F401
     noalloc_check, wait_selftest, verify_split, split_units,
     WindowCall, PrefixCall, AccumulateCall, EvictCall, cache_workspace_bytes, dustin_window_attn,
     dustin_prefix_attn, dustin_accumulate, dustin_evict,
+    Batch, Rope, PageMapCall, NormRopeCall, PagedAttnCall, paged_view, paged_workspace_bytes, dustin_page_map,
+    dustin_norm_rope, dustin_paged_attn,
     EXPORTS, LIB_PATH,
-    DEV_INDEX, DEV_NAN, DEV_APPEND, DEV_TIMEOUT, DEV_SEQLEN)
+    DEV_INDEX, DEV_NAN, DEV_APPEND, DEV_TIMEOUT, DEV_SEQLEN, DEV_PAGES)

@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libdustin.so")
 
 STATUS = {0: "DUSTIN_OK", -1: "DUSTIN_EINVAL", -2: "DUSTIN_ERANGE", -3: "DUSTIN_ECUDA",
           -4: "DUSTIN_EDEVICE", -5: "DUSTIN_EWORKSPACE"}
-DEV_INDEX, DEV_NAN, DEV_APPEND, DEV_TIMEOUT, DEV_SEQLEN = 1, 2, 4, 8, 16
+DEV_INDEX, DEV_NAN, DEV_APPEND, DEV_TIMEOUT, DEV_SEQLEN, DEV_PAGES = 1, 2, 4, 8, 16, 32
 MAX_SRH, MAX_PAIRS, MAX_LAYERS, MAX_QROWS, MAX_LCAP = 32, 32, 16, 128, 1 << 20
 
 EXPORTS = ["dustin_version", "dustin_workspace_bytes", "dustin_workspace_init", "dustin_check",
@@ -30,7 +30,8 @@ EXPORTS = ["dustin_version", "dustin_workspace_bytes", "dustin_workspace_init", 
            "dustin_kv_append", "dustin_verify_step", "dustin_step_launches", "dustin_compact_kv",
            "dustin_score_noalloc", "dustin_score_noalloc_check", "dustin_wait_selftest",
            "dustin_verify_split", "dustin_cache_workspace_bytes", "dustin_window_attn",
-           "dustin_prefix_attn", "dustin_accumulate", "dustin_evict"]
+           "dustin_prefix_attn", "dustin_accumulate", "dustin_evict",
+           "dustin_paged_workspace_bytes", "dustin_page_map", "dustin_norm_rope", "dustin_paged_attn"]
 
 
 class DustinError(RuntimeError):
@@ -76,6 +77,20 @@ class CStep(ctypes.Structure):
                 ("n_layers", c_int32), ("layers", POINTER(CVerifyLayer)),
                 ("seq_len", c_void_p), ("importance", c_void_p), ("i_verify", c_void_p),
                 ("stage_events", POINTER(c_void_p))]
+
+
+class CPagedKV(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("hkv", c_int32), ("d", c_int32), ("n_pages", c_int32), ("page", c_int32),
+                ("sp", c_int64), ("sh", c_int64), ("sl", c_int64)]
+
+
+class CBatch(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("N", c_int32), ("max_new", c_int32), ("max_pages", c_int32)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("N", c_int32), ("hq", c_int32), ("rot", c_int32), ("interleaved", c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib_handle = None
@@ -135,9 +150,17 @@ def lib():
         L.dustin_evict.argtypes = [POINTER(CParams), c_int32, POINTER(CKV), POINTER(CKV),
                                    POINTER(c_void_p), POINTER(c_void_p), c_void_p, c_void_p, c_void_p,
                                    c_size_t, c_void_p]
+        L.dustin_paged_workspace_bytes.restype = c_size_t
+        L.dustin_paged_workspace_bytes.argtypes = [POINTER(CBatch), c_int32, c_int32, c_int32]
+        L.dustin_page_map.argtypes = [POINTER(CBatch), c_int32, c_int32] + [c_void_p] * 11 + [c_size_t, c_void_p]
+        L.dustin_norm_rope.argtypes = [POINTER(CRope), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                                       CPagedKV, CPagedKV, c_void_p, c_size_t, c_void_p]
+        L.dustin_paged_attn.argtypes = [POINTER(CBatch), c_int32, c_void_p, CPagedKV, CPagedKV, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
         L.dustin_wait_selftest.argtypes = [ctypes.c_int64, c_void_p, c_void_p, c_size_t, c_void_p]
         for f in EXPORTS[1:]:
-            if f not in ("dustin_workspace_bytes", "dustin_cache_workspace_bytes"):
+            if f not in ("dustin_workspace_bytes", "dustin_cache_workspace_bytes", "dustin_paged_workspace_bytes"):
                 getattr(L, f).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -750,3 +773,185 @@ def dustin_evict(p: Params, ks, vs, weights, poss, n_seen, seq_len, ws=None, str
     ``seq_len``.  More than ``MAX_LAYERS`` layers go in groups, every group but
     the last with a copy of ``seq_len``: lengths already lowered move nothing."""
     return EvictCall(p, ks, vs, weights, poss, n_seen, seq_len, ws, stream)(stream)
+
+
+# ------------------------------------------------------------------ paged cache
+
+
+@dataclass
+class Batch:
+    """Shape of a ragged batch: ``B`` requests, ``N`` packed token rows, at most
+    ``max_new`` new tokens and ``max_pages`` pages of one request."""
+    B: int
+    N: int
+    max_new: int
+    max_pages: int
+
+    def c(self) -> CBatch:
+        return CBatch(self.B, self.N, self.max_new, self.max_pages)
+
+
+@dataclass
+class Rope:
+    """The rotation: the first ``rot`` elements of a head in pairs (j, j + rot/2),
+    or (2j, 2j + 1) if ``interleaved``; ``eps`` of the norms."""
+    rot: int
+    interleaved: bool = False
+    eps: float = 1e-6
+
+
+def paged_view(t: torch.Tensor) -> CPagedKV:
+    """C view of a bf16 pool of pages ``[n_pages][hkv][page][d]`` (any strides
+    with contiguous rows)."""
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError("a paged cache must be [n_pages][hkv][page][d] with contiguous rows")
+    _ptr(t, torch.bfloat16, contiguous=False)
+    return CPagedKV(t.data_ptr(), t.shape[1], t.shape[3], t.shape[0], t.shape[2], *t.stride()[:3])
+
+
+def paged_workspace_bytes(bt: Batch, hq: int = 0, hkv: int = 1, d: int = 128) -> int:
+    """Workspace bytes of the paged-cache operators; ``hq`` query heads of
+    attention (0: none)."""
+    n = lib().dustin_paged_workspace_bytes(ctypes.byref(bt.c()), hq, hkv, d)
+    if n == 0:
+        raise DustinError("dustin_paged_workspace_bytes", -1)
+    return int(n)
+
+
+def _int32_out(t, n: int, device, stream, own: list):
+    """t, or a new int32 [n] of the call's own on the stream that it is for."""
+    if t is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            t = torch.empty(n, dtype=torch.int32, device=device)
+        own.append(t)
+    return t
+
+
+class PageMapCall(_CacheCall):
+    """Pre-marshalled ``dustin_page_map``; calling it returns ``(cu, kv_len, slot,
+    pos)`` (``table``, ``held``, ``free_list`` and ``n_free`` change in place)."""
+
+    def __init__(self, bt: Batch, page: int, seq_len, n_new, table, held, free_list, n_free, cu=None,
+                 kv_len=None, slot=None, pos=None, ws=None, stream=None):
+        for name, t in (("seq_len", seq_len), ("n_new", n_new), ("held", held)):
+            _shape(name, t, bt.B)
+        _shape("table", table, bt.B, bt.max_pages)
+        if free_list.dim() != 1:
+            raise ValueError("free_list must be [n_pages]")
+        _shape("n_free", n_free, 1)
+        own = []
+        outs = [_int32_out(t, n, seq_len.device, stream, own)
+                for t, n in ((cu, bt.B + 1), (kv_len, bt.B), (slot, bt.N), (pos, bt.N))]
+        for name, t, n in zip(("cu", "kv_len", "slot", "pos"), outs, (bt.B + 1, bt.B, bt.N, bt.N)):
+            _shape(name, t, n)
+        tensors = (seq_len, n_new, table, held, free_list, n_free, *outs)
+        ptrs = tuple(_ptr(t, torch.int32) for t in tensors)
+        super().__init__("dustin_page_map", bt, tensors, ws, 0 if ws is not None else paged_workspace_bytes(bt),
+                         stream, own)
+        self._args = (ctypes.byref(self._p), int(page), free_list.shape[0]) + ptrs + (self.ws.ptr, self.ws.nbytes)
+        self._result = tuple(outs)
+
+
+def _token_rows(name: str, t: torch.Tensor, N: int, heads: int, d: int):
+    """(address, row stride) of bf16 token rows [N][heads][d] whose heads are packed."""
+    _shape(name, t, N, heads, d)
+    if (heads > 1 and t.stride(1) != d) or t.stride(2) != 1:
+        raise ValueError(f"{name}: the heads of a row must be packed")
+    return _ptr(t, torch.bfloat16, contiguous=False), t.stride(0) if N > 1 else max(t.stride(0), heads * d)
+
+
+class NormRopeCall(_CacheCall):
+    """Pre-marshalled ``dustin_norm_rope``; calling it returns ``q_out`` (the caches
+    change in place)."""
+
+    class _Shape:
+        def __init__(self, *a):
+            self._a = a
+
+        def c(self) -> CRope:
+            return CRope(*self._a)
+
+    def __init__(self, r: Rope, q, k, v, q_w, k_w, inv_freq, pos, slot, kc, vc, q_out=None, ws=None,
+                 stream=None):
+        if q.dim() != 3 or kc.dim() != 4:
+            raise ValueError("q must be [N][hq][d] and the caches [n_pages][hkv][page][d]")
+        N, hq, d = q.shape
+        hkv = kc.shape[1]
+        _shape("kc", kc, kc.shape[0], hkv, kc.shape[2], d)
+        _shape("vc", vc, *kc.shape)
+        _shape("pos", pos, N)
+        _shape("slot", slot, N)
+        for name, w in (("q_w", q_w), ("k_w", k_w)):
+            if w is not None:
+                _shape(name, w, d)
+        if r.rot:
+            _shape("inv_freq", inv_freq, r.rot // 2)
+        own = []
+        if q_out is None:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                q_out = torch.empty((N, hq, d), dtype=q.dtype, device=q.device)
+            own.append(q_out)
+        bf, i32 = torch.bfloat16, torch.int32
+        opt = lambda t, dtype: None if t is None else _ptr(t, dtype)
+        args = (*_token_rows("q", q, N, hq, d), *_token_rows("k", k, N, hkv, d), *_token_rows("v", v, N, hkv, d),
+                opt(q_w, bf), opt(k_w, bf), opt(inv_freq, torch.float32), _ptr(pos, i32), _ptr(slot, i32),
+                *_token_rows("q_out", q_out, N, hq, d), paged_view(kc), paged_view(vc))
+        super().__init__("dustin_norm_rope", self._Shape(N, hq, r.rot, int(r.interleaved), r.eps),
+                         (q, k, v, q_w, k_w, inv_freq, pos, slot, kc, vc, q_out), ws,
+                         0 if ws is not None else paged_workspace_bytes(Batch(1, 1, 1, 1)), stream, own)
+        self._args = (ctypes.byref(self._p),) + args + (self.ws.ptr, self.ws.nbytes)
+        self._result = q_out
+
+
+class PagedAttnCall(_CacheCall):
+    """Pre-marshalled ``dustin_paged_attn``; calling it returns ``(o, lse)``."""
+
+    def __init__(self, bt: Batch, q, kc, vc, table, cu, kv_len, o=None, lse=None, ws=None, stream=None):
+        if q.dim() != 3 or kc.dim() != 4:
+            raise ValueError("q must be [N][hq][d] and the caches [n_pages][hkv][page][d]")
+        hq, hkv, d = q.shape[1], kc.shape[1], q.shape[2]
+        _shape("q", q, bt.N, hq, d)
+        _shape("kc", kc, kc.shape[0], hkv, kc.shape[2], d)
+        _shape("vc", vc, *kc.shape)
+        _shape("table", table, bt.B, bt.max_pages)
+        _shape("cu", cu, bt.B + 1)
+        _shape("kv_len", kv_len, bt.B)
+        own = []
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            if o is None:
+                o = torch.empty((bt.N, hq, d), dtype=q.dtype, device=q.device)
+                own.append(o)
+            if lse is None:
+                lse = torch.empty((bt.N, hq), dtype=torch.float32, device=q.device)
+                own.append(lse)
+        _shape("o", o, bt.N, hq, d)
+        _shape("lse", lse, bt.N, hq)
+        bf, i32 = torch.bfloat16, torch.int32
+        args = (hq, _ptr(q, bf), paged_view(kc), paged_view(vc), _ptr(table, i32), _ptr(cu, i32), _ptr(kv_len, i32),
+                _ptr(o, bf), _ptr(lse, torch.float32))
+        super().__init__("dustin_paged_attn", bt, (q, kc, vc, table, cu, kv_len, o, lse), ws,
+                         0 if ws is not None else paged_workspace_bytes(bt, hq, hkv, d), stream, own)
+        self._args = (ctypes.byref(self._p),) + args + (self.ws.ptr, self.ws.nbytes)
+        self._result = (o, lse)
+
+
+def dustin_page_map(bt: Batch, page, seq_len, n_new, table, held, free_list, n_free, cu=None, kv_len=None,
+                    slot=None, pos=None, ws=None, stream=None):
+    """Gives back and takes pages of the pool ``free_list[:n_free]`` so that request
+    b holds what ``seq_len[b] + n_new[b]`` rows need, in ``table[b][:held[b]]``;
+    returns ``(cu, kv_len, slot, pos)`` of the packed new tokens."""
+    return PageMapCall(bt, page, seq_len, n_new, table, held, free_list, n_free, cu, kv_len, slot, pos, ws,
+                       stream)(stream)
+
+
+def dustin_norm_rope(r: Rope, q, k, v, q_w, k_w, inv_freq, pos, slot, kc, vc, q_out=None, ws=None, stream=None):
+    """Norms and rotates each head of ``q`` and ``k`` (``[N][heads][d]``, rows of any
+    stride), writes k and v to the paged caches at ``slot``; returns ``q_out``."""
+    return NormRopeCall(r, q, k, v, q_w, k_w, inv_freq, pos, slot, kc, vc, q_out, ws, stream)(stream)
+
+
+def dustin_paged_attn(bt: Batch, q, kc, vc, table, cu, kv_len, o=None, lse=None, ws=None, stream=None):
+    """Causal attention of packed new tokens ``q [N][hq][d]`` over paged caches
+    ``[n_pages][hkv][page][d]`` that hold their own rows already; returns
+    ``(o bf16, lse fp32)``."""
+    return PagedAttnCall(bt, q, kc, vc, table, cu, kv_len, o, lse, ws, stream)(stream)

@@ -371,6 +371,68 @@ struct EvictArgs {
 };
 cudaError_t evict_launch(EvictArgs& a, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------- paged cache
+
+struct PageMapArgs {
+  int B, N, max_new, max_pages, page, n_pages;
+  const int32_t* seq_len;
+  const int32_t* n_new;
+  int32_t* table;            // [B][max_pages]
+  int32_t* held;             // [B]
+  int32_t* free_list;        // [n_pages]
+  int32_t* n_free;
+  int32_t* cu;               // [B + 1]
+  int32_t* kv_len;           // [B]
+  int32_t* slot;             // [N]
+  int32_t* pos;              // [N]
+  int* err;
+};
+cudaError_t page_map_launch(const PageMapArgs& a, cudaStream_t stream);
+
+struct RopeArgs {
+  int N, hq, hkv, rot, interleaved;
+  float eps;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t qst, kst, vst;     // rows, in elements
+  const uint16_t* q_w;       // [D], or nullptr
+  const uint16_t* k_w;
+  const float* inv_freq;     // [rot / 2]
+  const int32_t* pos;
+  const int32_t* slot;
+  uint16_t* q_out;
+  int64_t ost;
+  uint16_t* kc;
+  uint16_t* vc;
+  int64_t ksp, ksh, ksl, vsp, vsh, vsl;
+  int n_pages, page;
+  int* err;
+};
+cudaError_t rope_launch(const RopeArgs& a, int D, int num_sms, cudaStream_t stream);
+
+struct PagedArgs {
+  int B, N, hq, hkv, max_new, max_pages;
+  int page, n_pages;
+  float scale_log2;          // log2(e) / sqrt(D)
+  const uint16_t* q;         // [N][hq][D]
+  const uint16_t* k;         // pools: element (id, g, r, j) at id*sp + g*sh + r*sl + j
+  const uint16_t* v;
+  int64_t ksp, ksh, ksl, vsp, vsh, vsl;
+  const int32_t* table;      // [B][max_pages]
+  const int32_t* cu;         // [B + 1]
+  const int32_t* kv_len;     // [B]
+  uint16_t* o;               // [N][hq][D] bf16
+  float* lse;                // [N][hq], or nullptr
+  int* err;
+};
+// Whether a request's numbers are consistent; one that fails is flagged and its
+// rows are left as they were.
+__host__ __device__ inline bool paged_ok(const PagedArgs& a, int c0, int c1, int kv) {
+  return c0 >= 0 && c1 >= c0 && c1 <= a.N && c1 - c0 <= a.max_new && kv >= 0 && kv <= (long long)a.max_pages * a.page;
+}
+cudaError_t paged_launch(PagedArgs& a, int D, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------ wait self-test
 cudaError_t wait_selftest_launch(int* err, long long* waited, unsigned long long limit_ns,
                                  cudaStream_t stream);
