@@ -388,7 +388,7 @@ int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, c
 /* A pool of n_pages pages of `page` rows: element (id, g, r, j) at
  *   ptr + id*sp + g*sh + r*sl + j         (strides in elements).
  * d is 64 or 128, rows are contiguous, ptr is 16-byte aligned, sp, sh and sl are
- * positive multiples of 8, and n_pages * page < 2^31.  Row `pos` of request b is
+ * positive multiples of 8 below 2^38, and n_pages * page < 2^31.  Row `pos` of request b is
  * row pos % page of page table[b][pos / page]. */
 typedef struct {
   void* ptr;

@@ -107,6 +107,20 @@ inline bool encode_cache_map(CUtensorMap* m, const dustin_kv& v, int Lcap, int B
   return r == CUDA_SUCCESS;
 }
 
+// Query rows [rows][hq][d] as 3-D (d, hq, rows) with box (64, G, T): one load
+// brings the G heads of a KV head of T rows as rows t*G + h.
+inline bool encode_rows_map(CUtensorMap* m, const void* q, int d, int hq, int rows, int G, int T) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(hq), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(hq) * d * 2};
+  cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(T)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Verify queries [B][T][hq][d] as 3-D (d, hq, B*T) with box (64, G, T): one
 // load brings the G x T query rows of one (sequence, KV head) as rows t*G + h.
 inline bool encode_query_map(CUtensorMap* m, const void* q, int d, int hq, int BT, int G, int T) {
@@ -126,16 +140,7 @@ inline bool encode_query_map(CUtensorMap* m, const void* q, int d, int hq, int B
       *m = maps[i];
       return true;
     }
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(hq), cuuint64_t(BT)};
-  cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(hq) * d * 2};
-  cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(T)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_rows_map(m, q, d, hq, BT, G, T)) return false;
   keys[next] = Key{q, d, hq, BT, G, T};
   maps[next] = *m;
   next = (next + 1) % kSlots;
@@ -152,6 +157,20 @@ inline bool encode_prefix_map(CUtensorMap* m, const dustin_kv& v, int cap, int r
   cuuint64_t dims[4] = {64, cuuint64_t(cap), cuuint64_t(v.d / 64), cuuint64_t(v.hkv)};
   cuuint64_t strides[3] = {cuuint64_t(v.sl) * 2, 128, cuuint64_t(v.sh) * 2};
   cuuint32_t box[4] = {64, cuuint32_t(rows), cuuint32_t(v.d / 64), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// TMA map over a pool of pages: (d, page, hkv, n_pages) with box (64, rows, 1, 1):
+// one load brings 64 columns of `rows` rows of one page and KV head.
+inline bool encode_pool_map(CUtensorMap* m, const dustin_paged_kv& v, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {cuuint64_t(v.d), cuuint64_t(v.page), cuuint64_t(v.hkv), cuuint64_t(v.n_pages)};
+  cuuint64_t strides[3] = {cuuint64_t(v.sl) * 2, cuuint64_t(v.sh) * 2, cuuint64_t(v.sp) * 2};
+  cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

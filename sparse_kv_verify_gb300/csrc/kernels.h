@@ -415,17 +415,22 @@ struct PagedArgs {
   int B, N, hq, hkv, max_new, max_pages;
   int page, n_pages;
   float scale_log2;          // log2(e) / sqrt(D)
-  const uint16_t* q;         // [N][hq][D]
-  const uint16_t* k;         // pools: element (id, g, r, j) at id*sp + g*sh + r*sl + j
-  const uint16_t* v;
-  int64_t ksp, ksh, ksl, vsp, vsh, vsl;
   const int32_t* table;      // [B][max_pages]
   const int32_t* cu;         // [B + 1]
   const int32_t* kv_len;     // [B]
   uint16_t* o;               // [N][hq][D] bf16
   float* lse;                // [N][hq], or nullptr
   int* err;
+  int nt, qt;                // tokens of a row tile, and of a query load
+  int4* split;               // [kPagedGridMax] (request, KV head, pair, last CTA) of the unit that a CTA starts and
+                             // does not end, last CTA -1: none
+  float* partial;            // slots [kPagedGridMax][2][lanes][128 * (D + 2)]: O, m [128], l [128]
+  CUtensorMap qmap, kmap, vmap;
 };
+constexpr int kPagedTile = 128;      // keys, and query rows, per tile
+constexpr int kPagedGridMax = 256;   // CTAs at most
+// Whether the batch's requests have one row tile each (the shape with one lane).
+inline int paged_lanes(int hq, int hkv, int max_new) { return max_new <= kPagedTile / (hq / hkv) ? 1 : 2; }
 // Whether a request's numbers are consistent; one that fails is flagged and its
 // rows are left as they were.
 __host__ __device__ inline bool paged_ok(const PagedArgs& a, int c0, int c1, int kv) {

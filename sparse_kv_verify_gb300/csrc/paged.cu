@@ -3,97 +3,668 @@
 // o = softmax(q.k / sqrt(d)) v and lse = ln sum exp(q.k / sqrt(d)) over the cache
 // rows 0..p, row j in row j % page of page table[b][j / page].
 //
-// One warp per (token, query head): 32 keys at a time, a lane for each key's
-// score, then a lane for D / 32 columns of the output; running maximum and sum.
+// Row tiles: nt = 128 / G tokens of a request, G query heads each, are the rows
+// t * G + h of a tile (G query heads share a KV head).  A unit is (request, KV
+// head, pair of row tiles; one row tile where no request has more) and reads the
+// 128-key tiles of the rows that its last token sees; masks inside a tile are the
+// causal rule's.  How many units and tiles there are only the device knows: every
+// CTA sums the requests' tiles (one warp) and takes its equal share of the
+// flattened tiles, so that single tokens behind long contexts and chunks of
+// prompts load the SMs alike; a unit counts kExtra tiles more than it has, for
+// what its start and end cost.  K and V rows are read once per pair of row tiles.
+//
+// Roles (handing over through mbarriers):
+//   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
+//                   step's scores in registers, P (bf16) stored over them; the
+//                   reference maximum moves only when a step passes it by more
+//                   than 2^8, and then the thread rescales its row of O.  P is
+//                   rounded to bf16 for the second product; the row sum adds the
+//                   unrounded fp32 values, so lse keeps fp32 accuracy;
+//   warps 9, 11     K and V tiles into a ring of 128-row stages: a page's rows in
+//                   one tiled TMA load per 64 columns, the pages of a tile by as
+//                   many threads, half of the loads by each warp (a load takes its
+//                   warp about 70 cycles, and small pages need 32 a tile);
+//   warp 8          zeroes the rows of a V tile past the request's last one, once the
+//                   tile has landed (they may hold anything, and 0 * NaN is not 0;
+//                   what K holds there gives scores that the mask drops);
+//   warp 10         one elected thread issues the MMAs, per step i and lane a batch
+//                   O += P(i) V(i), S(i + NB) = Q K(i + NB)^T over the S and P that
+//                   the first product has read (MMAs of one thread run in the
+//                   order of issue).
+// Two row tiles: steps of 128 keys, one S buffer per lane (NB = 1); while one
+// lane's softmax works the tensor core has the other lane's products.  One row
+// tile: steps of 64 keys with two S buffers (NB = 2).
+//
+// Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
+// [256, 256 + D) and [384, 384 + D).  A segment that covers its unit writes o and
+// lse.  Otherwise its row maxima, sums and unnormalised O go to a slot of its CTA
+// (0: the unit began in an earlier CTA, 1: here), and a second kernel merges them.
 #include "common.cuh"
 #include "kernels.h"
+#include "share.cuh"
+#include "tc.cuh"
 
 namespace dustin {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int TK = kPagedTile;       // keys per tile, and query rows per row tile
+constexpr int kTailWarp = 8, kLoadWarp = 9, kMmaWarp = 10, kLoadWarp2 = 11;
+constexpr int NTH = 384;             // 168 registers a thread (a softmax thread holds a row's scores)
+constexpr int kSCol = 0, kOCol = 256;                // lane 1: + 128
 constexpr float kNaN = __builtin_nanf("");
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) paged_kernel(const __grid_constant__ PagedArgs A) {
-  __shared__ float qs[kWarps][D];
+// Tiles that a unit counts beside its own.
+constexpr int kExtra = 2;
+
+// Where this CTA's share begins: at tile i of pair p of (request b, KV head g),
+// the kExtra ones counted first.
+struct Start {
+  long long count, total;
+  int b, g, p, i;
+};
+
+template <int D, int LANES>
+struct Cfg {
+  static constexpr int nb = LANES == 2 ? 1 : 2;      // S buffers per lane, and steps per tile
+  static constexpr int step = TK / nb;               // keys per step
+  static constexpr int nst = LANES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 6 : 12);   // K or V tiles in the ring
+  static constexpr uint32_t panel = TK * 128;        // 64 columns of a K, V or Q tile
+  static constexpr uint32_t stage = (D / 64) * panel;
+  static constexpr uint32_t ring_off = LANES * stage;   // after the query tiles
+  static constexpr uint32_t bar_off = ring_off + nst * stage;
+  static constexpr uint32_t misc_off = bar_off + (3 * nst + 15) * 8;   // barriers
+  static constexpr uint32_t total = misc_off + 16 + sizeof(Start) + 1024;
+};
+
+// A row whose sum of weights is 0 sees no key (its position is before the first),
+// or every score that it sees is -inf, which is NaN like the 0 / 0 it stands for.
+__device__ __forceinline__ float row_scale(float sum, int position) {
+  return sum != 0.f ? 1.f / sum : position >= 0 ? kNaN : 0.f;   // (a NaN stays one)
+}
+__device__ __forceinline__ float row_lse(float top, float sum, int position) {
+  return sum != 0.f ? (top + log2f(sum)) * kLn2 : position >= 0 ? kNaN : -INFINITY;
+}
+
+// A request: its packed rows [c0, c0 + n), cache rows, units of a KV head.
+struct Request {
+  int c0, n, kv, pairs;
+};
+template <int LANES>
+__device__ __forceinline__ Request request_of(const PagedArgs& A, int b) {
+  Request r;
+  const int c1 = __ldg(A.cu + b + 1);
+  r.c0 = __ldg(A.cu + b);
+  r.kv = __ldg(A.kv_len + b);
+  const bool ok = paged_ok(A, r.c0, c1, r.kv);
+  r.n = ok ? c1 - r.c0 : 0;
+  r.pairs = (r.n + LANES * A.nt - 1) / (LANES * A.nt);
+  return r;
+}
+// Key tiles of the p-th unit: of the rows that its last token sees, one at least.
+template <int LANES>
+__device__ __forceinline__ int unit_tiles(const PagedArgs& A, const Request& r, int p) {
+  const int seen = r.kv - r.n + min(r.n, (p + 1) * LANES * A.nt);
+  return max(1, (seen + TK - 1) / TK);
+}
+template <int LANES>
+__device__ __forceinline__ long long head_tiles(const PagedArgs& A, const Request& r) {
+  long long all = 0;
+#pragma unroll 1
+  for (int p = 0; p < r.pairs; ++p) all += unit_tiles<LANES>(A, r, p) + kExtra;
+  return all;
+}
+
+// Walks this CTA's segments: key tiles [i0, i0 + n) of unit (b, g, p).
+template <int LANES>
+struct Walk {
+  long long left;   // counted tiles from this segment's on
+  int b, g, p, i0, n, tiles, used;
+  Request r;
+  // The segment from counted tile `at` of the unit on; one without a tile of its
+  // own can only be a share's last.
+  __device__ __forceinline__ void cut(const PagedArgs& A, int at) {
+    tiles = unit_tiles<LANES>(A, r, p);
+    used = int(left < tiles + kExtra - at ? left : tiles + kExtra - at);
+    i0 = max(0, at - kExtra);
+    n = max(0, at + used - kExtra) - i0;
+    if (n == 0) left = 0;
+  }
+  __device__ __forceinline__ void init(const PagedArgs& A, const Start& s) {
+    left = s.count;
+    b = s.b;
+    g = s.g;
+    p = s.p;
+    if (left <= 0) return;
+    r = request_of<LANES>(A, b);
+    cut(A, s.i);
+  }
+  __device__ __forceinline__ void next(const PagedArgs& A) {
+    left -= used;
+    if (left <= 0) return;
+    if (++p == r.pairs) {
+      p = 0;
+      if (++g == A.hkv) {
+        g = 0;
+        do r = request_of<LANES>(A, ++b);
+        while (r.n == 0 && b + 1 < A.B);
+      }
+    }
+    cut(A, 0);
+  }
+  // the unit's first token within the request, and whether it has a second row tile
+  __device__ __forceinline__ int first(const PagedArgs& A) const { return p * LANES * A.nt; }
+  __device__ __forceinline__ bool two(const PagedArgs& A) const { return LANES == 2 && first(A) + A.nt < r.n; }
+};
+
+template <int D, int LANES>
+__global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ PagedArgs A) {
+  using C = Cfg<D, LANES>;
+  constexpr int NST = C::nst, NB = C::nb, SK = C::step;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bar_off);
+  uint64_t* empty = full + NST;
+  uint64_t* q_full = empty + NST;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;      // [lane][buffer] a batch with an S is done
+  uint64_t* p_full = s_full + 4;       // [lane][buffer] P is stored over S
+  uint64_t* o_full = p_full + 4;       // [lane][z] the z-th of a segment's last NB batches, without an S, is done
+  uint64_t* mma_done = o_full + 4;
+  uint64_t* landed = mma_done + 1;     // [stage] the rows of a V tile that ends past the request are in
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc_off + 8);
+  Start* start = reinterpret_cast<Start*>(smem + C::misc_off + 16 - C::misc_off % 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane_id = tid & 31;
+  const int G = A.hq / A.hkv;
+  const int n_act = (A.qt * G + 31) >> 5;   // softmax warps per lane that hold rows
+  if (tid == 32) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 32 * n_act);
+      mbar_init(&o_full[x], 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * kWarps + warp, i = blockIdx.x;
-  // the request of row i: the first whose tokens end behind it
-  int lo = -1, hi = A.B;   // cu[lo + 1] <= i < cu[hi + 1], as far as cu ascends
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (A.cu[mid + 1] <= i) lo = mid;
-    else hi = mid;
-  }
-  if (i == 0 && h == 0)
-    for (int b = lane; b < A.B; b += 32)
+  if (warp == 0) {
+    const Share sh = share_of(A.B, [&](int b) { return head_tiles<LANES>(A, request_of<LANES>(A, b)) * A.hkv; });
+    if (lane_id == 0) {
+      Start s{sh.count, sh.total, sh.b, 0, 0, 0};
+      if (s.count > 0) {
+        const Request r = request_of<LANES>(A, s.b);
+        const long long per = head_tiles<LANES>(A, r);
+        s.g = int(sh.offset / per);
+        int at = int(sh.offset - s.g * per);
+        for (int n; at >= (n = unit_tiles<LANES>(A, r, s.p) + kExtra); ++s.p) at -= n;
+        s.i = at;
+      }
+      *start = s;
+    }
+  } else if (warp == 1 && blockIdx.x == 0) {
+    for (int b = lane_id; b < A.B; b += 32)
       if (!paged_ok(A, A.cu[b], A.cu[b + 1], A.kv_len[b])) flag_error(A.err, DUSTIN_DEV_SEQLEN);
-  const int b = hi;
-  if (h >= A.hq || b >= A.B) return;
-  const int c0 = A.cu[b], c1 = A.cu[b + 1], kv = A.kv_len[b];
-  if (!paged_ok(A, c0, c1, kv) || i < c0) return;
-  const int p = kv - (c1 - c0) + (i - c0), g = h / (A.hq / A.hkv);
-  constexpr int C = D / 32;
-  for (int x = lane; x < D; x += 32)
-    qs[warp][x] = __uint_as_float(uint32_t(A.q[(size_t(i) * A.hq + h) * D + x]) << 16);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[C] = {};
-  for (int j0 = 0; j0 <= p; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    int id = -1, r = 0;
-    if (j <= p) {
-      id = A.table[size_t(b) * A.max_pages + j / A.page];
-      r = j % A.page;
-      if (id < 0 || id >= A.n_pages) {
-        flag_error(A.err, DUSTIN_DEV_INDEX);
-        id = -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk<LANES> w;
+  w.init(A, *start);
+
+  if (warp < 4 * LANES) {
+    // =============================================================== softmax
+    const int ln = warp >> 2;                       // lane (row tile of the pair)
+    const int row = tid & 127;
+    if ((warp & 3) < n_act) {
+      const float scale = A.scale_log2;
+      const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+      const uint32_t s_tmem = lane_base + uint32_t(kSCol + 128 * ln), o_tmem = lane_base + uint32_t(kOCol + 128 * ln);
+      // S of the lane's J-th step completes phase J / NB of s_full[lane][J % NB], in
+      // one batch with P V of step J - NB; P V of step n - NB + z of a segment
+      // completes a phase of o_full[lane][z].  Every thread waits for every phase
+      // in turn, and the one after it needs a P that the thread stores later: no
+      // wait by parity can be lapped or pass early.
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+      };
+      auto wait_s = [&](int J) { return wait_warp(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u); };
+      int j0 = 0, segs = 0;   // steps and segments of the lane before this segment
+      auto wait_o = [&](int z) { return wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
+      bool live = true;
+      int4 split = make_int4(0, 0, 0, -1);
+      for (; live && w.left > 0; w.next(A)) {
+        if (ln == 1 && !w.two(A)) continue;
+        const int tok = w.first(A) + ln * A.nt + row / G;             // within the request
+        const bool act = row < A.qt * G && tok < w.r.n;
+        const int position = w.r.kv - w.r.n + tok;
+        const int n = NB * w.n;                     // steps
+        float mref = -INFINITY, lsum = 0.f;
+        for (int i = 0; i < n; ++i) {
+          const int nv = position + 1 - (NB * w.i0 + i) * SK;        // keys of this step that the row sees, if under SK
+          const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
+          if (!wait_s(j0 + i)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          float x[SK];
+#pragma unroll
+          for (int c = 0; c < SK; c += 64) tc_ld64(sb + uint32_t(c), reinterpret_cast<uint32_t*>(x + c));
+          if (nv < SK) {
+#pragma unroll
+            for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
+          }
+          float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int j = 4; j + 8 <= SK; j += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], fmaxf(x[j + y], x[j + 4 + y]));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], x[SK - 4 + y]);
+          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // (a row that is not in use never rescales O; its P and O are never read)
+          const float mx = act ? top * scale : -INFINITY;
+          float alpha = 1.f;
+          if (mx > mref + 8.f) {
+            alpha = fast_exp2(mref - mx);   // 0 while mref is -inf
+            mref = mx;
+            lsum *= alpha;
+          }
+          const float nb = mref == -INFINITY ? 0.f : -mref;
+          // rescale this row of O once P V of the step before is in (NB = 1: it
+          // came with S of this step; NB = 2: it comes with S of the next one, or
+          // alone after the last)
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (NB > 1 && !(i + 1 < n ? wait_s(j0 + i + 1) : wait_o(0))) {
+              live = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tc_ld32(o_tmem + uint32_t(c), o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+              tc_st32(o_tmem + uint32_t(c), o);
+            }
+          }
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int h = 0; h < SK / 32; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              float* y = x + 32 * h + j;
+              fma2(y[0], y[1], scale, nb);
+              fma2(y[2], y[3], scale, nb);
+              const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]), p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
+              add2(l0, l1, p0, p1);
+              add2(l2, l3, p2, p3);
+              pk[j / 2] = pack_bf16(p0, p1);
+              pk[j / 2 + 1] = pack_bf16(p2, p3);
+            }
+            tc_st16(sb + uint32_t(16 * h), pk);
+          }
+          tc_wait_st();
+          lsum += (l0 + l1) + (l2 + l3);
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * ln + (j0 + i) % NB]);
+        }
+        if (!live) break;
+        // --------------------------------------------------------- epilogue
+#pragma unroll
+        for (int z = 0; z < NB; ++z) live = live && wait_o(z);
+        if (!live) break;
+        j0 += n;
+        ++segs;
+        tc_fence_after();
+        const bool whole = w.n == w.tiles;
+        // (tid 0: lane 0 has a row tile in every unit)
+        if (tid == 0 && !whole && w.i0 == 0) {
+          // the CTA that has the unit's last tile, the (tiles - n)-th after this CTA's last
+          const long long ctas = start->total < gridDim.x ? start->total : gridDim.x;
+          const long long last = (blockIdx.x + 1) * start->total / ctas + (w.tiles - w.n) - 1;
+          split = make_int4(w.b, w.g, w.p, int(((last + 1) * ctas - 1) / start->total));
+        }
+        float* part = A.partial + ((size_t(blockIdx.x) * 2 + (w.i0 == 0)) * LANES + ln) * (size_t(TK) * (D + 2));
+        const size_t orow = size_t(w.r.c0 + (act ? tok : 0)) * A.hq + size_t(w.g) * G + row % G;
+        const float inv = row_scale(lsum, position);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc_ld32(o_tmem + uint32_t(c), o);   // collective: every lane loads
+          if (act && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(A.o + orow * D + c);
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                pk[z] = pack_bf16(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+              dst[y / 8] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else if (act) {
+            float4* dst = reinterpret_cast<float4*>(part + size_t(row) * D + c);
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              dst[y / 4] = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
+                                       __uint_as_float(o[y + 3]));
+          }
+        }
+        if (act) {
+          if (whole) {
+            if (A.lse) A.lse[orow] = row_lse(mref, lsum, position);
+          } else {
+            part[size_t(TK) * D + row] = mref;
+            part[size_t(TK) * D + TK + row] = lsum;
+          }
+        }
+        tc_fence_before();
       }
-      s = 0.f;
-      if (id >= 0) {
-        const uint16_t* k = A.k + id * A.ksp + g * A.ksh + r * A.ksl;
-        for (int x = 0; x < D; ++x) s = fmaf(qs[warp][x], __uint_as_float(uint32_t(k[x]) << 16), s);
-      }
-      s *= A.scale_log2;
+      if (tid == 0) A.split[blockIdx.x] = live ? split : make_int4(0, 0, 0, -1);
     }
-    float top = fmaxf(m, s);
+  } else if (warp == kLoadWarp || warp == kLoadWarp2) {
+    // ================================================================ loads
+    // (both warps follow every phase of every stage; the first alone arms them)
+    const bool lead = warp == kLoadWarp;
+    const int box = min(A.page, TK);                  // rows of a load
+    int gi = 0, st = 0, segs = 0;
+    uint32_t ph = 0;                                  // of stage st
+    uint32_t tails = 0, tail_ph = 0;                  // stages whose latest load is waited for by `landed`; its phases
+    bool live = true;
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+      return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+    };
+    for (; live && w.left > 0; w.next(A)) {
+      const int32_t* table = A.table + size_t(w.b) * A.max_pages;
+      // the page of this thread in a tile; -1: none
+      auto page_at = [&](int i) {
+        const int at = (w.i0 + i) * TK + lane_id * box;
+        if (i >= w.n || lane_id * box >= TK || at >= w.r.kv) return -1;
+        const int id = __ldg(table + at / A.page);
+        if (id >= 0 && id < A.n_pages) return id;
+        flag_error(A.err, DUSTIN_DEV_INDEX);
+        return A.n_pages;   // past the end: the load fills in zeros
+      };
+      int ahead = page_at(0);
+      // this segment's query tiles, once the last one's S MMAs have read theirs
+      if (lead) {
+        if (segs > 0 && !wait_warp(q_empty, uint32_t(segs - 1) & 1u)) break;
+        if (lane_id == 0) {
+          const bool two = w.two(A);
+          const uint32_t bytes = uint32_t(A.qt * G) * D * 2;
+          mbar_arrive_expect_tx(q_full, two ? 2 * bytes : bytes);
+          for (int ln = 0; ln < (two ? 2 : 1); ++ln)
 #pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float base = top == -INFINITY ? 0.f : top, alpha = fast_exp2(m - base), w = fast_exp2(s - base);
-    m = top;
-    float sum = w;
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sbase + uint32_t(ln) * C::stage + uint32_t(h) * C::panel, &A.qmap, h * 64, w.g * G,
+                          w.r.c0 + w.first(A) + ln * A.nt, q_full);
+        }
+        ++segs;
+      }
+      for (int i = 0; live && i < w.n; ++i) {
+        const int base = (w.i0 + i) * TK, id = ahead;
+        ahead = page_at(i + 1);
+        const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
+        const int r0 = A.page >= TK ? base % A.page : 0;
 #pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = fmaf(l, alpha, sum);
+        for (int kv = 0; kv < 2; ++kv) {              // K, then V
+          if (gi >= NST && !wait_warp(&empty[st], ph ^ 1u)) {
+            live = false;
+            break;
+          }
+          const bool tail = kv && base + TK > w.r.kv;
+          uint64_t* bar = tail ? &landed[st] : &full[st];
+          if (lead && lane_id == 0) mbar_arrive_expect_tx(bar, uint32_t(np * box) * D * 2);
+          __syncwarp();
+          const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage + uint32_t(lane_id * box) * 128;
+          const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
+          if constexpr (D == 128) {   // a panel by each warp
+            const int h = lead ? 0 : 1;
+            if (id >= 0) tma_load_4d_u32(dst + h * C::panel, map, h * 64, r0, w.g, id, bar);
+          } else {                    // every other page by each warp
+            if (id >= 0 && (lane_id & 1) == (lead ? 0 : 1)) tma_load_4d_u32(dst, map, 0, r0, w.g, id, bar);
+          }
+          if (tail) tail_ph ^= 1u << st;
+          tails = tail ? tails | 1u << st : tails & ~(1u << st);
+          ++gi;
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    // what is in flight has landed before the CTA may exit: the query tiles
+    // and the latest load of each stage
+    if (lead && lane_id == 0) {
+      if (segs > 0) mbar_drain(q_full, uint32_t(segs - 1) & 1u, A.err);
+      for (int j = gi > NST ? gi - NST : 0; j < gi; ++j) {
+        const int x = j % NST;
+        if ((tails >> x) & 1u) mbar_drain(&landed[x], ((tail_ph >> x) & 1u) ^ 1u, A.err);
+        else mbar_drain(&full[x], uint32_t(j / NST) & 1u, A.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kTailWarp) {
+    // ================================================================ tails
+    int gi = 0;
+    uint32_t tail_ph = 0;   // phases of `landed`
+    for (; w.left > 0; w.next(A)) {
+      gi += 2 * w.n;
+      const int nv = max(w.r.kv - (w.i0 + w.n - 1) * TK, 0);   // rows of the segment's last tile
+      if (nv >= TK) continue;
+      const int st = (gi - 1) % NST;
+      if (!__all_sync(0xffffffffu, mbar_wait(&landed[st], (tail_ph >> st) & 1u, A.err, abort_flag))) break;
+      tail_ph ^= 1u << st;
+      unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] *= alpha;
-    for (int x = 0; x < 32 && j0 + x <= p; ++x) {
-      const int idx = __shfl_sync(0xffffffffu, id, x), rx = __shfl_sync(0xffffffffu, r, x);
-      const float wx = bf16_round(__shfl_sync(0xffffffffu, w, x));
-      if (idx < 0) continue;
-      const uint16_t* v = A.v + idx * A.vsp + g * A.vsh + rx * A.vsl;
+      for (int h = 0; h < D / 64; ++h)
+        for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)
+          *reinterpret_cast<uint4*>(rows + h * C::panel + x * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane_id == 0) mbar_arrive(&full[st]);
+    }
+    __syncwarp();
+  } else {
+    if (warp == kMmaWarp) {
+      // ================================================================ MMAs
+      constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
+      const uint64_t q_desc = tc_desc(sbase, 16, 1024);
+      const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, 1024), v_desc = tc_desc(sbase + C::ring_off, C::panel, 1024);
+      int st = 0, segs = 0;                 // ring stage to consume next; segments
+      uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
+      bool issued = false, live = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+      };
+      // the warp runs together and one elected lane issues; branches go by votes,
+      // so that the compiler too knows the warp as converged
+      auto uni = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };
+      auto next_stage = [&] {
+        if (++st == NST) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      for (; live && uni(w.left > 0); w.next(A)) {
+        const bool two = uni(w.two(A));
+        live = wait(q_full, uint32_t(segs++) & 1u);
+        const int n = NB * w.n;
+        int sv = 0, sk = 0;                 // stages of V and of K
+        for (int i = -NB; live && uni(i < n); ++i) {
+          const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
+          const bool pv = i >= 0, s = uni(i + NB < n);
+          // (tiles come as K, V, K, V, ...: a V is next in turn when P V of its tile is)
+          if (pv && first) {
+            sv = st;
+            live = wait(&full[sv], ph);
+            next_stage();
+          }
+          if (live && s && first) {
+            sk = st;
+            live = wait(&full[sk], ph);
+            next_stage();
+          }
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(wx, __uint_as_float(uint32_t(v[lane * C + c]) << 16), o[c]);
+          for (int ln = 0; ln < LANES; ++ln) {
+            if (!live || (ln == 1 && !two)) break;
+            const int buf = NB == 1 ? 0 : i & 1;   // of step i and of step i + NB
+            if (pv) {
+              live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
+              if (!live) break;
+              pp ^= 1u << (2 * ln + buf);
+            }
+            issued = true;
+            tc_fence_after();
+            const uint32_t sp = tmem + uint32_t(kSCol + 128 * ln + buf * SK);
+            if (pv) {
+              const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+#pragma unroll
+              for (int kk = 0; kk < SK / 16; ++kk)
+                tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk * 128), kIdPV,
+                          (i > 0 || kk > 0) ? 1 : 0);
+            }
+            if (s) {
+              const uint64_t q = q_desc + uint64_t(ln) * (C::stage >> 4);
+              const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2);
+                tc_mma_ss_elect(sp, q + off, k + off, kIdS, kk > 0);
+              }
+            }
+            tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
+          }
+          if (!live) break;
+          if (pv && last) tc_commit_elect(&empty[sv]);
+          if (s && last) tc_commit_elect(&empty[sk]);
+          if (uni(i + NB + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
+        }
+      }
+      if (issued) {   // every MMA has completed before tensor memory is freed
+        tc_commit_elect(mma_done);
+        if (lane_id == 0) mbar_drain(mma_done, 0, A.err);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+// Log-sum-exp merge of the segments of the unit that CTA blockIdx.x started and did
+// not end: one thread per four output columns.
+constexpr int kMergeThreads = 256;
+
+template <int D, int LANES>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedArgs A) {
+  constexpr int RPB = kMergeThreads / (D / 4);   // rows of a block
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 sp = __ldcg(A.split + blockIdx.x);
+  const int c0 = blockIdx.x, c1 = min(sp.w, int(gridDim.x) - 1);
+  if (c1 <= c0) return;
+  const int G = A.hq / A.hkv;
+  const int x = blockIdx.y * RPB + threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
+  const int ln = x / TK, row = x % TK;
+  const Request r = request_of<LANES>(A, sp.x);
+  const int tok = (sp.z * LANES + ln) * A.nt + row / G;
+  if (row >= A.qt * G || tok >= r.n) return;
+  constexpr size_t kLane = size_t(TK) * (D + 2);
+  const float* base_o = A.partial + ln * kLane + size_t(row) * D + 4 * c4;
+  const float* base_m = A.partial + ln * kLane + size_t(TK) * D + row;
+  constexpr int kDepth = 8;   // segments whose loads are in flight
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += kDepth) {
+    float m[kDepth], l[kDepth];
+    float4 o[kDepth];
+#pragma unroll
+    for (int y = 0; y < kDepth; ++y) {
+      m[y] = -INFINITY;
+      l[y] = 0.f;
+      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + y <= c1) {
+        const size_t off = (size_t(c + y) * 2 + (c + y == c0)) * LANES * kLane;
+        m[y] = __ldcg(base_m + off);
+        l[y] = __ldcg(base_m + off + TK);
+        o[y] = __ldcg(reinterpret_cast<const float4*>(base_o + off));
+      }
+    }
+    float ref = top;
+#pragma unroll
+    for (int y = 0; y < kDepth; ++y) ref = fmaxf(ref, m[y]);
+    const float base = ref == -INFINITY ? 0.f : ref;
+    const float w0 = fast_exp2(top - base);   // 2^-inf = 0
+    top = ref;
+    sum *= w0;
+    acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
+#pragma unroll
+    for (int y = 0; y < kDepth; ++y) {
+      const float w = fast_exp2(m[y] - base);
+      sum = fmaf(l[y], w, sum);
+      acc.x = fmaf(o[y].x, w, acc.x);
+      acc.y = fmaf(o[y].y, w, acc.y);
+      acc.z = fmaf(o[y].z, w, acc.z);
+      acc.w = fmaf(o[y].w, w, acc.w);
     }
   }
-  const size_t row = size_t(i) * A.hq + h;
-  const float inv = l != 0.f ? 1.f / l : p >= 0 ? kNaN : 0.f;   // (a NaN stays one)
-#pragma unroll
-  for (int c = 0; c < C; c += 2)
-    *reinterpret_cast<uint32_t*>(A.o + row * D + lane * C + c) = pack_bf16(o[c] * inv, o[c + 1] * inv);
-  if (A.lse && lane == 0) A.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : p >= 0 ? kNaN : -INFINITY;
+  const size_t orow = size_t(r.c0 + tok) * A.hq + size_t(sp.y) * G + row % G;
+  const int position = r.kv - r.n + tok;
+  const float inv = row_scale(sum, position);
+  reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (A.lse && c4 == 0) A.lse[orow] = row_lse(top, sum, position);
+}
+
+template <int D, int LANES>
+cudaError_t launch_t(const PagedArgs& a, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D, LANES>;
+  static_assert(C::total <= 227 * 1024, "shared memory of a CTA");
+  auto kern = paged_kernel<D, LANES>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(
+      done, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::total)); });
+  if (attr != cudaSuccess) return attr;
+  const int grid = num_sms < kPagedGridMax ? num_sms : kPagedGridMax;
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(NTH), C::total, stream, a);
+  if (e != cudaSuccess) return e;
+  constexpr int RPB = kMergeThreads / (D / 4);
+  const int rows = LANES == 2 ? 2 * TK : a.qt * (a.hq / a.hkv);
+  return launch_pdl(paged_merge_kernel<D, LANES>, dim3(grid, (rows + RPB - 1) / RPB), dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace
 
-cudaError_t paged_launch(PagedArgs& a, int D, int, cudaStream_t stream) {
-  const dim3 grid(a.N, (a.hq + kWarps - 1) / kWarps);
-  return D == 128 ? launch_pdl(paged_kernel<128>, grid, dim3(32 * kWarps), 0, stream, a)
-                  : launch_pdl(paged_kernel<64>, grid, dim3(32 * kWarps), 0, stream, a);
+cudaError_t paged_launch(PagedArgs& a, int D, int num_sms, cudaStream_t stream) {
+  if (paged_lanes(a.hq, a.hkv, a.max_new) == 1)
+    return D == 128 ? launch_t<128, 1>(a, num_sms, stream) : launch_t<64, 1>(a, num_sms, stream);
+  return D == 128 ? launch_t<128, 2>(a, num_sms, stream) : launch_t<64, 2>(a, num_sms, stream);
 }
 
 }  // namespace dustin

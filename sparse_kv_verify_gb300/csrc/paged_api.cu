@@ -21,7 +21,9 @@ int batch_status(const dustin_batch* bt) {
 
 bool pool_ok(const dustin_paged_kv& v) {
   if (!v.ptr || !aligned16(v.ptr) || (v.d != 64 && v.d != 128) || v.hkv < 1 || v.n_pages < 1 || v.page < 1) return false;
-  if (v.sp <= 0 || v.sh <= 0 || v.sl < v.d || v.sp % 8 || v.sh % 8 || v.sl % 8) return false;
+  for (int64_t s : {v.sp, v.sh, v.sl})
+    if (s <= 0 || s % 8 || s >= int64_t(1) << 38) return false;   // (a tensor map's strides are below 2^40 bytes)
+  if (v.sl < v.d) return false;
   return int64_t(v.n_pages) * v.page < (int64_t(1) << 31);
 }
 bool pools_match(const dustin_paged_kv& k, const dustin_paged_kv& v) {
@@ -33,14 +35,28 @@ int attn_shape(int32_t hq, int32_t hkv, int32_t d) {
   return hq / hkv > DUSTIN_MAX_QROWS ? DUSTIN_ERANGE : DUSTIN_OK;
 }
 
+// Workspace of the attention, after the fixed part: the units that CTAs start and
+// do not end, and two segment slots for each CTA.
+struct PagedPlan {
+  size_t split_off, part_off, total;
+};
+PagedPlan paged_plan(int hq, int hkv, int d, int max_new) {
+  PagedPlan pl;
+  pl.split_off = kScratch;
+  pl.part_off = round256(pl.split_off + kPagedGridMax * sizeof(int4));
+  pl.total = pl.part_off + round256(size_t(kPagedGridMax) * 2 * paged_lanes(hq, hkv, max_new) * kPagedTile * (size_t(d) + 2) * 4);
+  return pl;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t dustin_paged_workspace_bytes(const dustin_batch* bt, int32_t hq, int32_t hkv, int32_t d) {
   if (batch_status(bt) != DUSTIN_OK) return 0;
-  if (hq != 0 && attn_shape(hq, hkv, d) != DUSTIN_OK) return 0;
-  return round256(kScratch);
+  if (hq == 0) return round256(kScratch);
+  if (attn_shape(hq, hkv, d) != DUSTIN_OK) return 0;
+  return paged_plan(hq, hkv, d, bt->max_new).total;
 }
 
 int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const int32_t* seq_len,
@@ -153,7 +169,8 @@ int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_
   if (int64_t(bt->max_pages) * kc.page > DUSTIN_MAX_LCAP) return DUSTIN_ERANGE;
   st = attn_shape(hq, kc.hkv, kc.d);
   if (st != DUSTIN_OK) return st;
-  if (!ws_ok(ws, ws_bytes, kScratch)) return DUSTIN_EWORKSPACE;
+  const PagedPlan pl = paged_plan(hq, kc.hkv, kc.d, bt->max_new);
+  if (!ws_ok(ws, ws_bytes, pl.total)) return DUSTIN_EWORKSPACE;
   PagedArgs a{};
   a.B = bt->B;
   a.N = bt->N;
@@ -164,17 +181,19 @@ int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_
   a.page = kc.page;
   a.n_pages = kc.n_pages;
   a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(kc.d)));
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(kc.ptr);
-  a.v = static_cast<const uint16_t*>(vc.ptr);
-  a.ksp = kc.sp; a.ksh = kc.sh; a.ksl = kc.sl;
-  a.vsp = vc.sp; a.vsh = vc.sh; a.vsl = vc.sl;
   a.table = table;
   a.cu = cu;
   a.kv_len = kv_len;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   a.err = err_word(ws);
+  a.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + pl.split_off);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.part_off);
+  a.nt = kPagedTile / (hq / kc.hkv);
+  a.qt = a.nt < bt->max_new ? a.nt : bt->max_new;
+  if (!encode_rows_map(&a.qmap, q, kc.d, hq, bt->N, hq / kc.hkv, a.qt)) return DUSTIN_ECUDA;
+  const int rows = kc.page < kPagedTile ? kc.page : kPagedTile;
+  if (!encode_pool_map(&a.kmap, kc, rows) || !encode_pool_map(&a.vmap, vc, rows)) return DUSTIN_ECUDA;
   const int sms = num_sms();
   if (sms < 1) return DUSTIN_ECUDA;
   return paged_launch(a, kc.d, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;

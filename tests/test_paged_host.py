@@ -127,7 +127,7 @@ def _pool(bd, **o):
 
 
 BAD_POOL = [dict(ptr=None), dict(ptr=0x10008), dict(d=96), dict(hkv=0), dict(n_pages=0), dict(page=0), dict(page=-16),
-            dict(sl=64), dict(sl=132), dict(sp=0), dict(sh=-128), dict(sh=2052), dict(n_pages=1 << 27)]
+            dict(sl=64), dict(sl=132), dict(sp=0), dict(sh=-128), dict(sh=2052), dict(n_pages=1 << 27), dict(sp=1 << 38)]
 
 
 def test_page_map_refusals(L):
