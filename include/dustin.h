@@ -388,7 +388,7 @@ int dustin_evict(const dustin_params* p, int32_t n_layers, const dustin_kv* k, c
 /* A pool of n_pages pages of `page` rows: element (id, g, r, j) at
  *   ptr + id*sp + g*sh + r*sl + j         (strides in elements).
  * d is 64 or 128, rows are contiguous, ptr is 16-byte aligned, sp, sh and sl are
- * positive multiples of 8 below 2^38, and n_pages * page < 2^31.  Row `pos` of request b is
+ * positive multiples of 8 below 2^35, and n_pages * page < 2^31.  Row `pos` of request b is
  * row pos % page of page table[b][pos / page]. */
 typedef struct {
   void* ptr;
@@ -483,7 +483,7 @@ int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, cons
 /* Attention of a ragged batch's new tokens over a paged cache that holds their own
  * rows already.  Request b has n = cu[b+1] - cu[b] query rows; row t is at position
  * p = kv_len[b] - n + t and sees the cache rows 0..p:
- *   o    device bf16 [N][hq][d]: softmax(q.k/sqrt(d)) v, 0 where p < 0
+ *   o    device bf16 [N][hq][d], 32-byte aligned: softmax(q.k/sqrt(d)) v, 0 where p < 0
  *   lse  device fp32 [N][hq], or NULL: ln sum exp(q.k/sqrt(d)), -inf where p < 0
  *   q    device bf16 [N][hq][d];  hq / hkv <= 128
  *   table, cu, kv_len  of dustin_page_map (or of the caller's own)

@@ -163,16 +163,41 @@ inline bool encode_prefix_map(CUtensorMap* m, const dustin_kv& v, int cap, int r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// TMA map over a pool of pages: (d, page, hkv, n_pages) with box (64, rows, 1, 1):
-// one load brings 64 columns of `rows` rows of one page and KV head.
-inline bool encode_pool_map(CUtensorMap* m, const dustin_paged_kv& v, int rows) {
+// TMA map over a pool of pages that brings `rows` rows of one page and KV head in
+// one load, as groups of 8 rows: (64 columns, 8 rows, 64-column panels, groups,
+// pages).  A KV head is a step of the panels (heads packed in a row) or of the
+// groups (heads packed in a page): *panels, *groups; false where it is neither.
+inline bool pool_steps(const dustin_paged_kv& v, int* panels, int* groups) {
+  *panels = *groups = 0;
+  if (v.hkv == 1) return true;
+  if (v.sh == int64_t(v.page) * v.sl) *groups = v.page / 8;
+  else if (v.sh == v.d) *panels = v.d / 64;
+  else return false;
+  return true;
+}
+// merged = false: 64 columns, (d, 8 rows, groups, KV heads, pages) instead, which
+// any strides allow.  Its coordinates are in the same places but for the fourth,
+// the KV head.
+inline bool encode_pool_map(CUtensorMap* m, const dustin_paged_kv& v, int rows, bool merged) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[4] = {cuuint64_t(v.d), cuuint64_t(v.page), cuuint64_t(v.hkv), cuuint64_t(v.n_pages)};
-  cuuint64_t strides[3] = {cuuint64_t(v.sl) * 2, cuuint64_t(v.sh) * 2, cuuint64_t(v.sp) * 2};
-  cuuint32_t box[4] = {64, cuuint32_t(rows), 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  int panels = 0, groups = 0;
+  pool_steps(v, &panels, &groups);
+  const cuuint64_t P = v.d / 64, R = v.page / 8, H = v.hkv;
+  cuuint64_t dims[5] = {64, 8, panels ? P * H : P, groups ? R * H : R, cuuint64_t(v.n_pages)};
+  cuuint64_t strides[4] = {cuuint64_t(v.sl) * 2, 128, cuuint64_t(v.sl) * 16, cuuint64_t(v.sp) * 2};
+  cuuint32_t box[5] = {64, 8, cuuint32_t(P), cuuint32_t(rows / 8), 1};
+  if (!merged) {
+    dims[0] = cuuint64_t(v.d);
+    dims[2] = R;
+    dims[3] = H;
+    strides[1] = cuuint64_t(v.sl) * 16;
+    strides[2] = cuuint64_t(v.sh) * 2;
+    box[2] = cuuint32_t(rows / 8);
+    box[3] = 1;
+  }
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -8,10 +8,9 @@
 // head, pair of row tiles; one row tile where no request has more) and reads the
 // 128-key tiles of the rows that its last token sees; masks inside a tile are the
 // causal rule's.  How many units and tiles there are only the device knows: every
-// CTA sums the requests' tiles (one warp) and takes its equal share of the
+// CTA sums the requests' costs (one warp) and takes its equal share of the
 // flattened tiles, so that single tokens behind long contexts and chunks of
-// prompts load the SMs alike; a unit counts kExtra tiles more than it has, for
-// what its start and end cost.  K and V rows are read once per pair of row tiles.
+// prompts load the SMs alike.  K and V rows are read once per pair of row tiles.
 //
 // Roles (handing over through mbarriers):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
@@ -20,10 +19,13 @@
 //                   than 2^8, and then the thread rescales its row of O.  P is
 //                   rounded to bf16 for the second product; the row sum adds the
 //                   unrounded fp32 values, so lse keeps fp32 accuracy;
-//   warps 9, 11     K and V tiles into a ring of 128-row stages: a page's rows in
-//                   one tiled TMA load per 64 columns, the pages of a tile by as
-//                   many threads, half of the loads by each warp (a load takes its
-//                   warp about 70 cycles, and small pages need 32 a tile);
+//   warps 9, 11     K and V tiles into a ring of 128-row stages, a page's rows in one
+//                   tiled TMA load, the pages of a tile by as many threads, half
+//                   of them by each warp (a load takes about 95 cycles, however
+//                   small).  A stage holds groups of 8 rows one after another, a
+//                   group as its 64-column panels of 8 swizzled rows; pools whose
+//                   strides keep a load from more than 64 columns have a load and
+//                   a run of groups per panel instead;
 //   warp 8          zeroes the rows of a V tile past the request's last one, once the
 //                   tile has landed (they may hold anything, and 0 * NaN is not 0;
 //                   what K holds there gives scores that the mask drops);
@@ -31,17 +33,21 @@
 //                   O += P(i) V(i), S(i + NB) = Q K(i + NB)^T over the S and P that
 //                   the first product has read (MMAs of one thread run in the
 //                   order of issue).
-// Two row tiles: steps of 128 keys, one S buffer per lane (NB = 1); while one
-// lane's softmax works the tensor core has the other lane's products.  One row
-// tile: steps of 64 keys with two S buffers (NB = 2).
+// Batches whose requests may have two row tiles: steps of 128 keys, one S buffer
+// per lane (NB = 1); while one lane's softmax works the tensor core has the other
+// lane's products.  A unit with one row tile (single tokens beside a chunk) gives
+// every other key tile to lane 1, and lane 0 adds both lanes up at its end.
+// Batches of one row tile each: one lane, steps of 64 keys with two S buffers
+// (NB = 2).
 //
 // Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
 // [256, 256 + D) and [384, 384 + D).  A segment that covers its unit writes o and
 // lse.  Otherwise its row maxima, sums and unnormalised O go to a slot of its CTA
 // (0: the unit began in an earlier CTA, 1: here), and a second kernel merges them.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
-#include "share.cuh"
 #include "tc.cuh"
 
 namespace dustin {
@@ -54,14 +60,19 @@ constexpr int NTH = 384;             // 168 registers a thread (a softmax thread
 constexpr int kSCol = 0, kOCol = 256;                // lane 1: + 128
 constexpr float kNaN = __builtin_nanf("");
 
-// Tiles that a unit counts beside its own.
-constexpr int kExtra = 2;
+// The cost of a unit: kTile for each key tile (two lanes' products; or one row
+// tile's, whose time is its bytes'), and for its start and end kExtra.
+template <int LANES>
+struct Cost {
+  static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 4 : 3; }
+  static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 12 : 8; }
+  static constexpr int least = tile(LANES == 2);   // of a share, so that a CTA inside a unit has a tile
+};
 
-// Where this CTA's share begins: at tile i of pair p of (request b, KV head g),
-// the kExtra ones counted first.
+// Where this CTA's share begins: at cost `at` of pair p of (request b, KV head g).
 struct Start {
   long long count, total;
-  int b, g, p, i;
+  int b, g, p, at;
 };
 
 template <int D, int LANES>
@@ -73,8 +84,8 @@ struct Cfg {
   static constexpr uint32_t stage = (D / 64) * panel;
   static constexpr uint32_t ring_off = LANES * stage;   // after the query tiles
   static constexpr uint32_t bar_off = ring_off + nst * stage;
-  static constexpr uint32_t misc_off = bar_off + (3 * nst + 15) * 8;   // barriers
-  static constexpr uint32_t total = misc_off + 16 + sizeof(Start) + 1024;
+  static constexpr uint32_t misc_off = bar_off + (3 * nst + 17) * 8;   // barriers
+  static constexpr uint32_t total = misc_off + 16 + sizeof(Start) + (LANES == 2 ? TK * 8 : 0) + 1024;
 };
 
 // A row whose sum of weights is 0 sees no key (its position is before the first),
@@ -108,26 +119,145 @@ __device__ __forceinline__ int unit_tiles(const PagedArgs& A, const Request& r, 
   return max(1, (seen + TK - 1) / TK);
 }
 template <int LANES>
-__device__ __forceinline__ long long head_tiles(const PagedArgs& A, const Request& r) {
+__device__ __forceinline__ bool unit_two(const PagedArgs& A, const Request& r, int p) {
+  return LANES == 2 && (2 * p + 1) * A.nt < r.n;
+}
+template <int LANES>
+__device__ __forceinline__ int unit_cost(const PagedArgs& A, const Request& r, int p) {
+  const bool two = unit_two<LANES>(A, r, p);
+  return unit_tiles<LANES>(A, r, p) * Cost<LANES>::tile(two) + Cost<LANES>::extra(two);
+}
+// All units of a KV head, by one thread: few of them.
+template <int LANES>
+__device__ __forceinline__ long long head_cost(const PagedArgs& A, const Request& r) {
   long long all = 0;
 #pragma unroll 1
-  for (int p = 0; p < r.pairs; ++p) all += unit_tiles<LANES>(A, r, p) + kExtra;
+  for (int p = 0; p < r.pairs; ++p) all += unit_cost<LANES>(A, r, p);
   return all;
+}
+constexpr int kFewPairs = 4;
+// The same by a whole warp, of a request that all its threads have.
+template <int LANES>
+__device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Request& r) {
+  if (r.pairs <= kFewPairs) return head_cost<LANES>(A, r);
+  long long all = 0;
+#pragma unroll 1
+  for (int p = threadIdx.x & 31; p < r.pairs; p += 32) all += unit_cost<LANES>(A, r, p);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+  return all;
+}
+
+// CTAs that get a share of the batch's cost, each `least` of it at least.
+template <int LANES>
+__device__ __forceinline__ long long share_ctas(long long total) {
+  const long long runs = max(total / Cost<LANES>::least, total > 0 ? 1LL : 0LL);
+  return runs < gridDim.x ? runs : gridDim.x;
+}
+
+// Called by one whole warp: this CTA's equal run of the batch's cost.  Each lane
+// sums a run of neighbouring requests, those of many units together with the
+// others; one scan over the lanes finds the one whose run holds this CTA's first
+// tile.
+template <int LANES>
+__device__ __forceinline__ Start start_of(const PagedArgs& A) {
+  const int lane = threadIdx.x & 31;
+  const int per = (A.B + 31) / 32, b0 = lane * per;
+  long long mine = 0;
+  for (int k = 0; k < per; ++k) {   // the lanes' k-th requests
+    Request r{0, 0, 0, 0};
+    if (b0 + k < A.B) r = request_of<LANES>(A, b0 + k);
+    if (r.pairs <= kFewPairs) mine += head_cost<LANES>(A, r) * A.hkv;
+    for (uint32_t many = __ballot_sync(0xffffffffu, r.pairs > kFewPairs); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const Request x{0, __shfl_sync(0xffffffffu, r.n, src), __shfl_sync(0xffffffffu, r.kv, src),
+                      __shfl_sync(0xffffffffu, r.pairs, src)};
+      const long long all = head_cost_warp<LANES>(A, x) * A.hkv;
+      if (lane == src) mine += all;
+    }
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, x);
+    if (lane >= x) inc += y;
+  }
+  Start s{0, __shfl_sync(0xffffffffu, inc, 31), 0, 0, 0, 0};
+  const long long ctas = share_ctas<LANES>(s.total);
+  if (blockIdx.x >= ctas) return s;
+  const long long t0 = blockIdx.x * s.total / ctas;
+  s.count = (blockIdx.x + 1) * s.total / ctas - t0;
+  // the lane whose requests hold t0, then the request, the KV head and the unit
+  const int src = __ffs(__ballot_sync(0xffffffffu, t0 < inc)) - 1;
+  long long at = t0 - __shfl_sync(0xffffffffu, inc - mine, src), head = 0;
+  s.b = src * per;
+  for (;; ++s.b) {
+    const Request r = request_of<LANES>(A, s.b);
+    head = head_cost_warp<LANES>(A, r);
+    if (at < head * A.hkv || s.b + 1 == A.B) break;
+    at -= head * A.hkv;
+  }
+  s.g = int(at / head);
+  at -= s.g * head;
+  const Request r = request_of<LANES>(A, s.b);
+  for (; s.p < r.pairs; s.p += 32) {
+    const int p = s.p + lane;
+    const int cost = p < r.pairs ? unit_cost<LANES>(A, r, p) : 0;
+    long long upto = cost;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, at < upto);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      s.p += src;
+      s.at = int(at - __shfl_sync(0xffffffffu, upto - cost, src));
+      break;
+    }
+    at -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return s;
+}
+
+// 32 bytes to global memory in one instruction: a thread stores to a row of its own,
+// so that each store is a sector, and half as many pass the load-store unit.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Groups of 8 rows (all columns, or 64) of a page: coordinates (x, row 0 of a
+// group, c2, c3, page).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int c2, int c3, int page,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(c2), "r"(c3), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // Walks this CTA's segments: key tiles [i0, i0 + n) of unit (b, g, p).
 template <int LANES>
 struct Walk {
-  long long left;   // counted tiles from this segment's on
-  int b, g, p, i0, n, tiles, used;
+  long long left;   // cost from this segment's on
+  int b, g, p, at, i0, n, tiles, used;
+  bool two;         // the unit has a second row tile
   Request r;
-  // The segment from counted tile `at` of the unit on; one without a tile of its
-  // own can only be a share's last.
-  __device__ __forceinline__ void cut(const PagedArgs& A, int at) {
+  // The segment from cost `at` of the unit on.  The extra cost comes first; a
+  // tile belongs to the share that its cost ends in.  A segment without a tile can
+  // only be a share's last, as a share is no less than a tile.
+  __device__ __forceinline__ void cut(const PagedArgs& A, int from) {
+    at = from;
+    two = unit_two<LANES>(A, r, p);
     tiles = unit_tiles<LANES>(A, r, p);
-    used = int(left < tiles + kExtra - at ? left : tiles + kExtra - at);
-    i0 = max(0, at - kExtra);
-    n = max(0, at + used - kExtra) - i0;
+    const int extra = Cost<LANES>::extra(two), tile = Cost<LANES>::tile(two), all = tiles * tile + extra - at;
+    used = int(left < all ? left : all);
+    i0 = max(0, at - extra) / tile;
+    n = max(0, at + used - extra) / tile - i0;
     if (n == 0) left = 0;
   }
   __device__ __forceinline__ void init(const PagedArgs& A, const Start& s) {
@@ -137,7 +267,7 @@ struct Walk {
     p = s.p;
     if (left <= 0) return;
     r = request_of<LANES>(A, b);
-    cut(A, s.i);
+    cut(A, s.at);
   }
   __device__ __forceinline__ void next(const PagedArgs& A) {
     left -= used;
@@ -152,9 +282,8 @@ struct Walk {
     }
     cut(A, 0);
   }
-  // the unit's first token within the request, and whether it has a second row tile
+  // the unit's first token within the request
   __device__ __forceinline__ int first(const PagedArgs& A) const { return p * LANES * A.nt; }
-  __device__ __forceinline__ bool two(const PagedArgs& A) const { return LANES == 2 && first(A) + A.nt < r.n; }
 };
 
 template <int D, int LANES>
@@ -172,10 +301,14 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   uint64_t* p_full = s_full + 4;       // [lane][buffer] P is stored over S
   uint64_t* o_full = p_full + 4;       // [lane][z] the z-th of a segment's last NB batches, without an S, is done
   uint64_t* mma_done = o_full + 4;
-  uint64_t* landed = mma_done + 1;     // [stage] the rows of a V tile that ends past the request are in
+  uint64_t* pair_full = mma_done + 1;  // lane 1's part of a unit with one row tile is complete
+  uint64_t* pair_empty = pair_full + 1;   // and has been read
+  uint64_t* landed = pair_empty + 1;   // [stage] the rows of a V tile that ends past the request are in
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc_off + 8);
-  Start* start = reinterpret_cast<Start*>(smem + C::misc_off + 16 - C::misc_off % 8);
+  Start* start = reinterpret_cast<Start*>(smem + C::misc_off + 16);
+  float2* pair_ml = reinterpret_cast<float2*>(smem + C::misc_off + 16 + sizeof(Start));   // lane 1's maxima and sums
+  static_assert(C::misc_off % 8 == 0 && sizeof(Start) % 8 == 0, "alignment of the shared-memory tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane_id = tid & 31;
   const int G = A.hq / A.hkv;
@@ -194,6 +327,8 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       mbar_init(&o_full[x], 1);
     }
     mbar_init(mma_done, 1);
+    mbar_init(pair_full, 32 * n_act);
+    mbar_init(pair_empty, 32 * n_act);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -205,19 +340,8 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    const Share sh = share_of(A.B, [&](int b) { return head_tiles<LANES>(A, request_of<LANES>(A, b)) * A.hkv; });
-    if (lane_id == 0) {
-      Start s{sh.count, sh.total, sh.b, 0, 0, 0};
-      if (s.count > 0) {
-        const Request r = request_of<LANES>(A, s.b);
-        const long long per = head_tiles<LANES>(A, r);
-        s.g = int(sh.offset / per);
-        int at = int(sh.offset - s.g * per);
-        for (int n; at >= (n = unit_tiles<LANES>(A, r, s.p) + kExtra); ++s.p) at -= n;
-        s.i = at;
-      }
-      *start = s;
-    }
+    const Start s = start_of<LANES>(A);
+    if (lane_id == 0) *start = s;
   } else if (warp == 1 && blockIdx.x == 0) {
     for (int b = lane_id; b < A.B; b += 32)
       if (!paged_ok(A, A.cu[b], A.cu[b + 1], A.kv_len[b])) flag_error(A.err, DUSTIN_DEV_SEQLEN);
@@ -250,15 +374,19 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       auto wait_o = [&](int z) { return wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
       bool live = true;
       int4 split = make_int4(0, 0, 0, -1);
+      uint32_t pairs = 0;     // phase of pair_full and pair_empty
       for (; live && w.left > 0; w.next(A)) {
-        if (ln == 1 && !w.two(A)) continue;
-        const int tok = w.first(A) + ln * A.nt + row / G;             // within the request
+        // a unit with one row tile gives its odd tiles to lane 1
+        const bool halves = LANES == 2 && !w.two;
+        if (halves && ln == 1 && w.n == 1) continue;
+        const int tok = w.first(A) + (halves ? 0 : ln * A.nt) + row / G;   // within the request
         const bool act = row < A.qt * G && tok < w.r.n;
         const int position = w.r.kv - w.r.n + tok;
-        const int n = NB * w.n;                     // steps
+        const int n = halves ? (w.n + 1 - ln) / 2 : NB * w.n;              // steps
+        const int key0 = NB * w.i0 + (halves ? ln : 0), keyd = halves ? 2 : 1;
         float mref = -INFINITY, lsum = 0.f;
         for (int i = 0; i < n; ++i) {
-          const int nv = position + 1 - (NB * w.i0 + i) * SK;        // keys of this step that the row sees, if under SK
+          const int nv = position + 1 - (key0 + i * keyd) * SK;      // keys of this step that the row sees, if under SK
           const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
           if (!wait_s(j0 + i)) {
             live = false;
@@ -337,12 +465,39 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         j0 += n;
         ++segs;
         tc_fence_after();
+        // lane 1's part of a unit with one row tile goes into lane 0's (the two
+        // lanes' warps of a row reach the same tensor-memory lanes)
+        const bool join = halves && w.n > 1;
+        float w0 = 1.f, w1 = 0.f;
+        if (join) {
+          if (ln == 1) {
+            pair_ml[row] = make_float2(mref, lsum);
+            tc_fence_before();
+            mbar_arrive(pair_full);
+            live = wait_warp(pair_empty, pairs);
+            pairs ^= 1u;
+            tc_fence_after();
+            continue;
+          }
+          if (!wait_warp(pair_full, pairs)) {
+            live = false;
+            break;
+          }
+          pairs ^= 1u;
+          tc_fence_after();
+          const float2 ml = pair_ml[row];
+          const float ref = fmaxf(mref, ml.x), base = ref == -INFINITY ? 0.f : ref;
+          w0 = fast_exp2(mref - base);
+          w1 = fast_exp2(ml.x - base);
+          lsum = fmaf(lsum, w0, ml.y * w1);
+          mref = ref;
+        }
         const bool whole = w.n == w.tiles;
         // (tid 0: lane 0 has a row tile in every unit)
         if (tid == 0 && !whole && w.i0 == 0) {
-          // the CTA that has the unit's last tile, the (tiles - n)-th after this CTA's last
-          const long long ctas = start->total < gridDim.x ? start->total : gridDim.x;
-          const long long last = (blockIdx.x + 1) * start->total / ctas + (w.tiles - w.n) - 1;
+          // the CTA that the unit's cost ends in
+          const long long ctas = share_ctas<LANES>(start->total);
+          const long long last = (blockIdx.x + 1) * start->total / ctas - 1 - w.used + unit_cost<LANES>(A, w.r, w.p) - w.at;
           split = make_int4(w.b, w.g, w.p, int(((last + 1) * ctas - 1) / start->total));
         }
         float* part = A.partial + ((size_t(blockIdx.x) * 2 + (w.i0 == 0)) * LANES + ln) * (size_t(TK) * (D + 2));
@@ -352,23 +507,28 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tc_ld32(o_tmem + uint32_t(c), o);   // collective: every lane loads
-          if (act && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(A.o + orow * D + c);
+          if (join) {
+            uint32_t o1[32];
+            tc_ld32(o_tmem + uint32_t(128 + c), o1);
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                pk[z] = pack_bf16(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
-              dst[y / 8] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-          } else if (act) {
-            float4* dst = reinterpret_cast<float4*>(part + size_t(row) * D + c);
-#pragma unroll
-            for (int y = 0; y < 32; y += 4)
-              dst[y / 4] = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
-                                       __uint_as_float(o[y + 3]));
+            for (int y = 0; y < 32; ++y)
+              o[y] = __float_as_uint(fmaf(__uint_as_float(o[y]), w0, __uint_as_float(o1[y]) * w1));
           }
+          if (act && whole) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              pk[y] = pack_bf16(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) store32(A.o + orow * D + c + 16 * y, pk + 8 * y);
+          } else if (act) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) store32(part + size_t(row) * D + c + 8 * y, o + 8 * y);
+          }
+        }
+        if (join) {
+          tc_fence_before();
+          mbar_arrive(pair_empty);
         }
         if (act) {
           if (whole) {
@@ -396,21 +556,15 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
     };
     for (; live && w.left > 0; w.next(A)) {
       const int32_t* table = A.table + size_t(w.b) * A.max_pages;
-      // the page of this thread in a tile; -1: none
-      auto page_at = [&](int i) {
-        const int at = (w.i0 + i) * TK + lane_id * box;
-        if (i >= w.n || lane_id * box >= TK || at >= w.r.kv) return -1;
-        const int id = __ldg(table + at / A.page);
-        if (id >= 0 && id < A.n_pages) return id;
-        flag_error(A.err, DUSTIN_DEV_INDEX);
-        return A.n_pages;   // past the end: the load fills in zeros
-      };
+      // the table's entry for this thread in a tile, read a tile ahead of its use
+      auto needs = [&](int i) { return i < w.n && lane_id * box < TK && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
+      auto page_at = [&](int i) { return needs(i) ? __ldg(table + ((w.i0 + i) * TK + lane_id * box) / A.page) : 0; };
       int ahead = page_at(0);
       // this segment's query tiles, once the last one's S MMAs have read theirs
       if (lead) {
         if (segs > 0 && !wait_warp(q_empty, uint32_t(segs - 1) & 1u)) break;
         if (lane_id == 0) {
-          const bool two = w.two(A);
+          const bool two = w.two;
           const uint32_t bytes = uint32_t(A.qt * G) * D * 2;
           mbar_arrive_expect_tx(q_full, two ? 2 * bytes : bytes);
           for (int ln = 0; ln < (two ? 2 : 1); ++ln)
@@ -421,28 +575,44 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         }
         ++segs;
       }
-      for (int i = 0; live && i < w.n; ++i) {
-        const int base = (w.i0 + i) * TK, id = ahead;
+      // K(0), then K(i), V(i - 1) for each tile, V(n - 1): the order of their use
+      int id = -1;
+      for (int i = 0; live && i <= w.n; ++i) {
+        const int before = id;
+        id = -1;
+        if (needs(i)) {
+          id = ahead;
+          if (id < 0 || id >= A.n_pages) {
+            flag_error(A.err, DUSTIN_DEV_INDEX);
+            id = A.n_pages;   // past the end: the load fills in zeros
+          }
+        }
         ahead = page_at(i + 1);
-        const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
-        const int r0 = A.page >= TK ? base % A.page : 0;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {              // K, then V
+        for (int kv = 0; kv < 2; ++kv) {
+          if (kv ? i == 0 : i == w.n) continue;
+          const int base = (w.i0 + i - kv) * TK, page = kv ? before : id;
           if (gi >= NST && !wait_warp(&empty[st], ph ^ 1u)) {
             live = false;
             break;
           }
+          const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
+          const int r0 = A.page >= TK ? base % A.page : 0;
           const bool tail = kv && base + TK > w.r.kv;
           uint64_t* bar = tail ? &landed[st] : &full[st];
           if (lead && lane_id == 0) mbar_arrive_expect_tx(bar, uint32_t(np * box) * D * 2);
           __syncwarp();
-          const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage + uint32_t(lane_id * box) * 128;
+          const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage;
           const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
-          if constexpr (D == 128) {   // a panel by each warp
+          const int c2 = A.merged ? w.g * A.map_panels : r0 / 8, c3 = A.merged ? w.g * A.map_groups + r0 / 8 : w.g;
+          // every other page by each warp, or a panel of each page
+          if (page >= 0) {
             const int h = lead ? 0 : 1;
-            if (id >= 0) tma_load_4d_u32(dst + h * C::panel, map, h * 64, r0, w.g, id, bar);
-          } else {                    // every other page by each warp
-            if (id >= 0 && (lane_id & 1) == (lead ? 0 : 1)) tma_load_4d_u32(dst, map, 0, r0, w.g, id, bar);
+            if (D == 64 || A.merged) {
+              if ((lane_id & 1) == h) tma_load_5d(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar);
+            } else {
+              tma_load_5d(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar);
+            }
           }
           if (tail) tail_ph ^= 1u << st;
           tails = tail ? tails | 1u << st : tails & ~(1u << st);
@@ -477,10 +647,11 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       if (!__all_sync(0xffffffffu, mbar_wait(&landed[st], (tail_ph >> st) & 1u, A.err, abort_flag))) break;
       tail_ph ^= 1u << st;
       unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
+      const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)
-          *reinterpret_cast<uint4*>(rows + h * C::panel + x * 16) = make_uint4(0, 0, 0, 0);
+        for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)   // 16 bytes each, 64 of them a group
+          *reinterpret_cast<uint4*>(rows + h * panel + (x >> 6) * group + (x & 63) * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
       __syncwarp();
       if (lane_id == 0) mbar_arrive(&full[st]);
@@ -491,7 +662,9 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       // ================================================================ MMAs
       constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
       const uint64_t q_desc = tc_desc(sbase, 16, 1024);
-      const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, 1024), v_desc = tc_desc(sbase + C::ring_off, C::panel, 1024);
+      const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
+      const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, group), v_desc = tc_desc(sbase + C::ring_off, panel, group);
+      const uint32_t kpanel = panel >> 4, keys16 = group >> 3;   // per panel, and per 16 keys
       int st = 0, segs = 0;                 // ring stage to consume next; segments
       uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
       bool issued = false, live = true;
@@ -507,59 +680,77 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
           ph ^= 1u;
         }
       };
-      for (; live && uni(w.left > 0); w.next(A)) {
-        const bool two = uni(w.two(A));
-        live = wait(q_full, uint32_t(segs++) & 1u);
-        const int n = NB * w.n;
-        int sv = 0, sk = 0;                 // stages of V and of K
-        for (int i = -NB; live && uni(i < n); ++i) {
+      // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
+      auto segment = [&](auto halves, bool two) {
+        constexpr bool HALVES = decltype(halves)::value;
+        constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
+        const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
+        int sv = 0, sk = 0;                     // stages of V and of K
+        auto take = [&](int& stage) {
+          stage = st;
+          live = wait(&full[stage], ph);
+          next_stage();
+        };
+        for (int i = -lead; live && uni(i < n); ++i) {
           const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
-          const bool pv = i >= 0, s = uni(i + NB < n);
-          // (tiles come as K, V, K, V, ...: a V is next in turn when P V of its tile is)
-          if (pv && first) {
-            sv = st;
-            live = wait(&full[sv], ph);
-            next_stage();
-          }
-          if (live && s && first) {
-            sk = st;
-            live = wait(&full[sk], ph);
-            next_stage();
-          }
-#pragma unroll
-          for (int ln = 0; ln < LANES; ++ln) {
-            if (!live || (ln == 1 && !two)) break;
-            const int buf = NB == 1 ? 0 : i & 1;   // of step i and of step i + NB
+          const bool pv = i >= 0, s = uni(i + lead < n);
+          // tiles come as K(0), K(1), V(0), K(2), V(1), ...
+          if (HALVES && pv) take(sv);
+          if (live && s && first) take(sk);
+          if (live && !HALVES && pv && first) take(sv);
+          auto batch = [&](int ln, int buf) {
             if (pv) {
               live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
-              if (!live) break;
+              if (!live) return;
               pp ^= 1u << (2 * ln + buf);
             }
             issued = true;
             tc_fence_after();
             const uint32_t sp = tmem + uint32_t(kSCol + 128 * ln + buf * SK);
             if (pv) {
-              const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+              const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
+              const bool acc = i >= (HALVES ? 2 : 1);   // not the lane's first step
 #pragma unroll
               for (int kk = 0; kk < SK / 16; ++kk)
-                tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk * 128), kIdPV,
-                          (i > 0 || kk > 0) ? 1 : 0);
+                tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk) * keys16, kIdPV,
+                                (acc || kk > 0) ? 1 : 0);
             }
             if (s) {
-              const uint64_t q = q_desc + uint64_t(ln) * (C::stage >> 4);
-              const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : uint32_t(SK * 8));
+              const uint64_t q = q_desc + uint64_t(HALVES ? 0 : ln) * (C::stage >> 4);
+              const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2);
-                tc_mma_ss_elect(sp, q + off, k + off, kIdS, kk > 0);
-              }
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_ss_elect(sp, q + uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2),
+                                k + uint32_t(kk >> 2) * kpanel + uint32_t((kk & 3) * 2), kIdS, kk > 0);
             }
             tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
+          };
+          if (live) {
+            if constexpr (HALVES) {
+              if (pv || s) {
+                if (i & 1) batch(1, 0);
+                else batch(0, 0);
+              }
+            } else {
+              batch(0, NB == 1 ? 0 : i & 1);   // (step i and step i + NB have one buffer)
+              if (LANES == 2 && live && two) batch(1, 0);
+            }
           }
-          if (!live) break;
+          if (!live) return;
           if (pv && last) tc_commit_elect(&empty[sv]);
           if (s && last) tc_commit_elect(&empty[sk]);
-          if (uni(i + NB + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
+          if (uni(i + lead + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
+        }
+      };
+      for (; live && uni(w.left > 0); w.next(A)) {
+        const bool two = uni(w.two);
+        live = wait(q_full, uint32_t(segs++) & 1u);
+        if (!live) break;
+        if constexpr (LANES == 2) {
+          if (two) segment(std::false_type{}, true);
+          else segment(std::true_type{}, false);
+        } else {
+          segment(std::false_type{}, false);
         }
       }
       if (issued) {   // every MMA has completed before tensor memory is freed

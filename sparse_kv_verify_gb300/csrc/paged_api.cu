@@ -21,8 +21,8 @@ int batch_status(const dustin_batch* bt) {
 
 bool pool_ok(const dustin_paged_kv& v) {
   if (!v.ptr || !aligned16(v.ptr) || (v.d != 64 && v.d != 128) || v.hkv < 1 || v.n_pages < 1 || v.page < 1) return false;
-  for (int64_t s : {v.sp, v.sh, v.sl})
-    if (s <= 0 || s % 8 || s >= int64_t(1) << 38) return false;   // (a tensor map's strides are below 2^40 bytes)
+  for (int64_t s : {v.sp, v.sh, v.sl})   // (a tensor map's strides are below 2^40 bytes, eight rows' among them)
+    if (s <= 0 || s % 8 || s >= int64_t(1) << 35) return false;
   if (v.sl < v.d) return false;
   return int64_t(v.n_pages) * v.page < (int64_t(1) << 31);
 }
@@ -159,7 +159,7 @@ int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_
   int st = batch_status(bt);
   if (st != DUSTIN_OK) return st;
   if (!q || !table || !cu || !kv_len || !o || o == lse) return DUSTIN_EINVAL;
-  if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(table) || !aligned4(cu) || !aligned4(kv_len))
+  if (!aligned16(q) || (reinterpret_cast<uintptr_t>(o) & 31u) || !aligned4(lse) || !aligned4(table) || !aligned4(cu) || !aligned4(kv_len))
     return DUSTIN_EINVAL;
   if (!pool_ok(kc) || !pool_ok(vc) || !pools_match(kc, vc)) return DUSTIN_EINVAL;
   if (kc.page != 16 && kc.page != 32 && kc.page != 64 && kc.page % 128) return DUSTIN_EINVAL;
@@ -193,7 +193,10 @@ int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_
   a.qt = a.nt < bt->max_new ? a.nt : bt->max_new;
   if (!encode_rows_map(&a.qmap, q, kc.d, hq, bt->N, hq / kc.hkv, a.qt)) return DUSTIN_ECUDA;
   const int rows = kc.page < kPagedTile ? kc.page : kPagedTile;
-  if (!encode_pool_map(&a.kmap, kc, rows) || !encode_pool_map(&a.vmap, vc, rows)) return DUSTIN_ECUDA;
+  int panels, groups;
+  a.merged = pool_steps(kc, &a.map_panels, &a.map_groups) && pool_steps(vc, &panels, &groups) &&
+             panels == a.map_panels && groups == a.map_groups;
+  if (!encode_pool_map(&a.kmap, kc, rows, a.merged) || !encode_pool_map(&a.vmap, vc, rows, a.merged)) return DUSTIN_ECUDA;
   const int sms = num_sms();
   if (sms < 1) return DUSTIN_ECUDA;
   return paged_launch(a, kc.d, sms, stream) == cudaSuccess ? DUSTIN_OK : DUSTIN_ECUDA;

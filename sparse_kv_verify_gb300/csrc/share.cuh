@@ -7,9 +7,9 @@
 namespace dustin {
 
 // A CTA's run of flattened tiles: `count` tiles from tile `offset` of sequence
-// `b` on; `total` of all CTAs.
+// `b` on.
 struct Share {
-  long long count, offset, total;
+  long long count, offset;
   int b;
 };
 
@@ -34,7 +34,7 @@ __device__ __forceinline__ Share share_of(int B, Tiles tiles) {
   }
   const long long total = __shfl_sync(0xffffffffu, inc, 31);
   const long long ctas = total < gridDim.x ? total : gridDim.x;
-  Share s{0, 0, total, 0};
+  Share s{0, 0, 0};
   if (blockIdx.x >= ctas) return s;
   const long long t0 = blockIdx.x * total / ctas;
   s.count = (blockIdx.x + 1) * total / ctas - t0;
@@ -42,7 +42,7 @@ __device__ __forceinline__ Share share_of(int B, Tiles tiles) {
   if (here) {
     s.b = b0;
     s.offset = t0 - (inc - mine);
-    for (long long n; s.offset >= (n = tiles(s.b)); ++s.b) s.offset -= n;
+    for (int n; s.offset >= (n = tiles(s.b)); ++s.b) s.offset -= n;
   }
   const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
   s.b = __shfl_sync(0xffffffffu, s.b, src);

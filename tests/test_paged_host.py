@@ -127,7 +127,7 @@ def _pool(bd, **o):
 
 
 BAD_POOL = [dict(ptr=None), dict(ptr=0x10008), dict(d=96), dict(hkv=0), dict(n_pages=0), dict(page=0), dict(page=-16),
-            dict(sl=64), dict(sl=132), dict(sp=0), dict(sh=-128), dict(sh=2052), dict(n_pages=1 << 27), dict(sp=1 << 38)]
+            dict(sl=64), dict(sl=132), dict(sp=0), dict(sh=-128), dict(sh=2052), dict(n_pages=1 << 27), dict(sp=1 << 35)]
 
 
 def test_page_map_refusals(L):
@@ -191,7 +191,7 @@ def test_paged_attn_refusals(L):
         a.update(o)
         return lib.dustin_paged_attn(ctypes.byref(bt or _batch(bd)), *a.values(), ws, nbytes, None)
     for o in [dict(hq=0), dict(hq=60), dict(q=None), dict(q=0x1008), dict(table=None), dict(table=0x2002), dict(cu=None),
-              dict(kv=None), dict(o=None), dict(o=0x5008), dict(lse=0x6002), dict(lse=0x5000), dict(o=0x1000),
+              dict(kv=None), dict(o=None), dict(o=0x5008), dict(o=0x5010), dict(lse=0x6002), dict(lse=0x5000), dict(o=0x1000),
               dict(o=0x10000), dict(o=0x20000), dict(o=0x2000), dict(lse=0x2000), dict(lse=0x3000), dict(lse=0x4000),
               dict(vc=_pool(bd, ptr=0x20000, d=64, sl=64)), dict(vc=_pool(bd, ptr=0x20000, n_pages=3))]:
         assert call(**o) == -1, o
