@@ -10,7 +10,8 @@
 // causal rule's.  How many units and tiles there are only the device knows: every
 // CTA sums the requests' costs (one warp) and takes its equal share of the
 // flattened tiles, so that single tokens behind long contexts and chunks of
-// prompts load the SMs alike.  K and V rows are read once per pair of row tiles.
+// prompts load the SMs alike; a cut near the end of a unit is moved there.  K and V
+// rows are read once per pair of row tiles.
 //
 // Roles (handing over through mbarriers):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
@@ -67,12 +68,20 @@ struct Cost {
   static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 4 : 3; }
   static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 12 : 8; }
   static constexpr int least = tile(LANES == 2);   // of a share, so that a CTA inside a unit has a tile
+  static constexpr int snap = LANES == 1 ? 2 : 20; // a cut moves this far to the next end of a unit, to save a merge
 };
 
-// Where this CTA's share begins: at cost `at` of pair p of (request b, KV head g).
-struct Start {
-  long long count, total;
+// A cut of the flattened cost: at `at` of pair p of (request b, KV head g), all in
+// all at `pos`.
+struct Cut {
+  long long pos;
   int b, g, p, at;
+};
+// This CTA's share: from `from` to `to`, of `total` in `ctas` shares.
+struct Start {
+  Cut from;
+  long long to, total;
+  int ctas, snap;
 };
 
 template <int D, int LANES>
@@ -148,19 +157,13 @@ __device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Re
   return all;
 }
 
-// CTAs that get a share of the batch's cost, each `least` of it at least.
+// Called by one whole warp: the cut before this CTA's share (next = 0) or after it
+// (next = 1) where the batch's cost is cut into equal runs, moved to the end of a
+// unit where one is near.  Each lane sums a run of neighbouring requests, those of
+// many units together with the others; one scan over the lanes finds the one whose
+// run holds the cut.  CTAs without a share get two equal cuts.
 template <int LANES>
-__device__ __forceinline__ long long share_ctas(long long total) {
-  const long long runs = max(total / Cost<LANES>::least, total > 0 ? 1LL : 0LL);
-  return runs < gridDim.x ? runs : gridDim.x;
-}
-
-// Called by one whole warp: this CTA's equal run of the batch's cost.  Each lane
-// sums a run of neighbouring requests, those of many units together with the
-// others; one scan over the lanes finds the one whose run holds this CTA's first
-// tile.
-template <int LANES>
-__device__ __forceinline__ Start start_of(const PagedArgs& A) {
+__device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) {
   const int lane = threadIdx.x & 31;
   const int per = (A.B + 31) / 32, b0 = lane * per;
   long long mine = 0;
@@ -182,27 +185,31 @@ __device__ __forceinline__ Start start_of(const PagedArgs& A) {
     const long long y = __shfl_up_sync(0xffffffffu, inc, x);
     if (lane >= x) inc += y;
   }
-  Start s{0, __shfl_sync(0xffffffffu, inc, 31), 0, 0, 0, 0};
-  const long long ctas = share_ctas<LANES>(s.total);
-  if (blockIdx.x >= ctas) return s;
-  const long long t0 = blockIdx.x * s.total / ctas;
-  s.count = (blockIdx.x + 1) * s.total / ctas - t0;
-  // the lane whose requests hold t0, then the request, the KV head and the unit
-  const int src = __ffs(__ballot_sync(0xffffffffu, t0 < inc)) - 1;
-  long long at = t0 - __shfl_sync(0xffffffffu, inc - mine, src), head = 0;
-  s.b = src * per;
-  for (;; ++s.b) {
-    const Request r = request_of<LANES>(A, s.b);
+  const long long total = __shfl_sync(0xffffffffu, inc, 31);
+  // each share holds `least` at least
+  const long long runs = max(total / Cost<LANES>::least, total > 0 ? 1LL : 0LL);
+  const int ctas = int(runs < gridDim.x ? runs : gridDim.x), c = int(blockIdx.x) + next;
+  out.total = total;
+  out.ctas = ctas;
+  out.snap = ctas ? int(min((long long)Cost<LANES>::snap, total / ctas / 16)) : 0;
+  if (c >= ctas) return Cut{total, A.B, 0, 0, 0};
+  Cut s{c * total / ctas, 0, 0, 0, 0};
+  // the lane whose requests hold the cut, then the request, the KV head and the unit
+  const int src = __ffs(__ballot_sync(0xffffffffu, s.pos < inc)) - 1;
+  long long at = s.pos - __shfl_sync(0xffffffffu, inc - mine, src), head = 0;
+  Request r{};
+  for (s.b = src * per;; ++s.b) {
+    r = request_of<LANES>(A, s.b);
     head = head_cost_warp<LANES>(A, r);
     if (at < head * A.hkv || s.b + 1 == A.B) break;
     at -= head * A.hkv;
   }
   s.g = int(at / head);
   at -= s.g * head;
-  const Request r = request_of<LANES>(A, s.b);
+  int cost = 0;
   for (; s.p < r.pairs; s.p += 32) {
     const int p = s.p + lane;
-    const int cost = p < r.pairs ? unit_cost<LANES>(A, r, p) : 0;
+    cost = p < r.pairs ? unit_cost<LANES>(A, r, p) : 0;
     long long upto = cost;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -214,9 +221,25 @@ __device__ __forceinline__ Start start_of(const PagedArgs& A) {
       const int src = __ffs(past) - 1;
       s.p += src;
       s.at = int(at - __shfl_sync(0xffffffffu, upto - cost, src));
+      cost = __shfl_sync(0xffffffffu, cost, src);
       break;
     }
     at -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (s.at <= out.snap) {
+    s.pos -= s.at;
+    s.at = 0;
+  } else if (cost - s.at <= out.snap) {   // the next unit's start
+    s.pos += cost - s.at;
+    s.at = 0;
+    if (++s.p == r.pairs) {
+      s.p = 0;
+      if (++s.g == A.hkv) {
+        s.g = 0;
+        do ++s.b;
+        while (s.b < A.B && request_of<LANES>(A, s.b).n == 0);
+      }
+    }
   }
   return s;
 }
@@ -261,13 +284,13 @@ struct Walk {
     if (n == 0) left = 0;
   }
   __device__ __forceinline__ void init(const PagedArgs& A, const Start& s) {
-    left = s.count;
-    b = s.b;
-    g = s.g;
-    p = s.p;
+    left = s.to - s.from.pos;
+    b = s.from.b;
+    g = s.from.g;
+    p = s.from.p;
     if (left <= 0) return;
     r = request_of<LANES>(A, b);
-    cut(A, s.at);
+    cut(A, s.from.at);
   }
   __device__ __forceinline__ void next(const PagedArgs& A) {
     left -= used;
@@ -340,9 +363,19 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   pdl_launch_dependents();
   pdl_wait();
   if (warp == 0) {
-    const Start s = start_of<LANES>(A);
-    if (lane_id == 0) *start = s;
-  } else if (warp == 1 && blockIdx.x == 0) {
+    Start s;
+    s.from = cut_of<LANES>(A, 0, s);
+    if (lane_id == 0) {
+      start->from = s.from;
+      start->total = s.total;
+      start->ctas = s.ctas;
+      start->snap = s.snap;
+    }
+  } else if (warp == 1) {
+    Start s;
+    const Cut to = cut_of<LANES>(A, 1, s);
+    if (lane_id == 0) start->to = to.pos;
+  } else if (warp == 2 && blockIdx.x == 0) {
     for (int b = lane_id; b < A.B; b += 32)
       if (!paged_ok(A, A.cu[b], A.cu[b + 1], A.kv_len[b])) flag_error(A.err, DUSTIN_DEV_SEQLEN);
   }
@@ -496,9 +529,10 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         // (tid 0: lane 0 has a row tile in every unit)
         if (tid == 0 && !whole && w.i0 == 0) {
           // the CTA that the unit's cost ends in
-          const long long ctas = share_ctas<LANES>(start->total);
-          const long long last = (blockIdx.x + 1) * start->total / ctas - 1 - w.used + unit_cost<LANES>(A, w.r, w.p) - w.at;
-          split = make_int4(w.b, w.g, w.p, int(((last + 1) * ctas - 1) / start->total));
+          const long long end = start->to - w.used + unit_cost<LANES>(A, w.r, w.p) - w.at;
+          int last = int((end * start->ctas - 1) / start->total);
+          if (end - last * start->total / start->ctas <= start->snap) --last;   // (its share was moved past the unit)
+          split = make_int4(w.b, w.g, w.p, last);
         }
         float* part = A.partial + ((size_t(blockIdx.x) * 2 + (w.i0 == 0)) * LANES + ln) * (size_t(TK) * (D + 2));
         const size_t orow = size_t(w.r.c0 + (act ? tok : 0)) * A.hq + size_t(w.g) * G + row % G;
@@ -769,68 +803,94 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
 }
 
 // Log-sum-exp merge of the segments of the unit that CTA blockIdx.x started and did
-// not end: one thread per four output columns.
+// not end: one thread per four output columns of ROWS rows.  Units with two row
+// tiles are split in two or three, units of few rows among many CTAs.
 constexpr int kMergeThreads = 256;
+template <int D, int LANES>
+struct Merge {
+  static constexpr int rows = LANES;                       // rows of a thread
+  static constexpr int depth = LANES == 1 ? 8 : 3;         // segments whose loads are in flight
+  static constexpr int step = kMergeThreads / (D / 4);     // rows at a time
+  static constexpr int block = rows * step;                // rows of a block
+};
 
 template <int D, int LANES>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedArgs A) {
-  constexpr int RPB = kMergeThreads / (D / 4);   // rows of a block
+  using M = Merge<D, LANES>;
   pdl_launch_dependents();
   pdl_wait();
   const int4 sp = __ldcg(A.split + blockIdx.x);
   const int c0 = blockIdx.x, c1 = min(sp.w, int(gridDim.x) - 1);
   if (c1 <= c0) return;
-  const int G = A.hq / A.hkv;
-  const int x = blockIdx.y * RPB + threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
-  const int ln = x / TK, row = x % TK;
+  const int G = A.hq / A.hkv, c4 = threadIdx.x % (D / 4);
   const Request r = request_of<LANES>(A, sp.x);
-  const int tok = (sp.z * LANES + ln) * A.nt + row / G;
-  if (row >= A.qt * G || tok >= r.n) return;
   constexpr size_t kLane = size_t(TK) * (D + 2);
-  const float* base_o = A.partial + ln * kLane + size_t(row) * D + 4 * c4;
-  const float* base_m = A.partial + ln * kLane + size_t(TK) * D + row;
-  constexpr int kDepth = 8;   // segments whose loads are in flight
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; c += kDepth) {
-    float m[kDepth], l[kDepth];
-    float4 o[kDepth];
+  int tok[M::rows], row[M::rows];
+  bool act[M::rows];
+  const float* base_o[M::rows];
+  const float* base_m[M::rows];
+  float top[M::rows], sum[M::rows];
+  float4 acc[M::rows];
 #pragma unroll
-    for (int y = 0; y < kDepth; ++y) {
-      m[y] = -INFINITY;
-      l[y] = 0.f;
-      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + y <= c1) {
-        const size_t off = (size_t(c + y) * 2 + (c + y == c0)) * LANES * kLane;
-        m[y] = __ldcg(base_m + off);
-        l[y] = __ldcg(base_m + off + TK);
-        o[y] = __ldcg(reinterpret_cast<const float4*>(base_o + off));
+  for (int z = 0; z < M::rows; ++z) {
+    const int x = blockIdx.y * M::block + z * M::step + threadIdx.x / (D / 4), ln = x / TK;
+    row[z] = x % TK;
+    tok[z] = (sp.z * LANES + ln) * A.nt + row[z] / G;
+    act[z] = row[z] < A.qt * G && tok[z] < r.n;
+    base_o[z] = A.partial + ln * kLane + size_t(row[z]) * D + 4 * c4;
+    base_m[z] = A.partial + ln * kLane + size_t(TK) * D + row[z];
+    top[z] = -INFINITY;
+    sum[z] = 0.f;
+    acc[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int c = c0; c <= c1; c += M::depth) {
+    float m[M::rows][M::depth], l[M::rows][M::depth];
+    float4 o[M::rows][M::depth];
+#pragma unroll
+    for (int y = 0; y < M::depth; ++y)
+#pragma unroll
+      for (int z = 0; z < M::rows; ++z) {
+        m[z][y] = -INFINITY;
+        l[z][y] = 0.f;
+        o[z][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (act[z] && c + y <= c1) {
+          const size_t off = (size_t(c + y) * 2 + (c + y == c0)) * LANES * kLane;
+          m[z][y] = __ldcg(base_m[z] + off);
+          l[z][y] = __ldcg(base_m[z] + off + TK);
+          o[z][y] = __ldcg(reinterpret_cast<const float4*>(base_o[z] + off));
+        }
+      }
+#pragma unroll
+    for (int z = 0; z < M::rows; ++z) {
+      float ref = top[z];
+#pragma unroll
+      for (int y = 0; y < M::depth; ++y) ref = fmaxf(ref, m[z][y]);
+      const float base = ref == -INFINITY ? 0.f : ref;
+      const float w0 = fast_exp2(top[z] - base);   // 2^-inf = 0
+      top[z] = ref;
+      sum[z] *= w0;
+      acc[z] = make_float4(acc[z].x * w0, acc[z].y * w0, acc[z].z * w0, acc[z].w * w0);
+#pragma unroll
+      for (int y = 0; y < M::depth; ++y) {
+        const float w = fast_exp2(m[z][y] - base);
+        sum[z] = fmaf(l[z][y], w, sum[z]);
+        acc[z].x = fmaf(o[z][y].x, w, acc[z].x);
+        acc[z].y = fmaf(o[z][y].y, w, acc[z].y);
+        acc[z].z = fmaf(o[z][y].z, w, acc[z].z);
+        acc[z].w = fmaf(o[z][y].w, w, acc[z].w);
       }
     }
-    float ref = top;
-#pragma unroll
-    for (int y = 0; y < kDepth; ++y) ref = fmaxf(ref, m[y]);
-    const float base = ref == -INFINITY ? 0.f : ref;
-    const float w0 = fast_exp2(top - base);   // 2^-inf = 0
-    top = ref;
-    sum *= w0;
-    acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
-#pragma unroll
-    for (int y = 0; y < kDepth; ++y) {
-      const float w = fast_exp2(m[y] - base);
-      sum = fmaf(l[y], w, sum);
-      acc.x = fmaf(o[y].x, w, acc.x);
-      acc.y = fmaf(o[y].y, w, acc.y);
-      acc.z = fmaf(o[y].z, w, acc.z);
-      acc.w = fmaf(o[y].w, w, acc.w);
-    }
   }
-  const size_t orow = size_t(r.c0 + tok) * A.hq + size_t(sp.y) * G + row % G;
-  const int position = r.kv - r.n + tok;
-  const float inv = row_scale(sum, position);
-  reinterpret_cast<uint2*>(A.o + orow * D)[c4] =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (A.lse && c4 == 0) A.lse[orow] = row_lse(top, sum, position);
+#pragma unroll
+  for (int z = 0; z < M::rows; ++z) {
+    if (!act[z]) continue;
+    const size_t orow = size_t(r.c0 + tok[z]) * A.hq + size_t(sp.y) * G + row[z] % G;
+    const int position = r.kv - r.n + tok[z];
+    const float inv = row_scale(sum[z], position);
+    reinterpret_cast<uint2*>(A.o + orow * D)[c4] = make_uint2(pack_bf16(acc[z].x * inv, acc[z].y * inv),
+                                                              pack_bf16(acc[z].z * inv, acc[z].w * inv));
+    if (A.lse && c4 == 0) A.lse[orow] = row_lse(top[z], sum[z], position);
+  }
 }
 
 template <int D, int LANES>
@@ -845,9 +905,9 @@ cudaError_t launch_t(const PagedArgs& a, int num_sms, cudaStream_t stream) {
   const int grid = num_sms < kPagedGridMax ? num_sms : kPagedGridMax;
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(NTH), C::total, stream, a);
   if (e != cudaSuccess) return e;
-  constexpr int RPB = kMergeThreads / (D / 4);
+  constexpr int block = Merge<D, LANES>::block;
   const int rows = LANES == 2 ? 2 * TK : a.qt * (a.hq / a.hkv);
-  return launch_pdl(paged_merge_kernel<D, LANES>, dim3(grid, (rows + RPB - 1) / RPB), dim3(kMergeThreads), 0, stream, a);
+  return launch_pdl(paged_merge_kernel<D, LANES>, dim3(grid, (rows + block - 1) / block), dim3(kMergeThreads), 0, stream, a);
 }
 
 }  // namespace
