@@ -106,6 +106,12 @@ __device__ __forceinline__ float row_lse(float top, float sum, int position) {
   return sum != 0.f ? (top + log2f(sum)) * kLn2 : position >= 0 ? kNaN : -INFINITY;
 }
 
+// a / b, where both mostly fit 32 bits (a 64-bit division takes several times as long).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)(uint32_t(a) / uint32_t(b));
+  return a / b;
+}
+
 // A request: its packed rows [c0, c0 + n), cache rows, units of a KV head.
 struct Request {
   int c0, n, kv, pairs;
@@ -187,13 +193,13 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
   }
   const long long total = __shfl_sync(0xffffffffu, inc, 31);
   // each share holds `least` at least
-  const long long runs = max(total / Cost<LANES>::least, total > 0 ? 1LL : 0LL);
+  const long long runs = max(quot(total, Cost<LANES>::least), total > 0 ? 1LL : 0LL);
   const int ctas = int(runs < gridDim.x ? runs : gridDim.x), c = int(blockIdx.x) + next;
   out.total = total;
   out.ctas = ctas;
-  out.snap = ctas ? int(min((long long)Cost<LANES>::snap, total / ctas / 16)) : 0;
+  out.snap = ctas ? int(min((long long)Cost<LANES>::snap, quot(total, 16 * ctas))) : 0;
   if (c >= ctas) return Cut{total, A.B, 0, 0, 0};
-  Cut s{c * total / ctas, 0, 0, 0, 0};
+  Cut s{quot(c * total, ctas), 0, 0, 0, 0};
   // the lane whose requests hold the cut, then the request, the KV head and the unit
   const int src = __ffs(__ballot_sync(0xffffffffu, s.pos < inc)) - 1;
   long long at = s.pos - __shfl_sync(0xffffffffu, inc - mine, src), head = 0;
@@ -204,7 +210,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
     if (at < head * A.hkv || s.b + 1 == A.B) break;
     at -= head * A.hkv;
   }
-  s.g = int(at / head);
+  s.g = int(quot(at, head));
   at -= s.g * head;
   int cost = 0;
   for (; s.p < r.pairs; s.p += 32) {
@@ -354,6 +360,11 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
     mbar_init(pair_empty, 32 * n_act);
     *abort_flag = 0;
     fence_barrier_init();
+  }
+  if (tid == 64) {
+    prefetch_tensormap(&A.qmap);
+    prefetch_tensormap(&A.kmap);
+    prefetch_tensormap(&A.vmap);
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
@@ -530,34 +541,33 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         if (tid == 0 && !whole && w.i0 == 0) {
           // the CTA that the unit's cost ends in
           const long long end = start->to - w.used + unit_cost<LANES>(A, w.r, w.p) - w.at;
-          int last = int((end * start->ctas - 1) / start->total);
-          if (end - last * start->total / start->ctas <= start->snap) --last;   // (its share was moved past the unit)
+          int last = int(quot(end * start->ctas - 1, start->total));
+          if (end - quot(last * start->total, start->ctas) <= start->snap) --last;   // (its share was moved past the unit)
           split = make_int4(w.b, w.g, w.p, last);
         }
         float* part = A.partial + ((size_t(blockIdx.x) * 2 + (w.i0 == 0)) * LANES + ln) * (size_t(TK) * (D + 2));
         const size_t orow = size_t(w.r.c0 + (act ? tok : 0)) * A.hq + size_t(w.g) * G + row % G;
         const float inv = row_scale(lsum, position);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc_ld32(o_tmem + uint32_t(c), o);   // collective: every lane loads
+        for (int c = 0; c < D; c += 64) {
+          uint32_t o[64];
+          tc_ld64(o_tmem + uint32_t(c), o);   // collective: every lane loads
           if (join) {
-            uint32_t o1[32];
-            tc_ld32(o_tmem + uint32_t(128 + c), o1);
+            uint32_t o1[64];
+            tc_ld64(o_tmem + uint32_t(128 + c), o1);
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
+            for (int y = 0; y < 64; ++y)
               o[y] = __float_as_uint(fmaf(__uint_as_float(o[y]), w0, __uint_as_float(o1[y]) * w1));
           }
           if (act && whole) {
-            uint32_t pk[16];
 #pragma unroll
-            for (int y = 0; y < 16; ++y)
-              pk[y] = pack_bf16(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+            for (int y = 0; y < 32; ++y)
+              o[y] = pack_bf16(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) store32(A.o + orow * D + c + 16 * y, pk + 8 * y);
+            for (int y = 0; y < 4; ++y) store32(A.o + orow * D + c + 16 * y, o + 8 * y);
           } else if (act) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) store32(part + size_t(row) * D + c + 8 * y, o + 8 * y);
+            for (int y = 0; y < 8; ++y) store32(part + size_t(row) * D + c + 8 * y, o + 8 * y);
           }
         }
         if (join) {
