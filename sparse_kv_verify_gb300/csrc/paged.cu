@@ -27,13 +27,15 @@
 //                   group as its 64-column panels of 8 swizzled rows; pools whose
 //                   strides keep a load from more than 64 columns have a load and
 //                   a run of groups per panel instead;
-//   warp 8          zeroes the rows of a V tile past the request's last one, once the
-//                   tile has landed (they may hold anything, and 0 * NaN is not 0;
+//   warp 8          waits for the loads, and zeroes the rows of a V tile past the
+//                   request's last one (they may hold anything, and 0 * NaN is not 0;
 //                   what K holds there gives scores that the mask drops);
 //   warp 10         one elected thread issues the MMAs, per step i and lane a batch
 //                   O += P(i) V(i), S(i + NB) = Q K(i + NB)^T over the S and P that
 //                   the first product has read (MMAs of one thread run in the
-//                   order of issue).
+//                   order of issue).  It is told of P and of loads by named
+//                   barriers: an mbarrier's state is read behind its products that
+//                   the tensor core has not taken yet, about 480 cycles.
 // Batches whose requests may have two row tiles: steps of 128 keys, one S buffer
 // per lane (NB = 1); while one lane's softmax works the tensor core has the other
 // lane's products.  A unit with one row tile (single tokens beside a chunk) gives
@@ -56,9 +58,10 @@ namespace dustin {
 namespace {
 
 constexpr int TK = kPagedTile;       // keys per tile, and query rows per row tile
-constexpr int kTailWarp = 8, kLoadWarp = 9, kMmaWarp = 10, kLoadWarp2 = 11;
-constexpr int NTH = 384;             // 168 registers a thread (a softmax thread holds a row's scores)
+constexpr int kLandWarp = 8, kLoadWarp = 9, kMmaWarp = 10, kLoadWarp2 = 11;
+constexpr int NTH = 384;             // 168 registers a thread at the launch
 constexpr int kSCol = 0, kOCol = 256;                // lane 1: + 128
+constexpr int kPBar = 1, kLandedBar = 5;             // named barriers: P of [lane][buffer] is stored; loads are in
 constexpr float kNaN = __builtin_nanf("");
 
 // The cost of a unit: kTile for each key tile (two lanes' products; or one row
@@ -93,7 +96,7 @@ struct Cfg {
   static constexpr uint32_t stage = (D / 64) * panel;
   static constexpr uint32_t ring_off = LANES * stage;   // after the query tiles
   static constexpr uint32_t bar_off = ring_off + nst * stage;
-  static constexpr uint32_t misc_off = bar_off + (3 * nst + 17) * 8;   // barriers
+  static constexpr uint32_t misc_off = bar_off + (3 * nst + 13) * 8;   // barriers
   static constexpr uint32_t total = misc_off + 16 + sizeof(Start) + (LANES == 2 ? TK * 8 : 0) + 1024;
 };
 
@@ -258,6 +261,26 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
+  return a;
+}
+
+// mbar_wait that gives up at once where another wait of the CTA has: the softmax
+// warps and the landing warp then run on without data (the call is flagged), so that
+// the named barriers, which know no limit, are all met.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*abort) return false;
+  return mbar_wait(bar, parity, err, abort);
+}
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Groups of 8 rows (all columns, or 64) of a page: coordinates (x, row 0 of a
 // group, c2, c3, page).
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int c2, int c3, int page,
@@ -327,8 +350,7 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   uint64_t* q_full = empty + NST;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;      // [lane][buffer] a batch with an S is done
-  uint64_t* p_full = s_full + 4;       // [lane][buffer] P is stored over S
-  uint64_t* o_full = p_full + 4;       // [lane][z] the z-th of a segment's last NB batches, without an S, is done
+  uint64_t* o_full = s_full + 4;       // [lane][z] the z-th of a segment's last NB batches, without an S, is done
   uint64_t* mma_done = o_full + 4;
   uint64_t* pair_full = mma_done + 1;  // lane 1's part of a unit with one row tile is complete
   uint64_t* pair_empty = pair_full + 1;   // and has been read
@@ -352,7 +374,6 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
     mbar_init(q_empty, 1);
     for (int x = 0; x < 4; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 32 * n_act);
       mbar_init(&o_full[x], 1);
     }
     mbar_init(mma_done, 1);
@@ -395,10 +416,12 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk<LANES> w;
-  w.init(A, *start);
-
   if (warp < 4 * LANES) {
     // =============================================================== softmax
+    // a softmax thread holds a row's scores: 200 x 256 + 96 x 128 of the 168 x 384
+    // registers of the launch (LANES = 1 needs no more than these)
+    if constexpr (LANES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    w.init(A, *start);
     const int ln = warp >> 2;                       // lane (row tile of the pair)
     const int row = tid & 127;
     if ((warp & 3) < n_act) {
@@ -411,15 +434,15 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       // in turn, and the one after it needs a P that the thread stores later: no
       // wait by parity can be lapped or pass early.
       auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+        wait_on(bar, parity, A.err, abort_flag);
+        __syncwarp();
       };
-      auto wait_s = [&](int J) { return wait_warp(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u); };
+      auto wait_s = [&](int J) { wait_warp(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u); };
       int j0 = 0, segs = 0;   // steps and segments of the lane before this segment
-      auto wait_o = [&](int z) { return wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
-      bool live = true;
+      auto wait_o = [&](int z) { wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
       int4 split = make_int4(0, 0, 0, -1);
       uint32_t pairs = 0;     // phase of pair_full and pair_empty
-      for (; live && w.left > 0; w.next(A)) {
+      for (; w.left > 0; w.next(A)) {
         // a unit with one row tile gives its odd tiles to lane 1
         const bool halves = LANES == 2 && !w.two;
         if (halves && ln == 1 && w.n == 1) continue;
@@ -432,10 +455,7 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         for (int i = 0; i < n; ++i) {
           const int nv = position + 1 - (key0 + i * keyd) * SK;      // keys of this step that the row sees, if under SK
           const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
-          if (!wait_s(j0 + i)) {
-            live = false;
-            break;
-          }
+          wait_s(j0 + i);
           tc_fence_after();
           float x[SK];
 #pragma unroll
@@ -444,14 +464,14 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
 #pragma unroll
             for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
           }
-          float m4[4] = {x[0], x[1], x[2], x[3]};
+          float m4[4];
 #pragma unroll
-          for (int j = 4; j + 8 <= SK; j += 8)
+          for (int y = 0; y < 4; ++y) m4[y] = fmaxf(x[2 * y], x[2 * y + 1]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], fmaxf(x[j + y], x[j + 4 + y]));
+          for (int j = 8; j < SK; j += 8)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) m4[y] = fmaxf(m4[y], x[SK - 4 + y]);
-          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int y = 0; y < 4; ++y) m4[y] = max3(m4[y], x[j + 2 * y], x[j + 2 * y + 1]);
+          const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
           // (a row that is not in use never rescales O; its P and O are never read)
           const float mx = act ? top * scale : -INFINITY;
           float alpha = 1.f;
@@ -465,9 +485,9 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
           // came with S of this step; NB = 2: it comes with S of the next one, or
           // alone after the last)
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            if (NB > 1 && !(i + 1 < n ? wait_s(j0 + i + 1) : wait_o(0))) {
-              live = false;
-              break;
+            if (NB > 1) {
+              if (i + 1 < n) wait_s(j0 + i + 1);
+              else wait_o(0);
             }
             tc_fence_after();
 #pragma unroll 1
@@ -499,13 +519,11 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
           tc_wait_st();
           lsum += (l0 + l1) + (l2 + l3);
           tc_fence_before();
-          mbar_arrive(&p_full[2 * ln + (j0 + i) % NB]);
+          named_arrive(kPBar + 2 * ln + (j0 + i) % NB, 32 * n_act + 32);
         }
-        if (!live) break;
         // --------------------------------------------------------- epilogue
 #pragma unroll
-        for (int z = 0; z < NB; ++z) live = live && wait_o(z);
-        if (!live) break;
+        for (int z = 0; z < NB; ++z) wait_o(z);
         j0 += n;
         ++segs;
         tc_fence_after();
@@ -518,15 +536,12 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
             pair_ml[row] = make_float2(mref, lsum);
             tc_fence_before();
             mbar_arrive(pair_full);
-            live = wait_warp(pair_empty, pairs);
+            wait_warp(pair_empty, pairs);
             pairs ^= 1u;
             tc_fence_after();
             continue;
           }
-          if (!wait_warp(pair_full, pairs)) {
-            live = false;
-            break;
-          }
+          wait_warp(pair_full, pairs);
           pairs ^= 1u;
           tc_fence_after();
           const float2 ml = pair_ml[row];
@@ -584,192 +599,209 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         }
         tc_fence_before();
       }
-      if (tid == 0) A.split[blockIdx.x] = live ? split : make_int4(0, 0, 0, -1);
+      if (tid == 0) A.split[blockIdx.x] = split;
     }
-  } else if (warp == kLoadWarp || warp == kLoadWarp2) {
-    // ================================================================ loads
-    // (both warps follow every phase of every stage; the first alone arms them)
-    const bool lead = warp == kLoadWarp;
-    const int box = min(A.page, TK);                  // rows of a load
-    int gi = 0, st = 0, segs = 0;
-    uint32_t ph = 0;                                  // of stage st
-    uint32_t tails = 0, tail_ph = 0;                  // stages whose latest load is waited for by `landed`; its phases
-    bool live = true;
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-      return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
-    };
-    for (; live && w.left > 0; w.next(A)) {
-      const int32_t* table = A.table + size_t(w.b) * A.max_pages;
-      // the table's entry for this thread in a tile, read a tile ahead of its use
-      auto needs = [&](int i) { return i < w.n && lane_id * box < TK && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
-      auto page_at = [&](int i) { return needs(i) ? __ldg(table + ((w.i0 + i) * TK + lane_id * box) / A.page) : 0; };
-      int ahead = page_at(0);
-      // this segment's query tiles, once the last one's S MMAs have read theirs
-      if (lead) {
-        if (segs > 0 && !wait_warp(q_empty, uint32_t(segs - 1) & 1u)) break;
-        if (lane_id == 0) {
-          const bool two = w.two;
-          const uint32_t bytes = uint32_t(A.qt * G) * D * 2;
-          mbar_arrive_expect_tx(q_full, two ? 2 * bytes : bytes);
-          for (int ln = 0; ln < (two ? 2 : 1); ++ln)
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tma_load_3d(sbase + uint32_t(ln) * C::stage + uint32_t(h) * C::panel, &A.qmap, h * 64, w.g * G,
-                          w.r.c0 + w.first(A) + ln * A.nt, q_full);
-        }
-        ++segs;
-      }
-      // K(0), then K(i), V(i - 1) for each tile, V(n - 1): the order of their use
-      int id = -1;
-      for (int i = 0; live && i <= w.n; ++i) {
-        const int before = id;
-        id = -1;
-        if (needs(i)) {
-          id = ahead;
-          if (id < 0 || id >= A.n_pages) {
-            flag_error(A.err, DUSTIN_DEV_INDEX);
-            id = A.n_pages;   // past the end: the load fills in zeros
-          }
-        }
-        ahead = page_at(i + 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (kv ? i == 0 : i == w.n) continue;
-          const int base = (w.i0 + i - kv) * TK, page = kv ? before : id;
-          if (gi >= NST && !wait_warp(&empty[st], ph ^ 1u)) {
-            live = false;
-            break;
-          }
-          const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
-          const int r0 = A.page >= TK ? base % A.page : 0;
-          const bool tail = kv && base + TK > w.r.kv;
-          uint64_t* bar = tail ? &landed[st] : &full[st];
-          if (lead && lane_id == 0) mbar_arrive_expect_tx(bar, uint32_t(np * box) * D * 2);
-          __syncwarp();
-          const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage;
-          const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
-          const int c2 = A.merged ? w.g * A.map_panels : r0 / 8, c3 = A.merged ? w.g * A.map_groups + r0 / 8 : w.g;
-          // every other page by each warp, or a panel of each page
-          if (page >= 0) {
-            const int h = lead ? 0 : 1;
-            if (D == 64 || A.merged) {
-              if ((lane_id & 1) == h) tma_load_5d(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar);
-            } else {
-              tma_load_5d(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar);
-            }
-          }
-          if (tail) tail_ph ^= 1u << st;
-          tails = tail ? tails | 1u << st : tails & ~(1u << st);
-          ++gi;
-          if (++st == NST) {
-            st = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-    }
-    // what is in flight has landed before the CTA may exit: the query tiles
-    // and the latest load of each stage
-    if (lead && lane_id == 0) {
-      if (segs > 0) mbar_drain(q_full, uint32_t(segs - 1) & 1u, A.err);
-      for (int j = gi > NST ? gi - NST : 0; j < gi; ++j) {
-        const int x = j % NST;
-        if ((tails >> x) & 1u) mbar_drain(&landed[x], ((tail_ph >> x) & 1u) ^ 1u, A.err);
-        else mbar_drain(&full[x], uint32_t(j / NST) & 1u, A.err);
-      }
-    }
-    __syncwarp();
-  } else if (warp == kTailWarp) {
-    // ================================================================ tails
-    int gi = 0;
-    uint32_t tail_ph = 0;   // phases of `landed`
-    for (; w.left > 0; w.next(A)) {
-      gi += 2 * w.n;
-      const int nv = max(w.r.kv - (w.i0 + w.n - 1) * TK, 0);   // rows of the segment's last tile
-      if (nv >= TK) continue;
-      const int st = (gi - 1) % NST;
-      if (!__all_sync(0xffffffffu, mbar_wait(&landed[st], (tail_ph >> st) & 1u, A.err, abort_flag))) break;
-      tail_ph ^= 1u << st;
-      unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
-      const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)   // 16 bytes each, 64 of them a group
-          *reinterpret_cast<uint4*>(rows + h * panel + (x >> 6) * group + (x & 63) * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane_id == 0) mbar_arrive(&full[st]);
-    }
-    __syncwarp();
   } else {
-    if (warp == kMmaWarp) {
-      // ================================================================ MMAs
-      constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
-      const uint64_t q_desc = tc_desc(sbase, 16, 1024);
-      const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
-      const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, group), v_desc = tc_desc(sbase + C::ring_off, panel, group);
-      const uint32_t kpanel = panel >> 4, keys16 = group >> 3;   // per panel, and per 16 keys
-      int st = 0, segs = 0;                 // ring stage to consume next; segments
-      uint32_t ph = 0, pp = 0;              // its phase; phases of the P buffers (bit 2 lane + buffer)
-      bool issued = false, live = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if constexpr (LANES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    w.init(A, *start);
+    if (warp == kLoadWarp || warp == kLoadWarp2) {
+      // ================================================================ loads
+      // (both warps follow every phase of every stage; the first alone arms them)
+      const bool lead = warp == kLoadWarp;
+      const int box = min(A.page, TK);                  // rows of a load
+      int gi = 0, st = 0, segs = 0;
+      uint32_t ph = 0;                                  // of stage st
+      uint32_t tails = 0, tail_ph = 0;                  // stages whose latest load is waited for by `landed`; its phases
+      bool live = true;
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
         return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
       };
-      // the warp runs together and one elected lane issues; branches go by votes,
-      // so that the compiler too knows the warp as converged
-      auto uni = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };
-      auto next_stage = [&] {
-        if (++st == NST) {
-          st = 0;
-          ph ^= 1u;
+      for (; live && w.left > 0; w.next(A)) {
+        const int32_t* table = A.table + size_t(w.b) * A.max_pages;
+        // the table's entry for this thread in a tile, read a tile ahead of its use
+        auto needs = [&](int i) { return i < w.n && lane_id * box < TK && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
+        auto page_at = [&](int i) { return needs(i) ? __ldg(table + ((w.i0 + i) * TK + lane_id * box) / A.page) : 0; };
+        int ahead = page_at(0);
+        // this segment's query tiles, once the last one's S MMAs have read theirs
+        if (lead) {
+          if (segs > 0 && !wait_warp(q_empty, uint32_t(segs - 1) & 1u)) break;
+          if (lane_id == 0) {
+            const bool two = w.two;
+            const uint32_t bytes = uint32_t(A.qt * G) * D * 2;
+            mbar_arrive_expect_tx(q_full, two ? 2 * bytes : bytes);
+            for (int ln = 0; ln < (two ? 2 : 1); ++ln)
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(sbase + uint32_t(ln) * C::stage + uint32_t(h) * C::panel, &A.qmap, h * 64, w.g * G,
+                            w.r.c0 + w.first(A) + ln * A.nt, q_full);
+          }
+          ++segs;
         }
+        // K(0), then K(i), V(i - 1) for each tile, V(n - 1): the order of their use
+        int id = -1;
+        for (int i = 0; live && i <= w.n; ++i) {
+          const int before = id;
+          id = -1;
+          if (needs(i)) {
+            id = ahead;
+            if (id < 0 || id >= A.n_pages) {
+              flag_error(A.err, DUSTIN_DEV_INDEX);
+              id = A.n_pages;   // past the end: the load fills in zeros
+            }
+          }
+          ahead = page_at(i + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (kv ? i == 0 : i == w.n) continue;
+            const int base = (w.i0 + i - kv) * TK, page = kv ? before : id;
+            if (gi >= NST && !wait_warp(&empty[st], ph ^ 1u)) {
+              live = false;
+              break;
+            }
+            const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
+            const int r0 = A.page >= TK ? base % A.page : 0;
+            const bool tail = kv && base + TK > w.r.kv;
+            uint64_t* bar = tail ? &landed[st] : &full[st];
+            if (lead && lane_id == 0) mbar_arrive_expect_tx(bar, uint32_t(np * box) * D * 2);
+            __syncwarp();
+            const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage;
+            const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
+            const int c2 = A.merged ? w.g * A.map_panels : r0 / 8, c3 = A.merged ? w.g * A.map_groups + r0 / 8 : w.g;
+            // every other page by each warp, or a panel of each page
+            if (page >= 0) {
+              const int h = lead ? 0 : 1;
+              if (D == 64 || A.merged) {
+                if ((lane_id & 1) == h) tma_load_5d(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar);
+              } else {
+                tma_load_5d(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar);
+              }
+            }
+            if (tail) tail_ph ^= 1u << st;
+            tails = tail ? tails | 1u << st : tails & ~(1u << st);
+            ++gi;
+            if (++st == NST) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+      // what is in flight has landed before the CTA may exit: the query tiles
+      // and the latest load of each stage
+      if (lead && lane_id == 0) {
+        if (segs > 0) mbar_drain(q_full, uint32_t(segs - 1) & 1u, A.err);
+        for (int j = gi > NST ? gi - NST : 0; j < gi; ++j) {
+          const int x = j % NST;
+          if ((tails >> x) & 1u) mbar_drain(&landed[x], ((tail_ph >> x) & 1u) ^ 1u, A.err);
+          else mbar_drain(&full[x], uint32_t(j / NST) & 1u, A.err);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kLandWarp) {
+      // ============================================================ landings
+      // waits for what the products read and lets the MMA warp go on by a named barrier:
+      // a wait on an mbarrier by that warp would stand behind its queued products
+      int gi = 0, segs = 0;
+      uint32_t tail_ph = 0;   // phases of `landed`
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        wait_on(bar, parity, A.err, abort_flag);
+        __syncwarp();
       };
-      // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
-      auto segment = [&](auto halves, bool two) {
-        constexpr bool HALVES = decltype(halves)::value;
-        constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
-        const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
-        int sv = 0, sk = 0;                     // stages of V and of K
+      auto ready = [&](bool tail, int nv) {   // load gi
+        const int st = gi % NST;
+        if (tail) {
+          wait_warp(&landed[st], (tail_ph >> st) & 1u);
+          tail_ph ^= 1u << st;
+          unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
+          const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)   // 16 bytes each, 64 of them a group
+              *reinterpret_cast<uint4*>(rows + h * panel + (x >> 6) * group + (x & 63) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          if (lane_id == 0) mbar_arrive(&full[st]);   // every load is a phase of `full`
+        } else {
+          wait_warp(&full[st], uint32_t(gi / NST) & 1u);
+        }
+        ++gi;
+      };
+      for (; w.left > 0; w.next(A)) {
+        wait_warp(q_full, uint32_t(segs++) & 1u);
+        const int nv = max(w.r.kv - (w.i0 + w.n - 1) * TK, 0);   // rows of the segment's last tile
+        // K(0), then K(i), V(i - 1) for each tile, V(n - 1)
+        const bool halves = LANES == 2 && !w.two;
+        if (!halves) {
+          ready(false, 0);
+          named_sync(kLandedBar, 64);
+          for (int i = 0; i < w.n; ++i) {
+            if (i + 1 < w.n) ready(false, 0);
+            ready(i + 1 == w.n && nv < TK, nv);
+            named_sync(kLandedBar, 64);
+          }
+        } else {
+          for (int j = -2; j < w.n; ++j) {
+            if (j < 0 && j + 2 >= w.n) continue;
+            if (j >= 0) ready(j + 1 == w.n && nv < TK, nv);
+            if (j + 2 < w.n) ready(false, 0);
+            named_sync(kLandedBar, 64);
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      if (warp == kMmaWarp) {
+        // ================================================================ MMAs
+        constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
+        const uint64_t q_desc = tc_desc(sbase, 16, 1024);
+        const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
+        const uint64_t k_desc = tc_desc(sbase + C::ring_off, 16, group), v_desc = tc_desc(sbase + C::ring_off, panel, group);
+        const uint32_t kpanel = panel >> 4, keys16 = group >> 3;   // per panel, and per 16 keys
+        int st = 0;                           // ring stage to consume next
+        bool issued = false;
+        // the warp runs together and one elected lane issues; branches go by votes,
+        // so that the compiler too knows the warp as converged
+        auto uni = [](bool x) { return __any_sync(0xffffffffu, x) != 0; };
         auto take = [&](int& stage) {
           stage = st;
-          live = wait(&full[stage], ph);
-          next_stage();
+          st = st + 1 == NST ? 0 : st + 1;
         };
-        for (int i = -lead; live && uni(i < n); ++i) {
-          const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
-          const bool pv = i >= 0, s = uni(i + lead < n);
-          // tiles come as K(0), K(1), V(0), K(2), V(1), ...
-          if (HALVES && pv) take(sv);
-          if (live && s && first) take(sk);
-          if (live && !HALVES && pv && first) take(sv);
-          auto batch = [&](int ln, int buf) {
-            if (pv) {
-              live = wait(&p_full[2 * ln + buf], (pp >> (2 * ln + buf)) & 1u);
-              if (!live) return;
-              pp ^= 1u << (2 * ln + buf);
-            }
-            issued = true;
-            tc_fence_after();
-            const uint32_t sp = tmem + uint32_t(kSCol + 128 * ln + buf * SK);
-            if (pv) {
-              const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
-              const bool acc = i >= (HALVES ? 2 : 1);   // not the lane's first step
+        // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
+        auto segment = [&](auto halves, bool two) {
+          constexpr bool HALVES = decltype(halves)::value;
+          constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
+          const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
+          int sv = 0, sk = 0;                     // stages of V and of K
+          for (int i = -lead; uni(i < n); ++i) {
+            const bool first = NB == 1 || !(i & 1), last = NB == 1 || (i & 1);   // step of its tiles
+            const bool pv = i >= 0, s = uni(i + lead < n);
+            // tiles come as K(0), K(1), V(0), K(2), V(1), ...
+            if ((pv || s) && first) named_sync(kLandedBar, 64);
+            if (HALVES && pv) take(sv);
+            if (s && first) take(sk);
+            if (!HALVES && pv && first) take(sv);
+            auto batch = [&](int ln, int buf) {
+              if (pv) named_sync(kPBar + 2 * ln + buf, 32 * n_act + 32);
+              issued = true;
+              tc_fence_after();
+              const uint32_t sp = tmem + uint32_t(kSCol + 128 * ln + buf * SK);
+              if (pv) {
+                const uint64_t v = v_desc + uint64_t(sv) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
+                const bool acc = i >= (HALVES ? 2 : 1);   // not the lane's first step
 #pragma unroll
-              for (int kk = 0; kk < SK / 16; ++kk)
-                tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk) * keys16, kIdPV,
-                                (acc || kk > 0) ? 1 : 0);
-            }
-            if (s) {
-              const uint64_t q = q_desc + uint64_t(HALVES ? 0 : ln) * (C::stage >> 4);
-              const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
+                for (int kk = 0; kk < SK / 16; ++kk)
+                  tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk) * keys16, kIdPV,
+                                  (acc || kk > 0) ? 1 : 0);
+              }
+              if (s) {
+                const uint64_t q = q_desc + uint64_t(HALVES ? 0 : ln) * (C::stage >> 4);
+                const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma_ss_elect(sp, q + uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2),
-                                k + uint32_t(kk >> 2) * kpanel + uint32_t((kk & 3) * 2), kIdS, kk > 0);
-            }
-            tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
-          };
-          if (live) {
+                for (int kk = 0; kk < D / 16; ++kk)
+                  tc_mma_ss_elect(sp, q + uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2),
+                                  k + uint32_t(kk >> 2) * kpanel + uint32_t((kk & 3) * 2), kIdS, kk > 0);
+              }
+              tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
+            };
             if constexpr (HALVES) {
               if (pv || s) {
                 if (i & 1) batch(1, 0);
@@ -777,32 +809,29 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
               }
             } else {
               batch(0, NB == 1 ? 0 : i & 1);   // (step i and step i + NB have one buffer)
-              if (LANES == 2 && live && two) batch(1, 0);
+              if (LANES == 2 && two) batch(1, 0);
             }
+            if (pv && last) tc_commit_elect(&empty[sv]);
+            if (s && last) tc_commit_elect(&empty[sk]);
+            if (uni(i + lead + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
           }
-          if (!live) return;
-          if (pv && last) tc_commit_elect(&empty[sv]);
-          if (s && last) tc_commit_elect(&empty[sk]);
-          if (uni(i + lead + 1 == n)) tc_commit_elect(q_empty);   // the query tiles are no longer read
+        };
+        for (; uni(w.left > 0); w.next(A)) {
+          const bool two = uni(w.two);
+          if constexpr (LANES == 2) {
+            if (two) segment(std::false_type{}, true);
+            else segment(std::true_type{}, false);
+          } else {
+            segment(std::false_type{}, false);
+          }
         }
-      };
-      for (; live && uni(w.left > 0); w.next(A)) {
-        const bool two = uni(w.two);
-        live = wait(q_full, uint32_t(segs++) & 1u);
-        if (!live) break;
-        if constexpr (LANES == 2) {
-          if (two) segment(std::false_type{}, true);
-          else segment(std::true_type{}, false);
-        } else {
-          segment(std::false_type{}, false);
+        if (issued) {   // every MMA has completed before tensor memory is freed
+          tc_commit_elect(mma_done);
+          if (lane_id == 0) mbar_drain(mma_done, 0, A.err);
         }
       }
-      if (issued) {   // every MMA has completed before tensor memory is freed
-        tc_commit_elect(mma_done);
-        if (lane_id == 0) mbar_drain(mma_done, 0, A.err);
-      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 
   tc_fence_before();
