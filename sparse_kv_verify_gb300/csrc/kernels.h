@@ -424,8 +424,8 @@ struct PagedArgs {
   int nt, qt;                // tokens of a row tile, and of a query load
   int merged;                // a load of the pools brings all columns (else 64)
   int map_panels, map_groups;   // what a KV head adds to the third and fourth coordinate of a load
-  int4* split;               // [kPagedGridMax] (request, KV head, pair, last CTA) of the unit that a CTA starts and
-                             // does not end, last CTA -1: none
+  int4* split;               // [kPagedGridMax][2] of the unit that a CTA starts and does not end: first row of its
+                             // request, KV head, pair, last CTA (-1: none); its rows and cache rows
   float* partial;            // slots [kPagedGridMax][2][lanes][128 * (D + 2)]: O, m [128], l [128]
   CUtensorMap qmap, kmap, vmap;
 };

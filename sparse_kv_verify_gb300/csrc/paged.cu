@@ -68,10 +68,10 @@ constexpr float kNaN = __builtin_nanf("");
 // tile's, whose time is its bytes'), and for its start and end kExtra.
 template <int LANES>
 struct Cost {
-  static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 4 : 3; }
-  static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 12 : 8; }
+  static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 8 : 7; }
+  static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 20 : 8; }
   static constexpr int least = tile(LANES == 2);   // of a share, so that a CTA inside a unit has a tile
-  static constexpr int snap = LANES == 1 ? 2 : 20; // a cut moves this far to the next end of a unit, to save a merge
+  static constexpr int snap = LANES == 1 ? 2 : 40; // a cut moves this far to the next end of a unit, to save a merge
 };
 
 // A cut of the flattened cost: at `at` of pair p of (request b, KV head g), all in
@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       auto wait_s = [&](int J) { wait_warp(&s_full[2 * ln + J % NB], uint32_t(J / NB) & 1u); };
       int j0 = 0, segs = 0;   // steps and segments of the lane before this segment
       auto wait_o = [&](int z) { wait_warp(&o_full[2 * ln + z], uint32_t(segs) & 1u); };
-      int4 split = make_int4(0, 0, 0, -1);
+      int4 split = make_int4(0, 0, 0, -1);   // the unit that this CTA starts and does not end, and the last CTA of it
+      Request whose{0, 0, 0, 0};
       uint32_t pairs = 0;     // phase of pair_full and pair_empty
       for (; w.left > 0; w.next(A)) {
         // a unit with one row tile gives its odd tiles to lane 1
@@ -558,7 +559,8 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
           const long long end = start->to - w.used + unit_cost<LANES>(A, w.r, w.p) - w.at;
           int last = int(quot(end * start->ctas - 1, start->total));
           if (end - quot(last * start->total, start->ctas) <= start->snap) --last;   // (its share was moved past the unit)
-          split = make_int4(w.b, w.g, w.p, last);
+          split = make_int4(w.r.c0, w.g, w.p, last);
+          whose = w.r;
         }
         float* part = A.partial + ((size_t(blockIdx.x) * 2 + (w.i0 == 0)) * LANES + ln) * (size_t(TK) * (D + 2));
         const size_t orow = size_t(w.r.c0 + (act ? tok : 0)) * A.hq + size_t(w.g) * G + row % G;
@@ -599,7 +601,10 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         }
         tc_fence_before();
       }
-      if (tid == 0) A.split[blockIdx.x] = split;
+      if (tid == 0) {
+        A.split[2 * blockIdx.x] = split;
+        A.split[2 * blockIdx.x + 1] = make_int4(whose.n, whose.kv, 0, 0);
+      }
     }
   } else {
     if constexpr (LANES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -858,11 +863,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   using M = Merge<D, LANES>;
   pdl_launch_dependents();
   pdl_wait();
-  const int4 sp = __ldcg(A.split + blockIdx.x);
+  const int4 sp = __ldcg(A.split + 2 * blockIdx.x), of = __ldcg(A.split + 2 * blockIdx.x + 1);
   const int c0 = blockIdx.x, c1 = min(sp.w, int(gridDim.x) - 1);
   if (c1 <= c0) return;
   const int G = A.hq / A.hkv, c4 = threadIdx.x % (D / 4);
-  const Request r = request_of<LANES>(A, sp.x);
+  const Request r{sp.x, of.x, of.y, 0};
   constexpr size_t kLane = size_t(TK) * (D + 2);
   int tok[M::rows], row[M::rows];
   bool act[M::rows];

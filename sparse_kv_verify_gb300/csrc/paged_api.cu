@@ -43,7 +43,7 @@ struct PagedPlan {
 PagedPlan paged_plan(int hq, int hkv, int d, int max_new) {
   PagedPlan pl;
   pl.split_off = kScratch;
-  pl.part_off = round256(pl.split_off + kPagedGridMax * sizeof(int4));
+  pl.part_off = round256(pl.split_off + kPagedGridMax * 2 * sizeof(int4));
   pl.total = pl.part_off + round256(size_t(kPagedGridMax) * 2 * paged_lanes(hq, hkv, max_new) * kPagedTile * (size_t(d) + 2) * 4);
   return pl;
 }
