@@ -15,22 +15,23 @@
 //
 // Roles (handing over through mbarriers):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
-//                   step's scores in registers, P (bf16) stored over them; the
-//                   reference maximum moves only when a step passes it by more
-//                   than 2^8, and then the thread rescales its row of O.  P is
-//                   rounded to bf16 for the second product; the row sum adds the
-//                   unrounded fp32 values, so lse keeps fp32 accuracy;
-//   warps 9, 11     K and V tiles into a ring of 128-row stages, a page's rows in one
+//                   step's scores in registers, P (bf16) stored over them.  The
+//                   reference maximum is the first step's; a later step is weighed
+//                   against it at once, and only where a row's weights sum to more
+//                   than 2^12 again against a new one, with which the thread rescales
+//                   its row of O.  P is rounded to bf16 for the second product; the
+//                   row sum adds the unrounded fp32 values, so lse keeps fp32 accuracy;
+//   two warps       K and V tiles into a ring of 128-row stages, a page's rows in one
 //                   tiled TMA load, the pages of a tile by as many threads, half
 //                   of them by each warp (a load takes about 95 cycles, however
 //                   small).  A stage holds groups of 8 rows one after another, a
 //                   group as its 64-column panels of 8 swizzled rows; pools whose
 //                   strides keep a load from more than 64 columns have a load and
 //                   a run of groups per panel instead;
-//   warp 8          waits for the loads, and zeroes the rows of a V tile past the
+//   a warp          waits for the loads, and zeroes the rows of a V tile past the
 //                   request's last one (they may hold anything, and 0 * NaN is not 0;
 //                   what K holds there gives scores that the mask drops);
-//   warp 10         one elected thread issues the MMAs, per step i and lane a batch
+//   a warp          one elected thread issues the MMAs, per step i and lane a batch
 //                   O += P(i) V(i), S(i + NB) = Q K(i + NB)^T over the S and P that
 //                   the first product has read (MMAs of one thread run in the
 //                   order of issue).  It is told of P and of loads by named
@@ -58,11 +59,10 @@ namespace dustin {
 namespace {
 
 constexpr int TK = kPagedTile;       // keys per tile, and query rows per row tile
-constexpr int kLandWarp = 8, kLoadWarp = 9, kMmaWarp = 10, kLoadWarp2 = 11;
-constexpr int NTH = 384;             // 168 registers a thread at the launch
 constexpr int kSCol = 0, kOCol = 256;                // lane 1: + 128
 constexpr int kPBar = 1, kLandedBar = 5;             // named barriers: P of [lane][buffer] is stored; loads are in
 constexpr float kNaN = __builtin_nanf("");
+constexpr float kFarPast = 0x1p12f;   // sum of a step's weights past which a row takes a new reference maximum
 
 // The cost of a unit: kTile for each key tile (two lanes' products; or one row
 // tile's, whose time is its bytes'), and for its start and end kExtra.
@@ -89,6 +89,11 @@ struct Start {
 
 template <int D, int LANES>
 struct Cfg {
+  // warps behind the lanes' softmax warps
+  static constexpr int land_warp = 4 * LANES, load_warp = land_warp + 1, mma_warp = land_warp + 2, load_warp2 = land_warp + 3;
+  // 384 threads: 168 registers each at the launch.  256: they leave registers for a
+  // CTA of the merge, which then need not be launched when this kernel's have ended.
+  static constexpr int threads = 32 * (land_warp + 4);
   static constexpr int nb = LANES == 2 ? 1 : 2;      // S buffers per lane, and steps per tile
   static constexpr int step = TK / nb;               // keys per step
   static constexpr int nst = LANES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 6 : 12);   // K or V tiles in the ring
@@ -148,16 +153,18 @@ __device__ __forceinline__ int unit_cost(const PagedArgs& A, const Request& r, i
 // All units of a KV head, by one thread: few of them.
 template <int LANES>
 __device__ __forceinline__ long long head_cost(const PagedArgs& A, const Request& r) {
+  if constexpr (LANES == 1) return r.pairs ? unit_cost<LANES>(A, r, 0) : 0;   // (max_new fits a row tile)
   long long all = 0;
 #pragma unroll 1
   for (int p = 0; p < r.pairs; ++p) all += unit_cost<LANES>(A, r, p);
   return all;
 }
 constexpr int kFewPairs = 4;
+constexpr int kZeroTiles = 4;   // key tiles of a segment from which on its unused query rows are zeroed
 // The same by a whole warp, of a request that all its threads have.
 template <int LANES>
 __device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Request& r) {
-  if (r.pairs <= kFewPairs) return head_cost<LANES>(A, r);
+  if (LANES == 1 || r.pairs <= kFewPairs) return head_cost<LANES>(A, r);
   long long all = 0;
 #pragma unroll 1
   for (int p = threadIdx.x & 31; p < r.pairs; p += 32) all += unit_cost<LANES>(A, r, p);
@@ -179,7 +186,8 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
   for (int k = 0; k < per; ++k) {   // the lanes' k-th requests
     Request r{0, 0, 0, 0};
     if (b0 + k < A.B) r = request_of<LANES>(A, b0 + k);
-    if (r.pairs <= kFewPairs) mine += head_cost<LANES>(A, r) * A.hkv;
+    if (LANES == 1 || r.pairs <= kFewPairs) mine += head_cost<LANES>(A, r) * A.hkv;
+    if constexpr (LANES == 2)
     for (uint32_t many = __ballot_sync(0xffffffffu, r.pairs > kFewPairs); many; many &= many - 1) {
       const int src = __ffs(many) - 1;
       const Request x{0, __shfl_sync(0xffffffffu, r.n, src), __shfl_sync(0xffffffffu, r.kv, src),
@@ -216,13 +224,17 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
   s.g = int(quot(at, head));
   at -= s.g * head;
   int cost = 0;
-  for (; s.p < r.pairs; s.p += 32) {
+  if constexpr (LANES == 1) {
+    cost = int(head);
+    s.at = int(at);
+  }
+  for (; LANES == 2 && s.p < r.pairs; s.p += 32) {
     const int p = s.p + lane;
     cost = p < r.pairs ? unit_cost<LANES>(A, r, p) : 0;
-    long long upto = cost;
+    int upto = cost;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+      const int y = __shfl_up_sync(0xffffffffu, upto, x);
       if (lane >= x) upto += y;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, at < upto);
@@ -339,7 +351,7 @@ struct Walk {
 };
 
 template <int D, int LANES>
-__global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ PagedArgs A) {
+__global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const __grid_constant__ PagedArgs A) {
   using C = Cfg<D, LANES>;
   constexpr int NST = C::nst, NB = C::nb, SK = C::step;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -387,7 +399,13 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
     prefetch_tensormap(&A.kmap);
     prefetch_tensormap(&A.vmap);
   }
-  if (warp == kMmaWarp) {
+  // Query rows that no load writes are zeros: the tensor core takes less power for
+  // them, and under the power limit that is time.
+  for (int x = A.qt * G * 8 + tid; x < TK * 8; x += C::threads)
+    for (int h = 0; h < LANES * (D / 64); ++h)
+      *reinterpret_cast<uint4*>(smem + uint32_t(h) * C::panel + x * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  if (warp == C::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -458,30 +476,54 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
           const uint32_t sb = s_tmem + uint32_t((j0 + i) % NB * SK);
           wait_s(j0 + i);
           tc_fence_after();
-          float x[SK];
+          float alpha = 1.f, step = 0.f;
+          uint32_t pk[SK / 2];
+          // P of this step against the reference maximum.  Rows with `mine` take the
+          // step's maximum first: those that have none yet, and, the second time, those
+          // whose weights came out too large for the one they have (sums and O are fp32
+          // and the rounding of P is relative, so until then it needs no change).
+          bool mine = act && mref == -INFINITY;
+#pragma unroll 1
+          for (int time = 0;; ++time) {
+            float x[SK];
 #pragma unroll
-          for (int c = 0; c < SK; c += 64) tc_ld64(sb + uint32_t(c), reinterpret_cast<uint32_t*>(x + c));
-          if (nv < SK) {
+            for (int c = 0; c < SK; c += 64) tc_ld64(sb + uint32_t(c), reinterpret_cast<uint32_t*>(x + c));
+            if (nv < SK) {
 #pragma unroll
-            for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
+              for (int j = 0; j < SK; ++j) x[j] = j < nv ? x[j] : -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, mine)) {
+              float m4[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) m4[y] = fmaxf(x[2 * y], x[2 * y + 1]);
+#pragma unroll
+              for (int j = 8; j < SK; j += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) m4[y] = max3(m4[y], x[j + 2 * y], x[j + 2 * y + 1]);
+              const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * scale;
+              if (mine && mx > mref) {
+                alpha = fast_exp2(mref - mx);   // 0 while mref is -inf
+                mref = mx;
+              }
+            }
+            // (the weights of a row that is not in use are 0, which costs the product less power)
+            const float nb = !act ? -INFINITY : mref == -INFINITY ? 0.f : -mref;
+            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+            for (int j = 0; j < SK; j += 4) {
+              float* y = x + j;
+              fma2(y[0], y[1], scale, nb);
+              fma2(y[2], y[3], scale, nb);
+              const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]), p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
+              add2(l0, l1, p0, p1);
+              add2(l2, l3, p2, p3);
+              pk[j / 2] = pack_bf16(p0, p1);
+              pk[j / 2 + 1] = pack_bf16(p2, p3);
+            }
+            step = (l0 + l1) + (l2 + l3);
+            mine = act && !mine && !(step <= kFarPast);
+            if (time > 0 || !__any_sync(0xffffffffu, mine)) break;
           }
-          float m4[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) m4[y] = fmaxf(x[2 * y], x[2 * y + 1]);
-#pragma unroll
-          for (int j = 8; j < SK; j += 8)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) m4[y] = max3(m4[y], x[j + 2 * y], x[j + 2 * y + 1]);
-          const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-          // (a row that is not in use never rescales O; its P and O are never read)
-          const float mx = act ? top * scale : -INFINITY;
-          float alpha = 1.f;
-          if (mx > mref + 8.f) {
-            alpha = fast_exp2(mref - mx);   // 0 while mref is -inf
-            mref = mx;
-            lsum *= alpha;
-          }
-          const float nb = mref == -INFINITY ? 0.f : -mref;
           // rescale this row of O once P V of the step before is in (NB = 1: it
           // came with S of this step; NB = 2: it comes with S of the next one, or
           // alone after the last)
@@ -500,25 +542,10 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
               tc_st32(o_tmem + uint32_t(c), o);
             }
           }
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-          for (int h = 0; h < SK / 32; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float* y = x + 32 * h + j;
-              fma2(y[0], y[1], scale, nb);
-              fma2(y[2], y[3], scale, nb);
-              const float p0 = fast_exp2(y[0]), p1 = fast_exp2(y[1]), p2 = fast_exp2(y[2]), p3 = fast_exp2(y[3]);
-              add2(l0, l1, p0, p1);
-              add2(l2, l3, p2, p3);
-              pk[j / 2] = pack_bf16(p0, p1);
-              pk[j / 2 + 1] = pack_bf16(p2, p3);
-            }
-            tc_st16(sb + uint32_t(16 * h), pk);
-          }
+          for (int h = 0; h < SK / 32; ++h) tc_st16(sb + uint32_t(16 * h), pk + 16 * h);
           tc_wait_st();
-          lsum += (l0 + l1) + (l2 + l3);
+          lsum = fmaf(lsum, alpha, step);
           tc_fence_before();
           named_arrive(kPBar + 2 * ln + (j0 + i) % NB, 32 * n_act + 32);
         }
@@ -609,10 +636,10 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   } else {
     if constexpr (LANES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     w.init(A, *start);
-    if (warp == kLoadWarp || warp == kLoadWarp2) {
+    if (warp == C::load_warp || warp == C::load_warp2) {
       // ================================================================ loads
       // (both warps follow every phase of every stage; the first alone arms them)
-      const bool lead = warp == kLoadWarp;
+      const bool lead = warp == C::load_warp;
       const int box = min(A.page, TK);                  // rows of a load
       int gi = 0, st = 0, segs = 0;
       uint32_t ph = 0;                                  // of stage st
@@ -702,7 +729,7 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
         }
       }
       __syncwarp();
-    } else if (warp == kLandWarp) {
+    } else if (warp == C::land_warp) {
       // ============================================================ landings
       // waits for what the products read and lets the MMA warp go on by a named barrier:
       // a wait on an mbarrier by that warp would stand behind its queued products
@@ -732,6 +759,14 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       };
       for (; w.left > 0; w.next(A)) {
         wait_warp(q_full, uint32_t(segs++) & 1u);
+        if (LANES == 2 && !w.two && w.n >= kZeroTiles) {   // rows of other requests' tokens, as above
+          for (int x = (w.r.n - w.first(A)) * G * 8 + lane_id; x < TK * 8; x += 32)
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              *reinterpret_cast<uint4*>(smem + uint32_t(h) * C::panel + x * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          __syncwarp();
+        }
         const int nv = max(w.r.kv - (w.i0 + w.n - 1) * TK, 0);   // rows of the segment's last tile
         // K(0), then K(i), V(i - 1) for each tile, V(n - 1)
         const bool halves = LANES == 2 && !w.two;
@@ -754,7 +789,7 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
       }
       __syncwarp();
     } else {
-      if (warp == kMmaWarp) {
+      if (warp == C::mma_warp) {
         // ================================================================ MMAs
         constexpr uint32_t kIdS = tc_idesc(128, SK, 0), kIdPV = tc_idesc(128, D, 1);
         const uint64_t q_desc = tc_desc(sbase, 16, 1024);
@@ -842,7 +877,7 @@ __global__ void __launch_bounds__(NTH, 1) paged_kernel(const __grid_constant__ P
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp)
+  if (warp == C::mma_warp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
@@ -947,7 +982,7 @@ cudaError_t launch_t(const PagedArgs& a, int num_sms, cudaStream_t stream) {
       done, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::total)); });
   if (attr != cudaSuccess) return attr;
   const int grid = num_sms < kPagedGridMax ? num_sms : kPagedGridMax;
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(NTH), C::total, stream, a);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(C::threads), C::total, stream, a);
   if (e != cudaSuccess) return e;
   constexpr int block = Merge<D, LANES>::block;
   const int rows = LANES == 2 ? 2 * TK : a.qt * (a.hq / a.hkv);
