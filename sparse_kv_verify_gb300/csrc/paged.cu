@@ -354,6 +354,7 @@ template <int D, int LANES>
 __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const __grid_constant__ PagedArgs A) {
   using C = Cfg<D, LANES>;
   constexpr int NST = C::nst, NB = C::nb, SK = C::step;
+  constexpr bool LOW = LANES == 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
           wait_s(j0 + i);
           tc_fence_after();
           float alpha = 1.f, step = 0.f;
-          uint32_t pk[SK / 2];
+          uint32_t pk[SK / 2], lo[LOW ? SK / 2 : 1];
           // P of this step against the reference maximum.  Rows with `mine` take the
           // step's maximum first: those that have none yet, and, the second time, those
           // whose weights came out too large for the one they have (sums and O are fp32
@@ -519,6 +520,15 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               add2(l2, l3, p2, p3);
               pk[j / 2] = pack_bf16(p0, p1);
               pk[j / 2 + 1] = pack_bf16(p2, p3);
+              if constexpr (LOW) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  float r0 = z ? p2 : p0, r1 = z ? p3 : p1;
+                  const uint32_t h = pk[j / 2 + z];
+                  add2(r0, r1, -__uint_as_float(h << 16), -__uint_as_float(h & 0xFFFF0000u));
+                  lo[j / 2 + z] = pack_bf16(r0, r1);
+                }
+              }
             }
             step = (l0 + l1) + (l2 + l3);
             mine = act && !mine && !(step <= kFarPast);
@@ -543,7 +553,10 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
             }
           }
 #pragma unroll
-          for (int h = 0; h < SK / 32; ++h) tc_st16(sb + uint32_t(16 * h), pk + 16 * h);
+          for (int h = 0; h < SK / 32; ++h) {
+            tc_st16(sb + uint32_t(16 * h), pk + 16 * h);
+            if constexpr (LOW) tc_st16(sb + uint32_t(SK / 2 + 16 * h), lo + 16 * h);
+          }
           tc_wait_st();
           lsum = fmaf(lsum, alpha, step);
           tc_fence_before();
@@ -831,6 +844,11 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
                 for (int kk = 0; kk < SK / 16; ++kk)
                   tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(kk * 8), v + uint32_t(kk) * keys16, kIdPV,
                                   (acc || kk > 0) ? 1 : 0);
+                if constexpr (LOW)   // what the rounding of P left over
+#pragma unroll
+                  for (int kk = 0; kk < SK / 16; ++kk)
+                    tc_mma_ts_elect(tmem + uint32_t(kOCol + 128 * ln), sp + uint32_t(SK / 2 + kk * 8),
+                                    v + uint32_t(kk) * keys16, kIdPV, 1);
               }
               if (s) {
                 const uint64_t q = q_desc + uint64_t(HALVES ? 0 : ln) * (C::stage >> 4);
