@@ -598,7 +598,16 @@ class _CacheCall:
         self.ws = ws
         self._built_on, self._home = self._home, self._home.cuda_stream
         self._joined = set()   # streams that have waited for that one
-        self._fn = getattr(lib(), fn)
+        # the entry point without argument types: they are applied once, in _marshal
+        # (0.7 of 2.5 us of a call with nineteen arguments)
+        self._fn = lib()[fn]
+        self._fn.restype = ctypes.c_int
+        self._carg = None
+
+    def _marshal(self):
+        types = getattr(lib(), self._name).argtypes
+        self._carg = tuple(t.from_param(a) for t, a in zip(types, self._args))
+        return self._carg
 
     def _join(self, other):
         """Lets ``other`` use the buffers that the call has allocated."""
@@ -622,11 +631,12 @@ class _CacheCall:
             s = stream.cuda_stream
         if s != self._home and self._own:
             self._join(stream or torch.cuda.current_stream(self.device))
+        args = self._carg or self._marshal()
         if torch.cuda.current_device() == self.device.index:
-            st = self._fn(*self._args, s)
+            st = self._fn(*args, c_void_p(s))
         else:
             with torch.cuda.device(self.device):
-                st = self._fn(*self._args, s)
+                st = self._fn(*args, c_void_p(s))
         if st != 0:
             raise DustinError(self._name, st)
         return self._result
