@@ -906,7 +906,7 @@ constexpr int kMergeThreads = 256;
 template <int D, int LANES>
 struct Merge {
   static constexpr int rows = LANES;                       // rows of a thread
-  static constexpr int depth = LANES == 1 ? 8 : 3;         // segments whose loads are in flight
+  static constexpr int depth = LANES == 1 ? 10 : 3;        // segments whose loads are in flight
   static constexpr int step = kMergeThreads / (D / 4);     // rows at a time
   static constexpr int block = rows * step;                // rows of a block
 };
