@@ -127,9 +127,10 @@ struct Request {
 template <int LANES>
 __device__ __forceinline__ Request request_of(const PagedArgs& A, int b) {
   Request r;
-  const int c1 = __ldg(A.cu + b + 1);
-  r.c0 = __ldg(A.cu + b);
-  r.kv = __ldg(A.kv_len + b);
+  // (plain loads: the kernel before this one may write these while this one waits for it)
+  const int c1 = A.cu[b + 1];
+  r.c0 = A.cu[b];
+  r.kv = A.kv_len[b];
   const bool ok = paged_ok(A, r.c0, c1, r.kv);
   r.n = ok ? c1 - r.c0 : 0;
   r.pairs = (r.n + LANES * A.nt - 1) / (LANES * A.nt);
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         const int32_t* table = A.table + size_t(w.b) * A.max_pages;
         // the table's entry for this thread in a tile, read a tile ahead of its use
         auto needs = [&](int i) { return i < w.n && lane_id * box < TK && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
-        auto page_at = [&](int i) { return needs(i) ? __ldg(table + ((w.i0 + i) * TK + lane_id * box) / A.page) : 0; };
+        auto page_at = [&](int i) { return needs(i) ? table[((w.i0 + i) * TK + lane_id * box) / A.page] : 0; };
         int ahead = page_at(0);
         // this segment's query tiles, once the last one's S MMAs have read theirs
         if (lead) {

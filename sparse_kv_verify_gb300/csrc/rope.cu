@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant
         for (int y = 1; y < LPH; y <<= 1) ss += __shfl_xor_sync(who, ss, y);
         const float r = rsqrtf(ss / D + A.eps);
         float wa[8], wb[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8 * c0)), wa);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8 * c1)), wb);
+        unpack8(*reinterpret_cast<const uint4*>(w + 8 * c0), wa);
+        unpack8(*reinterpret_cast<const uint4*>(w + 8 * c1), wb);
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
           a[y] *= r * wa[y];

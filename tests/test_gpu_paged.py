@@ -309,6 +309,67 @@ def test_attn_strided_pools(layout):
     assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
 
 
+@pytest.mark.parametrize("d,kl,vl", [(128, "head", "token"), (64, "token", "token"), (64, "padded", "head"), (128, "token", "padded")])
+def test_attn_pools_of_different_layouts(d, kl, vl):
+    x = Paged([300, 97, 64, 700], [4, 30, 1, 150], 8, 2, d, 32, seed=6)
+    ref = check_attn(x)
+    for name, layout in (("kc", kl), ("vc", vl)):
+        pool = x._pool(layout)
+        pool.copy_(getattr(x, name))
+        setattr(x, name, pool)
+    got = check_attn(x)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
+def test_attn_over_a_contiguous_cache():
+    """A contiguous cache is a pool of one page a sequence."""
+    B, hq, hkv, d, Lcap, kv, n = 3, 8, 2, 128, 384, [300, 7, 129], [1, 7, 60]
+    kc, vc = (torch.full((B, hkv, Lcap, d), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for b in range(B):
+        for t, s in ((kc, 1), (vc, 2)):
+            t[b, :, :kv[b]] = normal(10 * b + s, hkv, kv[b], d)
+    q, cu = normal(5, sum(n), hq, d, scale=2.0), np.concatenate([[0], np.cumsum(n)])
+    o, lse = dk.dustin_paged_attn(dk.Batch(B, sum(n), max(n), 1), q, kc, vc, i32([[0], [1], [2]]), i32(cu), i32(kv))
+    ro, rl, ra = O.paged_attn(to_bits(q), to_bits(kc), to_bits(vc), [[0], [1], [2]], cu, kv)
+    assert_attended(o, lse, ro, rl, ra, logit_error(q, *[kc[b, :, :kv[b]] for b in range(B)]), max(kv))
+
+
+@pytest.mark.parametrize("max_new", [1, 64])
+def test_attn_without_any_token(max_new):
+    """A captured batch with nothing in it: rows and flags are left alone."""
+    x = Paged([0, 0, 0], [0, 0, 0], 8, 2, 128, 16, pad=5)
+    for kv in ([0, 0, 0], [16, 0, 32]):
+        ws = workspace(x.batch(dk, max_new=max_new), 8, 2, 128)
+        o, lse = torch.full((5, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 8), 7.0, device="cuda")
+        dk.dustin_paged_attn(x.batch(dk, max_new=max_new), x.q, x.kc, x.vc, x.table, x.cu, i32(kv), o, lse, ws=ws)
+        assert dk.check(ws) == 0 and bool((o == 7).all()) and bool((lse == 7).all())
+
+
+def test_attn_without_lse():
+    import ctypes
+    x = Paged([100, 3000], [40, 2], 8, 2, 64, 32, seed=13)
+    ref = dk.dustin_paged_attn(x.batch(dk), x.q, x.kc, x.vc, x.table, x.cu, x.kv_len)
+    ws, o = workspace(x.batch(dk), 8, 2, 64), torch.empty_like(x.q)
+    bt, bd = x.batch(dk).c(), dk.binding
+    st = dk.lib().dustin_paged_attn(ctypes.byref(bt), 8, x.q.data_ptr(), bd.paged_view(x.kc), bd.paged_view(x.vc),
+                                    x.table.data_ptr(), x.cu.data_ptr(), x.kv_len.data_ptr(), o.data_ptr(), None, ws.ptr,
+                                    ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and dk.check(ws) == 0 and torch.equal(o, ref[0])
+
+
+def test_attn_scores_that_rise_and_fall():
+    """The largest scores come late, early, in steps far over the first ones', and
+    in one row of a warp only: the reference maximum has to follow."""
+    for d, new, page in ((64, 1, 16), (128, 6, 64), (128, 200, 128), (64, 90, 16)):
+        x = Paged([1500], [new], 8, 1, d, page, seed=31)
+        for at, f in ((40, 9.0), (300, 30.0), (301, 60.0), (900, 120.0), (1400, 3.0)):
+            j = int(x.table_host[0, at // page])
+            x.kc[j, 0, at % page] = (x.q[0, 3].float() * f / x.q[0, 3].float().norm()).to(torch.bfloat16)
+        check_attn(x)
+        x.q.mul_(0)          # and none at all
+        check_attn(x)
+
+
 def test_attn_many_requests_and_extreme_scores():
     """Ragged lengths over a large batch; scores far apart (up to about 150),
     so that the running maximum moves and most weights underflow."""
@@ -462,6 +523,27 @@ def test_attn_matches_the_contiguous_operators():
 
 
 # ---------------------------------------------------------------- together
+
+
+def test_large_batches_of_single_tokens():
+    """More requests than CTAs, and every length from 0 on."""
+    lens = list(range(0, 320))
+    x = Paged(lens, [1] * 320, 4, 2, 64, 16, seed=40)
+    ws = workspace(x.batch(dk), 4, 2, 64)
+    o, lse = dk.dustin_paged_attn(x.batch(dk), x.q, x.kc, x.vc, x.table, x.cu, x.kv_len, ws=ws)
+    assert dk.check(ws) == 0
+    for b in range(0, 320, 7):
+        for g in range(2):
+            q, k, (ro, rl, ra) = big_reference(x, b, g, 0, 1)
+            assert_attended(o[b, 2 * g:2 * g + 2], lse[b, 2 * g:2 * g + 2], ro.cpu().numpy(), rl.cpu().numpy(),
+                            ra.cpu().numpy(), logit_error(q, k), x.kv[b])
+
+
+def test_a_single_token_in_a_batch_that_allows_chunks():
+    """The same requests in both shapes of the kernel (the batch's max_new chooses)."""
+    x = Paged([0, 1, 500, 127, 128, 4000], [1] * 6, 16, 2, 128, 16, seed=41)
+    for max_new in (1, 16, 17, 4096):
+        check_attn(x, batch=dict(max_new=max_new)) if max_new > 1 else check_attn(x)
 
 
 def test_deterministic():
