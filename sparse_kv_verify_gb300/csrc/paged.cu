@@ -296,19 +296,23 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 
 // Groups of 8 rows (all columns, or 64) of a page: coordinates (x, row 0 of a
 // group, c2, c3, page).
+template <bool ONCE>   // rows that nobody else reads: they leave L2 first
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int c2, int c3, int page,
                                             uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(c2), "r"(c3), "r"(page), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
+  if constexpr (ONCE)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(c2), "r"(c3), "r"(page), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(c2), "r"(c3), "r"(page), "r"(smem_u32(bar))
+        : "memory");
 }
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
+
 
 // Walks this CTA's segments: key tiles [i0, i0 + n) of unit (b, g, p).
 template <int LANES>
@@ -659,9 +663,9 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
       // ================================================================ loads
       // (both warps follow every phase of every stage; the first alone arms them)
       const bool lead = warp == C::load_warp;
-      // rows that one unit alone reads (64 requests of 512 to 1024 rows 46.0 -> 43.8 us;
+      // rows that one unit alone reads leave L2 first (64 requests of 512 to 1024 rows 46.0 -> 43.8 us;
       // for the units of one row tile beside a chunk it was worse, 430 -> 449)
-      const uint64_t policy = LANES == 1 ? policy_evict_first() : policy_evict_normal();
+      const uint64_t policy = LANES == 1 ? policy_evict_first() : 0;
       const int box = min(A.page, TK);                  // rows of a load
       int gi = 0, st = 0, segs = 0;
       uint32_t ph = 0;                                  // of stage st
@@ -725,9 +729,9 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
             if (page >= 0) {
               const int h = lead ? 0 : 1;
               if (D == 64 || A.merged) {
-                if ((lane_id & 1) == h) tma_load_5d(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar, policy);
+                if ((lane_id & 1) == h) tma_load_5d<LANES == 1>(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar, policy);
               } else {
-                tma_load_5d(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar, policy);
+                tma_load_5d<LANES == 1>(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar, policy);
               }
             }
             if (tail) tail_ph ^= 1u << st;
