@@ -114,10 +114,22 @@ __device__ __forceinline__ float row_lse(float top, float sum, int position) {
   return sum != 0.f ? (top + log2f(sum)) * kLn2 : position >= 0 ? kNaN : -INFINITY;
 }
 
-// a / b, where both mostly fit 32 bits (a 64-bit division takes several times as long).
+// a / b for a, b >= 0, where both mostly fit 32 bits.  Otherwise bit by bit, in a
+// short loop: a 64-bit division's code, in all the places that divide, would push
+// the rest out of the instruction cache.
 __device__ __forceinline__ long long quot(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (long long)(uint32_t(a) / uint32_t(b));
-  return a / b;
+  unsigned long long q = 0, r = 0;
+#pragma unroll 1
+  for (int x = 63; x >= 0; --x) {
+    r = (r << 1) | ((unsigned long long)a >> x & 1u);
+    q <<= 1;
+    if (r >= (unsigned long long)b) {
+      r -= b;
+      q |= 1u;
+    }
+  }
+  return (long long)q;
 }
 
 // A request: its packed rows [c0, c0 + n), cache rows, units of a KV head.
@@ -284,8 +296,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // the named barriers, which know no limit, are all met.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  if (*abort) return false;
-  return mbar_wait(bar, parity, err, abort);
+  return !*abort && mbar_wait(bar, parity, err, abort);
 }
 __device__ __forceinline__ void named_arrive(int id, int threads) {
   asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -423,19 +434,19 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
   }
   pdl_launch_dependents();
   pdl_wait();
-  if (warp == 0) {
+  if (warp < 2) {   // the share's start and its end
     Start s;
-    s.from = cut_of<LANES>(A, 0, s);
+    const Cut cut = cut_of<LANES>(A, warp, s);
     if (lane_id == 0) {
-      start->from = s.from;
-      start->total = s.total;
-      start->ctas = s.ctas;
-      start->snap = s.snap;
+      if (warp == 0) {
+        start->from = cut;
+        start->total = s.total;
+        start->ctas = s.ctas;
+        start->snap = s.snap;
+      } else {
+        start->to = cut.pos;
+      }
     }
-  } else if (warp == 1) {
-    Start s;
-    const Cut to = cut_of<LANES>(A, 1, s);
-    if (lane_id == 0) start->to = to.pos;
   } else if (warp == 2 && blockIdx.x == 0) {
     for (int b = lane_id; b < A.B; b += 32)
       if (!paged_ok(A, A.cu[b], A.cu[b + 1], A.kv_len[b])) flag_error(A.err, DUSTIN_DEV_SEQLEN);
@@ -672,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
       uint32_t tails = 0, tail_ph = 0;                  // stages whose latest load is waited for by `landed`; its phases
       bool live = true;
       auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-        return bool(__all_sync(0xffffffffu, mbar_wait(bar, parity, A.err, abort_flag)));
+        return bool(__all_sync(0xffffffffu, wait_on(bar, parity, A.err, abort_flag)));
       };
       for (; live && w.left > 0; w.next(A)) {
         const int32_t* table = A.table + size_t(w.b) * A.max_pages;
@@ -765,24 +776,6 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         wait_on(bar, parity, A.err, abort_flag);
         __syncwarp();
       };
-      auto ready = [&](bool tail, int nv) {   // load gi
-        const int st = gi % NST;
-        if (tail) {
-          wait_warp(&landed[st], (tail_ph >> st) & 1u);
-          tail_ph ^= 1u << st;
-          unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
-          const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)   // 16 bytes each, 64 of them a group
-              *reinterpret_cast<uint4*>(rows + h * panel + (x >> 6) * group + (x & 63) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();
-          if (lane_id == 0) mbar_arrive(&full[st]);   // every load is a phase of `full`
-        } else {
-          wait_warp(&full[st], uint32_t(gi / NST) & 1u);
-        }
-        ++gi;
-      };
       for (; w.left > 0; w.next(A)) {
         wait_warp(q_full, uint32_t(segs++) & 1u);
         if (LANES == 2 && !w.two && w.n >= kZeroTiles) {   // rows of other requests' tokens, as above
@@ -794,23 +787,29 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
           __syncwarp();
         }
         const int nv = max(w.r.kv - (w.i0 + w.n - 1) * TK, 0);   // rows of the segment's last tile
-        // K(0), then K(i), V(i - 1) for each tile, V(n - 1)
         const bool halves = LANES == 2 && !w.two;
-        if (!halves) {
-          ready(false, 0);
-          named_sync(kLandedBar, 64);
-          for (int i = 0; i < w.n; ++i) {
-            if (i + 1 < w.n) ready(false, 0);
-            ready(i + 1 == w.n && nv < TK, nv);
-            named_sync(kLandedBar, 64);
+        // K(0), then K(i), V(i - 1) for each tile, V(n - 1)
+#pragma unroll 1
+        for (int t = 0; t < 2 * w.n; ++t, ++gi) {
+          const int st = gi % NST;
+          const bool is_v = t == 2 * w.n - 1 || (t > 0 && !(t & 1));
+          if (t == 2 * w.n - 1 && nv < TK) {
+            wait_warp(&landed[st], (tail_ph >> st) & 1u);
+            tail_ph ^= 1u << st;
+            unsigned char* rows = smem + C::ring_off + uint32_t(st) * C::stage;
+            const uint32_t panel = A.merged ? 1024 : C::panel, group = A.merged ? (D / 64) * 1024 : 1024;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              for (int x = nv * 8 + lane_id; x < TK * 8; x += 32)   // 16 bytes each, 64 of them a group
+                *reinterpret_cast<uint4*>(rows + h * panel + (x >> 6) * group + (x & 63) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane_id == 0) mbar_arrive(&full[st]);   // every load is a phase of `full`
+          } else {
+            wait_warp(&full[st], uint32_t(gi / NST) & 1u);
           }
-        } else {
-          for (int j = -2; j < w.n; ++j) {
-            if (j < 0 && j + 2 >= w.n) continue;
-            if (j >= 0) ready(j + 1 == w.n && nv < TK, nv);
-            if (j + 2 < w.n) ready(false, 0);
-            named_sync(kLandedBar, 64);
-          }
+          // a batch takes K(i + 1) and V(i), or, where the lanes share the tiles, V(i) and K(i + 2)
+          if (t == 0 || (halves ? !is_v || t >= 2 * w.n - 2 : is_v)) named_sync(kLandedBar, 64);
         }
       }
       __syncwarp();
@@ -874,13 +873,12 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               tc_commit_elect(s ? &s_full[2 * ln + buf] : &o_full[2 * ln + buf]);   // (n is even where NB = 2)
             };
             if constexpr (HALVES) {
-              if (pv || s) {
-                if (i & 1) batch(1, 0);
-                else batch(0, 0);
-              }
+              if (pv || s) batch(i & 1, 0);
+            } else if constexpr (LANES == 2) {
+              batch(0, 0);
+              if (two) batch(1, 0);
             } else {
-              batch(0, NB == 1 ? 0 : i & 1);   // (step i and step i + NB have one buffer)
-              if (LANES == 2 && two) batch(1, 0);
+              batch(0, i & 1);   // (step i and step i + NB have one buffer)
             }
             if (pv && last) tc_commit_elect(&empty[sv]);
             if (s && last) tc_commit_elect(&empty[sk]);
