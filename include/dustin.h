@@ -473,7 +473,8 @@ int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const
  *             number, so that a contiguous cache [B][hkv][Lcap][d] is a pool of B
  *             pages of Lcap rows, with slot = b * Lcap + position
  * Everything is fp32 with one rounding at the end; turns are reduced exactly (64-bit
- * fractions of a turn), so that far positions lose nothing. */
+ * fractions of a turn), so that far positions lose nothing.  A normed head's sum of
+ * squares has to stay within fp32's range (elements below about 2^60). */
 int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, const void* k,
                      int64_t k_stride, const void* v, int64_t v_stride, const void* q_w, const void* k_w,
                      const float* inv_freq, const int32_t* pos, const int32_t* slot, void* q_out,
@@ -495,7 +496,10 @@ int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, cons
  * kv_len[b] may hold anything; keys and values below it must be finite.  A query
  * row that is not finite and sees a key gives NaN in its own o and lse.  Softmax
  * weights are rounded to bf16 for the product with v, each by at most 2^-8 of
- * itself, and o once more; their sum, and so lse, takes them unrounded in fp32.
+ * itself (2^-16 where max_new * hq / hkv <= 128), and o once more; their sum, and so
+ * lse, takes them unrounded in fp32.  The order of the fp32 sums goes by the whole
+ * batch: a request's bits may differ between batches, not between runs of one.
+ * max_new and N shape the launch; both may be larger than what a batch brings.
  * `page` is 16, 32, 64 or a multiple of 128 (DUSTIN_EINVAL).  o and lse are no
  * input's memory (DUSTIN_EINVAL). */
 int dustin_paged_attn(const dustin_batch* bt, int32_t hq, const void* q, dustin_paged_kv kc,

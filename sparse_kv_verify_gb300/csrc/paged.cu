@@ -13,14 +13,16 @@
 // prompts load the SMs alike; a cut near the end of a unit is moved there.  K and V
 // rows are read once per pair of row tiles.
 //
-// Roles (handing over through mbarriers):
+// Roles (handing over through mbarriers and named barriers):
 //   warps 0-3, 4-7  softmax of row tile 0 and 1 ("lanes"), one thread per row: a
 //                   step's scores in registers, P (bf16) stored over them.  The
 //                   reference maximum is the first step's; a later step is weighed
 //                   against it at once, and only where a row's weights sum to more
 //                   than 2^12 again against a new one, with which the thread rescales
-//                   its row of O.  P is rounded to bf16 for the second product; the
-//                   row sum adds the unrounded fp32 values, so lse keeps fp32 accuracy;
+//                   its row of O (looking for each step's maximum first took 2.48
+//                   instead of 2.39 ms for 4096 tokens over 28 K).  P is rounded to
+//                   bf16 for the second product; the row sum adds the unrounded fp32
+//                   values, so lse keeps fp32 accuracy;
 //   two warps       K and V tiles into a ring of 128-row stages, a page's rows in one
 //                   tiled TMA load, the pages of a tile by as many threads, half
 //                   of them by each warp (a load takes about 95 cycles, however
@@ -42,12 +44,28 @@
 // lane's products.  A unit with one row tile (single tokens beside a chunk) gives
 // every other key tile to lane 1, and lane 0 adds both lanes up at its end.
 // Batches of one row tile each: one lane, steps of 64 keys with two S buffers
-// (NB = 2).
+// (NB = 2).  Bytes bound them, so the second product is taken twice there, of P and
+// of what P's rounding left over: o's error is its own rounding's (0.0017 of o
+// against float64, with P alone 0.0019 to 0.0027; 243 instead of 242 us for the case
+// below).
 //
 // Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
 // [256, 256 + D) and [384, 384 + D).  A segment that covers its unit writes o and
 // lse.  Otherwise its row maxima, sums and unnormalised O go to a slot of its CTA
-// (0: the unit began in an earlier CTA, 1: here), and a second kernel merges them.
+// (0: the unit began in an earlier CTA, 1: here), and a second kernel merges them (a
+// unit's last CTA merging it in this kernel took 22 us longer for prompts, and 1 for
+// a token).
+//
+// What bounds it, 64/8/128:
+//   draft blocks of 16 requests over up to 32 K rows: the bytes, 241 us for 1.61 GB
+//   (6.7 TB/s, the rate of a plain copy);
+//   a 4096-token chunk over 28 K: 2.39 ms, 1.72 PFLOP/s (0.90 of cuBLAS's measured
+//   rate) while the clock holds; run on end it meets the power limit, 2.72 ms (cuBLAS
+//   then falls to 0.89 of its rate, too).  A step of both lanes takes 2900 cycles
+//   for 2048 of products: the chain of a lane, products -> S -> softmax (1300 to
+//   1500) -> P, is longer than the other lane's products hide;
+//   short prompts: about 3.5 us for a unit's start and end, as much as 2.5 tiles;
+//   one token over 4 K: 13 us, the latency of two launches.
 #include <type_traits>
 
 #include "common.cuh"
@@ -64,8 +82,10 @@ constexpr int kPBar = 1, kLandedBar = 5;             // named barriers: P of [la
 constexpr float kNaN = __builtin_nanf("");
 constexpr float kFarPast = 0x1p12f;   // sum of a step's weights past which a row takes a new reference maximum
 
-// The cost of a unit: kTile for each key tile (two lanes' products; or one row
-// tile's, whose time is its bytes'), and for its start and end kExtra.
+// The cost of a unit: `tile` for each key tile (two lanes' products; or one row
+// tile's, whose time is its bytes'), and for its start and end `extra`.  Fitted to
+// the CTAs' times over batches of prompts and of single tokens beside a chunk: two
+// lanes 1.4 us a tile and 3.5 a unit, one row tile 1.3 and 1.5.
 template <int LANES>
 struct Cost {
   static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 8 : 7; }
@@ -173,7 +193,7 @@ __device__ __forceinline__ long long head_cost(const PagedArgs& A, const Request
   return all;
 }
 constexpr int kFewPairs = 4;
-constexpr int kZeroTiles = 4;   // key tiles of a segment from which on its unused query rows are zeroed
+constexpr int kZeroTiles = 4;   // key tiles of a segment from which on its unused query rows are zeroed (0.3 us)
 // The same by a whole warp, of a request that all its threads have.
 template <int LANES>
 __device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Request& r) {
