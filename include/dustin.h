@@ -78,6 +78,7 @@ typedef enum {
 #define DUSTIN_MAX_LCAP (1 << 20)   /* positions per cache */
 #define DUSTIN_MAX_REQUESTS 8192    /* requests per paged-cache call */
 #define DUSTIN_MAX_TOKENS (1 << 20) /* packed token rows per paged-cache call */
+#define DUSTIN_MAX_HEADS 65536      /* query heads, and KV heads, per paged-cache call */
 
 /* A bf16 KV-cache view, element (b, g, pos, j) at
  *   ptr + b*sb + g*sh + pos*sl + j          (strides in elements).
@@ -447,8 +448,9 @@ size_t dustin_paged_workspace_bytes(const dustin_batch* bt, int32_t hq, int32_t 
  * is flagged (DUSTIN_DEV_PAGES) and left alone: nothing is given back or taken.
  * A table entry outside [0, n_pages) gives slot -1 and DUSTIN_DEV_INDEX.  A page
  * belongs to one request: tables that share pages are not for this call, which
- * would give such a page back twice.  `page` is any positive number.  No two of
- * the buffers may be the same (DUSTIN_EINVAL). */
+ * would give such a page back twice.  `page` is any positive number, and the
+ * table has fewer than 2^31 entries (DUSTIN_ERANGE).  No two of the buffers may be
+ * the same (DUSTIN_EINVAL). */
 int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const int32_t* seq_len,
                     const int32_t* n_new, int32_t* table, int32_t* held, int32_t* free_list,
                     int32_t* n_free, int32_t* cu, int32_t* kv_len, int32_t* slot, int32_t* pos, void* ws,

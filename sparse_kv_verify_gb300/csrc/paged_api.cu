@@ -32,7 +32,7 @@ bool pools_match(const dustin_paged_kv& k, const dustin_paged_kv& v) {
 
 int attn_shape(int32_t hq, int32_t hkv, int32_t d) {
   if (hkv < 1 || hq < 1 || hq % hkv || (d != 64 && d != 128)) return DUSTIN_EINVAL;
-  return hq / hkv > DUSTIN_MAX_QROWS ? DUSTIN_ERANGE : DUSTIN_OK;
+  return hq / hkv > DUSTIN_MAX_QROWS || hq > DUSTIN_MAX_HEADS ? DUSTIN_ERANGE : DUSTIN_OK;
 }
 
 // Workspace of the attention, after the fixed part: the units that CTAs start and
@@ -67,6 +67,7 @@ int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const
   if (st != DUSTIN_OK) return st;
   if (page < 1 || n_pages < 1) return DUSTIN_EINVAL;
   if (int64_t(bt->max_pages) * page > DUSTIN_MAX_LCAP) return DUSTIN_ERANGE;
+  if (int64_t(bt->B) * bt->max_pages >= (int64_t(1) << 31)) return DUSTIN_ERANGE;   // (sums of pages are 32 bits)
   if (int64_t(n_pages) * page >= (int64_t(1) << 31)) return DUSTIN_ERANGE;
   const void* bufs[] = {seq_len, n_new, table, held, free_list, n_free, cu, kv_len, slot, pos};
   constexpr int n = sizeof(bufs) / sizeof(bufs[0]);
@@ -110,7 +111,7 @@ int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, cons
     return DUSTIN_EINVAL;
   if (!pool_ok(kc) || !pool_ok(vc) || !pools_match(kc, vc) || kc.ptr == vc.ptr) return DUSTIN_EINVAL;
   if (r->rot < 0 || r->rot > kc.d || r->rot % 16 || (r->rot && !inv_freq)) return DUSTIN_EINVAL;
-  if (r->N > DUSTIN_MAX_TOKENS) return DUSTIN_ERANGE;
+  if (r->N > DUSTIN_MAX_TOKENS || r->hq > DUSTIN_MAX_HEADS || kc.hkv > DUSTIN_MAX_HEADS) return DUSTIN_ERANGE;
   const int64_t wq = int64_t(r->hq) * kc.d, wk = int64_t(kc.hkv) * kc.d;
   if (q_stride < wq || q_out_stride < wq || k_stride < wk || v_stride < wk) return DUSTIN_EINVAL;
   if (q_stride % 8 || q_out_stride % 8 || k_stride % 8 || v_stride % 8) return DUSTIN_EINVAL;

@@ -192,7 +192,7 @@ def check_rope(x, q, k, v, w, pos, slot, inv, rot, interleaved=False, eps=1e-6, 
     (96, 64, 8, 128, 64, 128, False, "padded", True), (33, 8, 8, 128, 128, 64, False, "token", True),
     (130, 3, 1, 128, 1, 16, True, "head", True), (61, 5, 5, 64, 24, 48, False, "head", False),
     (9, 128, 1, 64, 100, 16, False, "padded", False), (1001, 16, 4, 128, 256, 112, True, "head", True),
-    (4, 2, 1, 64, 16, 0, False, "head", True), (300, 48, 2, 64, 16, 64, True, "token", True)])
+    (4, 2, 1, 64, 16, 0, False, "head", True), (300, 40, 2, 64, 16, 64, True, "token", True)])
 def test_rope_parity(N, hq, hkv, d, page, rot, interleaved, layout, fused):
     for norm in (True, False):
         c = rope_case(N, hq, hkv, d, page, rot, N + hq, layout=layout, fused=fused)

@@ -150,6 +150,7 @@ def test_page_map_refusals(L):
     for o in BIG_BATCH + [dict(max_pages=(1 << 16) + 1)]:
         assert call(_batch(bd, **o)) == -2, o
     assert call(n_pages=1 << 27) == -2
+    assert call(_batch(bd, B=2048, max_pages=1 << 20), page=1) == -2   # a table of 2^31 entries
     assert call(ws=None) == -5 and call(ws=0x100008) == -5 and call(nbytes=1000) == -5
     assert lib.dustin_page_map(None, 16, 64, *range(0x1000, 0xB000, 0x1000), 0x100000, 1 << 20, None) == -1
 
@@ -169,6 +170,8 @@ def test_norm_rope_refusals(L):
               dict(eps=math.nan), dict(eps=math.inf)]:
         assert call(r) == -1, r
     assert call(dict(N=(1 << 20) + 1)) == -2
+    assert call(dict(hq=65537), qs=1 << 24, os=1 << 24) == -2
+    assert call(ks=1 << 24, vs=1 << 24, kc=_pool(bd, hkv=65537), vc=_pool(bd, ptr=0x20000, hkv=65537)) == -2
     for o in [dict(q=None), dict(q=0x1008), dict(qs=8184), dict(qs=8196), dict(k=None), dict(ks=1016), dict(v=0x3004),
               dict(vs=0), dict(qw=0x4008), dict(kw=0x5002), dict(f=None), dict(f=0x6002), dict(pos=None), dict(slot=None),
               dict(slot=0x8001), dict(out=None), dict(os=8), dict(out=0x1000, os=8200), dict(out=0x2000), dict(out=0x3000),
@@ -205,6 +208,7 @@ def test_paged_attn_refusals(L):
     for o in BIG_BATCH + [dict(max_pages=(1 << 16) + 1)]:
         assert call(_batch(bd, **o)) == -2, o
     assert call(hq=8 * 129) == -2
+    assert call(hq=65537, kc=_pool(bd, hkv=65537), vc=_pool(bd, ptr=0x20000, hkv=65537)) == -2
     assert call(ws=None) == -5 and call(nbytes=1000) == -5
 
 
