@@ -14,8 +14,9 @@
 // its upper 32 bits are the half-turns in [-1, 1) that sincospif takes.
 //
 // Bound by the bytes: each row is read and written once.  16384 tokens, 64/8/128:
-// 112 us for 671 MB, 6.0 TB/s (0.88 of a plain copy's rate).  One token: 2.6 us, the
-// latency of one launch.
+// 104 us for 671 MB, 6.4 TB/s (a plain copy of as many bytes takes 101).  Two elements
+// an instruction (f32x2) where the layout allows it: one at a time the issue of
+// instructions cost 8 us more.  One token: 2.4 us, the latency of one launch.
 #include <algorithm>
 
 #include "common.cuh"
@@ -28,23 +29,45 @@ namespace {
 constexpr int NTH = 128, kPerSm = 8;   // threads of a CTA, CTAs per SM
 constexpr int kTokensMax = 32;   // tokens of a CTA at most
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* x) {
+// Two floats for the packed instructions.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void halves(f32x2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void unpack8(const uint4& u, f32x2* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const f32x2* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    halves(x[i], a, b);
+    w[i] = pack_bf16(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // CTA (x, y): tokens [x tb, (x + 1) tb), every gridDim.y-th run of heads.
 template <int D>
 __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant__ RopeArgs A, int tb) {
   constexpr int LPH = D / 16, GROUPS = NTH / LPH;   // lanes per head, heads at a time
-  extern __shared__ float2 cs[];                    // [tb][rot / 2]
+  extern __shared__ __align__(16) float cs[];       // [tb]: cosines [rot / 2], sines [rot / 2], in an order of `place`
   __shared__ int2 rows[kTokensMax];                 // page and row of the cache, or -1
   const int tid = threadIdx.x, i0 = blockIdx.x * tb, nt = min(tb, A.N - i0);
   const int half = A.rot / 2, heads = A.hq + 2 * A.hkv;
@@ -56,6 +79,9 @@ __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant
     c0 = lane;
     c1 = turned + lane;
   }
+  // where a pair's angle is: a lane's eight as two runs of four, so that the lanes'
+  // 16-byte loads are next to one another
+  auto place = [&](int j) { return A.interleaved ? j : ((j >> 2) & 1) * (half / 2) + (j >> 3) * 4 + (j & 3); };
   auto load = [&](int t, int h, uint4& u0, uint4& u1) {
     const int64_t i = i0 + t;
     const uint16_t* src = h < A.hq           ? A.q + i * A.qst + h * D
@@ -84,7 +110,9 @@ __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant
     const long long turn = (long long)(one * (unsigned long long)(long long)A.pos[i0 + tx]);
     float s, c;
     sincospif(float(int(turn >> 32)) * 0x1p-31f, &s, &c);
-    cs[x] = make_float2(c, s);
+    float* at = cs + tx * A.rot + place(j);
+    at[0] = c;
+    at[half] = s;
   }
   if (tid < nt) {
     const int s = A.slot[i0 + tid];
@@ -102,45 +130,60 @@ __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant
     if (tn < nt) load(tn, hn, n0, n1);
     const bool is_q = h < A.hq, is_v = h >= A.hq + A.hkv;
     if (!is_v) {
-      float a[8], b[8];
+      f32x2 a[4], b[4];
       unpack8(u0, a);
       unpack8(u1, b);
       const uint16_t* w = is_q ? A.q_w : A.k_w;
       if (w) {
-        float ss = 0.f;
+        f32x2 sa = mul2(a[0], a[0]), sb = mul2(b[0], b[0]);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) ss = fmaf(a[y], a[y], fmaf(b[y], b[y], ss));
+        for (int y = 1; y < 4; ++y) {
+          sa = fma2(a[y], a[y], sa);
+          sb = fma2(b[y], b[y], sb);
+        }
+        float s0, s1, s2, s3;
+        halves(sa, s0, s1);
+        halves(sb, s2, s3);
+        float ss = (s0 + s1) + (s2 + s3);
 #pragma unroll
         for (int y = 1; y < LPH; y <<= 1) ss += __shfl_xor_sync(who, ss, y);
         const float r = rsqrtf(ss / D + A.eps);
-        float wa[8], wb[8];
+        const f32x2 r2 = pair(r, r);
+        f32x2 wa[4], wb[4];
         unpack8(*reinterpret_cast<const uint4*>(w + 8 * c0), wa);
         unpack8(*reinterpret_cast<const uint4*>(w + 8 * c1), wb);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          a[y] *= r * wa[y];
-          b[y] *= r * wb[y];
+        for (int y = 0; y < 4; ++y) {
+          a[y] = mul2(a[y], mul2(r2, wa[y]));
+          b[y] = mul2(b[y], mul2(r2, wb[y]));
         }
       }
       if (turns) {
-        const float2* at = cs + t * half;
+        const float* at = cs + t * A.rot;
         if (A.interleaved) {
+          auto turn = [&](f32x2& x, int j) {
+            const float c = at[j], s = at[half + j];
+            float x0, x1;
+            halves(x, x0, x1);
+            x = pair(x0 * c - x1 * s, x1 * c + x0 * s);
+          };
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const float2 p = at[4 * c0 + y], q = at[4 * c1 + y];
-            const float a0 = a[2 * y], a1 = a[2 * y + 1], b0 = b[2 * y], b1 = b[2 * y + 1];
-            a[2 * y] = a0 * p.x - a1 * p.y;
-            a[2 * y + 1] = a1 * p.x + a0 * p.y;
-            b[2 * y] = b0 * q.x - b1 * q.y;
-            b[2 * y + 1] = b1 * q.x + b0 * q.y;
+            turn(a[y], 4 * c0 + y);
+            turn(b[y], 4 * c1 + y);
           }
         } else {
+          const f32x2 minus = pair(-1.f, -1.f);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float2 p = at[8 * lane + y];
-            const float a0 = a[y], b0 = b[y];
-            a[y] = a0 * p.x - b0 * p.y;
-            b[y] = b0 * p.x + a0 * p.y;
+          for (int z = 0; z < 2; ++z) {
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(at + z * (half / 2) + 4 * lane);
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(at + half + z * (half / 2) + 4 * lane);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const f32x2 a0 = a[2 * z + y], b0 = b[2 * z + y], cy = y ? c.y : c.x, sy = y ? s.y : s.x;
+              a[2 * z + y] = fma2(mul2(b0, minus), sy, mul2(a0, cy));
+              b[2 * z + y] = fma2(a0, sy, mul2(b0, cy));
+            }
           }
         }
       }
@@ -170,8 +213,8 @@ cudaError_t launch_d(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   const int heads = a.hq + 2 * a.hkv;
   // Tokens and splits of the heads: as many CTAs as fill the SMs where the batch is
   // short, ten runs of heads for each where it is long.  us by tokens of a CTA,
-  // 64/8/128, 16384 tokens (5 runs of heads a token): 1 116, 2 112, 4 114, 6 116 (256
-  // threads: 135, 120, 116, 117); 14/2/64, 5003 tokens (1 run): 2 8.0, 4 7.7, 6 9.9.
+  // 64/8/128, 16384 tokens (5 runs of heads a token): 1 106.7, 2 104.4, 4 107.1;
+  // 14/2/64, 5003 tokens (1 run): 2 8.0, 4 7.7, 6 9.9.
   const long long runs = ((long long)a.N * heads + GROUPS - 1) / GROUPS, ctas = (long long)kPerSm * num_sms;
   const int tb = int(std::min<long long>({kTokensMax, std::max(1LL, (long long)a.N / ctas),
                                           std::max(1, 10 * GROUPS / heads)}));
@@ -179,7 +222,7 @@ cudaError_t launch_d(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.N + tb - 1) / tb, splits);
   cfg.blockDim = dim3(NTH);
-  cfg.dynamicSmemBytes = size_t(tb) * (a.rot / 2) * sizeof(float2);
+  cfg.dynamicSmemBytes = size_t(tb) * a.rot * sizeof(float);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
