@@ -15,8 +15,9 @@
 // pool, not from the table, so that slots need not wait for the tables.
 //
 // Bound by the latency of its chain (lengths -> sums -> pages -> slots): 16 requests
-// of one token 2.7 us; 256 requests with 32 K tokens, 4 K pages given back and 8 K
-// taken about 10 us (one CTA without the cluster: 41).
+// of one token 2.6 us; 256 requests with 32 K tokens, 4 K pages given back and 8 K
+// taken about 10 us (one CTA without the cluster: 41), 6.7 where none is given back
+// or taken (7.8 with the loops unrolled by 4: the code is fetched for one pass).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(NTH) page_map_kernel(const __grid_constant__ P
 
   // pages given back: entries past need, which is held less what is given back
   const int first = rank * NTH + tid, stride = ctas * NTH;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = first; i < rel_all; i += stride) {
     const int b = find(S.rel, B, i);
     const int end = b + 1 < B ? S.rel[b + 1] : rel_all, was = int(S.held[b] & 0x7FFFFFFFu);
@@ -183,13 +184,13 @@ __global__ void __launch_bounds__(NTH) page_map_kernel(const __grid_constant__ P
       __syncthreads();
     }
   }
-#pragma unroll 4
+#pragma unroll 1
   for (int i = first; i < taken; i += stride) {
     const int b = find(S.take, B, i);
     A.table[size_t(b) * A.max_pages + int(S.held[b] & 0x7FFFFFFFu) + (i - S.take[b])] = __ldcg(A.free_list + avail - 1 - i);
   }
   if (rank == 0 && tid == 0 && pool) *A.n_free = avail - taken;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = first; i < A.N; i += stride) {
     int p = 0, s = -1;
     if (i < tokens) {
