@@ -64,7 +64,9 @@
 //   then falls to 0.89 of its rate, too).  A step of both lanes takes 2900 cycles
 //   for 2048 of products: the chain of a lane, products -> S -> softmax (1300 to
 //   1500) -> P, is longer than the other lane's products hide;
-//   short prompts: about 3.5 us for a unit's start and end, as much as 2.5 tiles;
+//   short prompts: about 3.5 us for a unit's start and end, as much as 2.5 tiles; most of
+//   it is the fetching of code that runs once a unit, which is why loops off the path
+//   of a step are rolled (12 % of the code, 6 % of the time of 8 prompts);
 //   one token over 4 K: 13 us, the latency of two launches.
 #include <type_traits>
 
@@ -201,7 +203,7 @@ __device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Re
   long long all = 0;
 #pragma unroll 1
   for (int p = threadIdx.x & 31; p < r.pairs; p += 32) all += unit_cost<LANES>(A, r, p);
-#pragma unroll
+#pragma unroll 1
   for (int x = 16; x; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
   return all;
 }
@@ -216,11 +218,13 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
   const int lane = threadIdx.x & 31;
   const int per = (A.B + 31) / 32, b0 = lane * per;
   long long mine = 0;
+#pragma unroll 1
   for (int k = 0; k < per; ++k) {   // the lanes' k-th requests
     Request r{0, 0, 0, 0};
     if (b0 + k < A.B) r = request_of<LANES>(A, b0 + k);
     if (LANES == 1 || r.pairs <= kFewPairs) mine += head_cost<LANES>(A, r) * A.hkv;
     if constexpr (LANES == 2)
+#pragma unroll 1
     for (uint32_t many = __ballot_sync(0xffffffffu, r.pairs > kFewPairs); many; many &= many - 1) {
       const int src = __ffs(many) - 1;
       const Request x{0, __shfl_sync(0xffffffffu, r.n, src), __shfl_sync(0xffffffffu, r.kv, src),
@@ -230,7 +234,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
     }
   }
   long long inc = mine;
-#pragma unroll
+#pragma unroll 1
   for (int x = 1; x < 32; x <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, inc, x);
     if (lane >= x) inc += y;
@@ -248,6 +252,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
   const int src = __ffs(__ballot_sync(0xffffffffu, s.pos < inc)) - 1;
   long long at = s.pos - __shfl_sync(0xffffffffu, inc - mine, src), head = 0;
   Request r{};
+#pragma unroll 1
   for (s.b = src * per;; ++s.b) {
     r = request_of<LANES>(A, s.b);
     head = head_cost_warp<LANES>(A, r);
@@ -261,11 +266,12 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
     cost = int(head);
     s.at = int(at);
   }
+#pragma unroll 1
   for (; LANES == 2 && s.p < r.pairs; s.p += 32) {
     const int p = s.p + lane;
     cost = p < r.pairs ? unit_cost<LANES>(A, r, p) : 0;
     int upto = cost;
-#pragma unroll
+#pragma unroll 1
     for (int x = 1; x < 32; x <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, x);
       if (lane >= x) upto += y;
@@ -290,6 +296,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) 
       s.p = 0;
       if (++s.g == A.hkv) {
         s.g = 0;
+#pragma unroll 1
         do ++s.b;
         while (s.b < A.B && request_of<LANES>(A, s.b).n == 0);
       }
@@ -306,6 +313,12 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
+// (a, b) * (s, s)
+__device__ __forceinline__ void mul2(float& a, float& b, float s) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(s));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(b), "f"(c));
   return a;
@@ -647,25 +660,28 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         const size_t orow = size_t(w.r.c0 + (act ? tok : 0)) * A.hq + size_t(w.g) * G + row % G;
         const float inv = row_scale(lsum, position);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t o[64];
-          tc_ld64(o_tmem + uint32_t(c), o);   // collective: every lane loads
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc_ld32(o_tmem + uint32_t(c), o);   // collective: every lane loads
           if (join) {
-            uint32_t o1[64];
-            tc_ld64(o_tmem + uint32_t(128 + c), o1);
+            uint32_t o1[32];
+            tc_ld32(o_tmem + uint32_t(128 + c), o1);
 #pragma unroll
-            for (int y = 0; y < 64; ++y)
+            for (int y = 0; y < 32; ++y)
               o[y] = __float_as_uint(fmaf(__uint_as_float(o[y]), w0, __uint_as_float(o1[y]) * w1));
           }
           if (act && whole) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-              o[y] = pack_bf16(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+            for (int y = 0; y < 16; ++y) {
+              float2 p = make_float2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
+              mul2(p.x, p.y, inv);
+              o[y] = pack_bf16(p.x, p.y);
+            }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) store32(A.o + orow * D + c + 16 * y, o + 8 * y);
+            for (int y = 0; y < 2; ++y) store32(A.o + orow * D + c + 16 * y, o + 8 * y);
           } else if (act) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) store32(part + size_t(row) * D + c + 8 * y, o + 8 * y);
+            for (int y = 0; y < 4; ++y) store32(part + size_t(row) * D + c + 8 * y, o + 8 * y);
           }
         }
         if (join) {
@@ -853,6 +869,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
         auto segment = [&](auto halves, bool two) {
           constexpr bool HALVES = decltype(halves)::value;
+          constexpr int kUnroll = LANES == 2 ? 2 : 8;   // of S's products (8: prompts 225 instead of 212 us)
           constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
           const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
           int sv = 0, sk = 0;                     // stages of V and of K
@@ -885,7 +902,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               if (s) {
                 const uint64_t q = q_desc + uint64_t(HALVES ? 0 : ln) * (C::stage >> 4);
                 const uint64_t k = k_desc + uint64_t(sk) * (C::stage >> 4) + (first ? 0u : keys16 * (SK / 16));
-#pragma unroll
+#pragma unroll kUnroll
                 for (int kk = 0; kk < D / 16; ++kk)
                   tc_mma_ss_elect(sp, q + uint32_t(kk >> 2) * (C::panel >> 4) + uint32_t((kk & 3) * 2),
                                   k + uint32_t(kk >> 2) * kpanel + uint32_t((kk & 3) * 2), kIdS, kk > 0);
