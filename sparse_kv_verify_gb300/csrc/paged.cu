@@ -714,6 +714,12 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
       // for the units of one row tile beside a chunk it was worse, 430 -> 449)
       const uint64_t policy = LANES == 1 ? policy_evict_first() : 0;
       const int box = min(A.page, TK);                  // rows of a load
+      const int per_tile = TK / box, tiles = A.page / box;   // pages of a tile, and tiles of a page (one of them is 1)
+      // every other page by each warp, or a panel of each page
+      const bool panels = D == 128 && !A.merged;
+      const int h = lead ? 0 : 1, own_x = panels ? h * 64 : 0;
+      const bool own = panels || (lane_id & 1) == h;
+      const uint32_t own_off = panels ? uint32_t(lane_id * box * 128 + h * int(C::panel)) : uint32_t(lane_id * box * D * 2);
       int gi = 0, st = 0, segs = 0;
       uint32_t ph = 0;                                  // of stage st
       uint32_t tails = 0, tail_ph = 0;                  // stages whose latest load is waited for by `landed`; its phases
@@ -722,11 +728,11 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         return bool(__all_sync(0xffffffffu, wait_on(bar, parity, A.err, abort_flag)));
       };
       for (; live && w.left > 0; w.next(A)) {
-        const int32_t* table = A.table + size_t(w.b) * A.max_pages;
-        // the table's entry for this thread in a tile, read a tile ahead of its use
-        auto needs = [&](int i) { return i < w.n && lane_id * box < TK && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
-        auto page_at = [&](int i) { return needs(i) ? table[((w.i0 + i) * TK + lane_id * box) / A.page] : 0; };
-        int ahead = page_at(0);
+        // this thread's entry of the table for a tile, read a tile ahead of its use
+        auto needs = [&](int i) { return i < w.n && lane_id < per_tile && (w.i0 + i) * TK + lane_id * box < w.r.kv; };
+        const int32_t* entry = A.table + size_t(w.b) * A.max_pages + w.i0 / tiles * per_tile + lane_id;
+        int row = w.i0 % tiles;                           // the tile within its page
+        int ahead = needs(0) ? *entry : 0;
         // this segment's query tiles, once the last one's S MMAs have read theirs
         if (lead) {
           if (segs > 0 && !wait_warp(q_empty, uint32_t(segs - 1) & 1u)) break;
@@ -743,10 +749,11 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
           ++segs;
         }
         // K(0), then K(i), V(i - 1) for each tile, V(n - 1): the order of their use
-        int id = -1;
+        int id = -1, at = 0;
         for (int i = 0; live && i <= w.n; ++i) {
-          const int before = id;
+          const int before = id, row_before = at;
           id = -1;
+          at = row;
           if (needs(i)) {
             id = ahead;
             if (id < 0 || id >= A.n_pages) {
@@ -754,7 +761,11 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               id = A.n_pages;   // past the end: the load fills in zeros
             }
           }
-          ahead = page_at(i + 1);
+          if (++row == tiles) {
+            row = 0;
+            entry += per_tile;
+          }
+          ahead = needs(i + 1) ? *entry : 0;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (kv ? i == 0 : i == w.n) continue;
@@ -764,23 +775,15 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               break;
             }
             const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
-            const int r0 = A.page >= TK ? base % A.page : 0;
+            const int r8 = (kv ? row_before : at) * (TK / 8);   // groups of 8 rows before it
             const bool tail = kv && base + TK > w.r.kv;
             uint64_t* bar = tail ? &landed[st] : &full[st];
             if (lead && lane_id == 0) mbar_arrive_expect_tx(bar, uint32_t(np * box) * D * 2);
             __syncwarp();
             const uint32_t dst = sbase + C::ring_off + uint32_t(st) * C::stage;
             const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
-            const int c2 = A.merged ? w.g * A.map_panels : r0 / 8, c3 = A.merged ? w.g * A.map_groups + r0 / 8 : w.g;
-            // every other page by each warp, or a panel of each page
-            if (page >= 0) {
-              const int h = lead ? 0 : 1;
-              if (D == 64 || A.merged) {
-                if ((lane_id & 1) == h) tma_load_5d<LANES == 1>(dst + uint32_t(lane_id * box * D * 2), map, 0, c2, c3, page, bar, policy);
-              } else {
-                tma_load_5d<LANES == 1>(dst + uint32_t(lane_id * box * 128 + h * int(C::panel)), map, h * 64, c2, c3, page, bar, policy);
-              }
-            }
+            const int c2 = A.merged ? w.g * A.map_panels : r8, c3 = A.merged ? w.g * A.map_groups + r8 : w.g;
+            if (page >= 0 && own) tma_load_5d<LANES == 1>(dst + own_off, map, own_x, c2, c3, page, bar, policy);
             if (tail) tail_ph ^= 1u << st;
             tails = tail ? tails | 1u << st : tails & ~(1u << st);
             ++gi;
