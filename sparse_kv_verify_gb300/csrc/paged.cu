@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
               live = false;
               break;
             }
-            const int np = (min(max(w.r.kv - base, 0), TK) + box - 1) / box;   // pages of the tile
+            const int np = __popc(__ballot_sync(0xffffffffu, page >= 0));   // pages of the tile
             const int r8 = (kv ? row_before : at) * (TK / 8);   // groups of 8 rows before it
             const bool tail = kv && base + TK > w.r.kv;
             uint64_t* bar = tail ? &landed[st] : &full[st];
@@ -809,8 +809,8 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
       // ============================================================ landings
       // waits for what the products read and lets the MMA warp go on by a named barrier:
       // a wait on an mbarrier by that warp would stand behind its queued products
-      int gi = 0, segs = 0;
-      uint32_t tail_ph = 0;   // phases of `landed`
+      int st = 0, segs = 0;
+      uint32_t ph = 0, tail_ph = 0;   // phases of stage st, and of `landed`
       auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
         wait_on(bar, parity, A.err, abort_flag);
         __syncwarp();
@@ -829,8 +829,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         const bool halves = LANES == 2 && !w.two;
         // K(0), then K(i), V(i - 1) for each tile, V(n - 1)
 #pragma unroll 1
-        for (int t = 0; t < 2 * w.n; ++t, ++gi) {
-          const int st = gi % NST;
+        for (int t = 0; t < 2 * w.n; ++t) {
           const bool is_v = t == 2 * w.n - 1 || (t > 0 && !(t & 1));
           if (t == 2 * w.n - 1 && nv < TK) {
             wait_warp(&landed[st], (tail_ph >> st) & 1u);
@@ -845,10 +844,14 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
             __syncwarp();
             if (lane_id == 0) mbar_arrive(&full[st]);   // every load is a phase of `full`
           } else {
-            wait_warp(&full[st], uint32_t(gi / NST) & 1u);
+            wait_warp(&full[st], ph);
           }
           // a batch takes K(i + 1) and V(i), or, where the lanes share the tiles, V(i) and K(i + 2)
           if (t == 0 || (halves ? !is_v || t >= 2 * w.n - 2 : is_v)) named_sync(kLandedBar, 64);
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
       }
       __syncwarp();
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
         auto segment = [&](auto halves, bool two) {
           constexpr bool HALVES = decltype(halves)::value;
-          constexpr int kUnroll = LANES == 2 ? 2 : 8;   // of S's products (8: prompts 225 instead of 212 us)
+          constexpr int kUnroll = LANES == 2 ? 4 : 8;   // of S's products (8: prompts 205 instead of 199 us, 2: the same, chunks 2 % slower)
           constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
           const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
           int sv = 0, sk = 0;                     // stages of V and of K
