@@ -59,14 +59,16 @@
 // What bounds it, 64/8/128:
 //   draft blocks of 16 requests over up to 32 K rows: the bytes, 241 us for 1.61 GB
 //   (6.7 TB/s, the rate of a plain copy);
-//   a 4096-token chunk over 28 K: 2.39 ms, 1.72 PFLOP/s (0.90 of cuBLAS's measured
-//   rate) while the clock holds; run on end it meets the power limit, 2.72 ms (cuBLAS
+//   a 4096-token chunk over 28 K: 2.36 ms, 1.75 PFLOP/s (0.92 of cuBLAS's measured
+//   rate) while the clock holds; run on end it meets the power limit, 2.73 ms (cuBLAS
 //   then falls to 0.89 of its rate, too).  A step of both lanes takes 2900 cycles
 //   for 2048 of products: the chain of a lane, products -> S -> softmax (1300 to
 //   1500) -> P, is longer than the other lane's products hide;
-//   short prompts: about 3.5 us for a unit's start and end, as much as 2.5 tiles; most of
-//   it is the fetching of code that runs once a unit, which is why loops off the path
-//   of a step are rolled (12 % of the code, 6 % of the time of 8 prompts);
+//   short prompts: about 3 us for a unit's start and end, as much as 2 tiles; most of it
+//   is the fetching of code that runs once a unit, which is why loops off the path of a
+//   step are rolled (12 % of the code, 10 % of the time of 8 prompts: 199 us);
+//   tokens beside a chunk (32 over up to 16 K rows, and 1000 tokens): 380 us, bytes and
+//   products one after another, as a CTA has units of one kind at a time;
 //   one token over 4 K: 13 us, the latency of two launches.
 #include <type_traits>
 
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
         // One segment.  HALVES: its unit has one row tile, whose odd tiles are lane 1's.
         auto segment = [&](auto halves, bool two) {
           constexpr bool HALVES = decltype(halves)::value;
-          constexpr int kUnroll = LANES == 2 ? 4 : 8;   // of S's products (8: prompts 205 instead of 199 us, 2: the same, chunks 2 % slower)
+          constexpr int kUnroll = LANES == 2 ? 4 : 8;   // of S's products (8: prompts 205 instead of 199 us)
           constexpr int lead = HALVES ? 2 : NB;   // steps that S runs ahead of P V
           const int n = NB * w.n;                 // steps (of both lanes together where they share the tiles)
           int sv = 0, sk = 0;                     // stages of V and of K
