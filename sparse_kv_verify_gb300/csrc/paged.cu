@@ -66,8 +66,8 @@
 //   1500) -> P, is longer than the other lane's products hide;
 //   short prompts: about 3 us for a unit's start and end, as much as 2 tiles; most of it
 //   is the fetching of code that runs once a unit, which is why loops off the path of a
-//   step are rolled (12 % of the code, 10 % of the time of 8 prompts: 199 us);
-//   tokens beside a chunk (32 over up to 16 K rows, and 1000 tokens): 380 us, bytes and
+//   step are rolled (12 % of the code, 10 % of the time of 8 prompts: 200 us);
+//   tokens beside a chunk (32 over up to 16 K rows, and 1000 tokens): 362 us, bytes and
 //   products one after another, as a CTA has units of one kind at a time;
 //   one token over 4 K: 13 us, the latency of two launches.
 #include <type_traits>
@@ -89,13 +89,13 @@ constexpr float kFarPast = 0x1p12f;   // sum of a step's weights past which a ro
 // The cost of a unit: `tile` for each key tile (two lanes' products; or one row
 // tile's, whose time is its bytes'), and for its start and end `extra`.  Fitted to
 // the CTAs' times over batches of prompts and of single tokens beside a chunk: two
-// lanes 1.4 us a tile and 3.5 a unit, one row tile 1.3 and 1.5.
+// lanes 1.33 us a tile and 3.2 a unit, one row tile 0.97 and 1.6.
 template <int LANES>
 struct Cost {
-  static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 8 : 7; }
-  static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 20 : 8; }
+  static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 11 : 8; }
+  static constexpr int extra(bool two) { return LANES == 1 ? 2 : two ? 27 : 13; }
   static constexpr int least = tile(LANES == 2);   // of a share, so that a CTA inside a unit has a tile
-  static constexpr int snap = LANES == 1 ? 2 : 40; // a cut moves this far to the next end of a unit, to save a merge
+  static constexpr int snap = LANES == 1 ? 2 : 55; // a cut moves this far to the next end of a unit, to save a merge
 };
 
 // A cut of the flattened cost: at `at` of pair p of (request b, KV head g), all in
