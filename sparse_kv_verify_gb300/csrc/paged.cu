@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
   if (tid == 32) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);   // the products that read the stage, and the second loading warp
       mbar_init(&landed[s], 1);
     }
     mbar_init(q_full, 1);
@@ -710,7 +710,12 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
     w.init(A, *start);
     if (warp == C::load_warp || warp == C::load_warp2) {
       // ================================================================ loads
-      // (both warps follow every phase of every stage; the first alone arms them)
+      // Both warps follow every phase of `empty`; the first alone arms the stages.
+      // No wait by parity can be lapped or pass early: the phase after the one
+      // that a warp waits for needs that warp past the wait, the first because it arms
+      // the stage's next load, the second because it arrives at `empty` itself.  (The
+      // load that it may have in that stage does not do: with pages of a tile or more it
+      // has none in the whole call, and else none in a tile of one page.)
       const bool lead = warp == C::load_warp;
       // rows that one unit alone reads leave L2 first (64 requests of 512 to 1024 rows 46.0 -> 43.8 us;
       // for the units of one row tile beside a chunk it was worse, 430 -> 449)
@@ -786,6 +791,7 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
             const CUtensorMap* map = kv ? &A.vmap : &A.kmap;
             const int c2 = A.merged ? w.g * A.map_panels : r8, c3 = A.merged ? w.g * A.map_groups + r8 : w.g;
             if (page >= 0 && own) tma_load_5d<LANES == 1>(dst + own_off, map, own_x, c2, c3, page, bar, policy);
+            if (!lead && lane_id == 0) mbar_arrive(&empty[st]);   // (all lanes have passed the wait above)
             if (tail) tail_ph ^= 1u << st;
             tails = tail ? tails | 1u << st : tails & ~(1u << st);
             ++gi;
