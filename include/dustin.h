@@ -466,7 +466,7 @@ int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const
  *             ptr + i * stride (elements, a multiple of 8, at least the row), as the
  *             slices of one projection's output are
  *   q_w, k_w  device bf16 [d], 16-byte aligned, or NULL
- *   inv_freq  device fp32 [rot/2], finite, or NULL with rot = 0
+ *   inv_freq  device fp32 [rot/2], below 2^39 in size, or NULL with rot = 0
  *   pos, slot device int32 [N].  slot -1: the row's k and v are not written (its q
  *             is); any other value outside [0, n_pages * page) as well, with
  *             DUSTIN_DEV_INDEX.  No slot may occur twice.
@@ -474,8 +474,9 @@ int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const
  *   kc, vc    caches of the same hkv, d, n_pages and page; `page` is any positive
  *             number, so that a contiguous cache [B][hkv][Lcap][d] is a pool of B
  *             pages of Lcap rows, with slot = b * Lcap + position
- * Everything is fp32 with one rounding at the end; turns are reduced exactly (64-bit
- * fractions of a turn), so that far positions lose nothing.  A normed head's sum of
+ * Everything is fp32 with one rounding at the end.  Angles are reduced to a turn in whole
+ * numbers, to 2^-33 of it at any position where |inv_freq| < 2^39, and then rounded to
+ * fp32's 24 bits of half a turn, so that far positions lose nothing.  A normed head's sum of
  * squares has to stay within fp32's range (elements below about 2^60). */
 int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, const void* k,
                      int64_t k_stride, const void* v, int64_t v_stride, const void* q_w, const void* k_w,

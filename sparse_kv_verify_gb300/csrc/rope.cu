@@ -9,9 +9,10 @@
 // first heads' loads are on their way; each head's loads are issued before the
 // head before it is computed.
 //
-// Angles: inv_freq / 2 pi as a fraction of 2^64 times the position, modulo 2^64,
-// is the fraction of a turn without any rounding that grows with the position;
-// its upper 32 bits are the half-turns in [-1, 1) that sincospif takes.
+// Angles: inv_freq / 2 pi as a fraction of 2^64 (whole numbers, turns.h) times the
+// position, modulo 2^64, is the fraction of a turn, within 2^-33 at any position;
+// its upper 32 bits are the half-turns in [-1, 1) that sincospif takes, in fp32's
+// 24 bits.
 //
 // Bound by the bytes: each row is read and written once.  16384 tokens, 64/8/128:
 // 104 us for 671 MB, 6.4 TB/s (a plain copy of as many bytes takes 101).  Two elements
@@ -21,6 +22,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "turns.h"
 
 namespace dustin {
 
@@ -105,9 +107,7 @@ __global__ void __launch_bounds__(NTH, kPerSm) rope_kernel(const __grid_constant
   if (t < nt) load(t, h, u0, u1);
   for (int x = tid; x < nt * half; x += NTH) {
     const int tx = x / half, j = x - tx * half;
-    const double all = double(A.inv_freq[j]) * 0.15915494309189533577;   // 1 / (2 pi)
-    const unsigned long long one = __double2ull_rn((all - floor(all)) * 18446744073709551616.0);
-    const long long turn = (long long)(one * (unsigned long long)(long long)A.pos[i0 + tx]);
+    const long long turn = (long long)(turn_of(__float_as_uint(A.inv_freq[j])) * (unsigned long long)(long long)A.pos[i0 + tx]);
     float s, c;
     sincospif(float(int(turn >> 32)) * 0x1p-31f, &s, &c);
     float* at = cs + tx * A.rot + place(j);

@@ -1,0 +1,56 @@
+"""Corners of the paged-cache operators: calls that their documentation allows and
+that the other tests do not make."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU too
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import sparse_kv_verify_gb300 as dk  # noqa: E402
+from synth import to_bits  # noqa: E402
+from oracle.dustin_oracle import bf16  # noqa: E402
+
+from _cache_cases import i32, normal  # noqa: E402
+from _paged_cases import Paged, assert_rotated, pages_of  # noqa: E402
+from _turns import angles  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__ as g
+    g.build()
+
+
+# --------------------------------------------------------------- norm, rope
+
+
+FAR = [0, 1, 5, -1, 2 ** 20, 2 ** 24 + 1, 10 ** 9 + 7, 2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 12345, -2 ** 31, 1 - 2 ** 31]
+FREQS = [1.0, 0.649, 1e-3, 1e-6, 1e-30, 1e-42, 0.0, -0.5, 6.2831855, 3.1415927, 1000.0, 1e6, 12345.678, 1e9, 2.0 ** 38, -2.0 ** 38 - 2.0 ** 15]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_angles_lose_nothing_at_far_positions(d, interleaved):
+    """Against angles reduced in whole numbers: fp64 products of 31 bits of position and
+    24 of frequency would be rounded already.  The bounds are those of near ones."""
+    N, rot, rng = len(FAR), 2 * len(FREQS), np.random.default_rng(d)
+    freqs = np.float32(rng.permutation(FREQS))
+    q, k, v = normal(d, N, 3, d), normal(d + 1, N, 1, d), normal(d + 2, N, 1, d)
+    kc, vc = (torch.zeros((N, 1, 16, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = dk.binding.Workspace(dk.paged_workspace_bytes(dk.Batch(1, 1, 1, 1)))
+    got = dk.dustin_norm_rope(dk.Rope(rot, interleaved), q, k, v, None, None, torch.as_tensor(freqs, device="cuda"),
+                              i32(FAR), i32(16 * np.arange(N)), kc, vc, ws=ws)
+    assert dk.check(ws) == 0
+    t = angles(freqs, FAR)
+    for x, out in ((q, got), (k, kc[:, :, 0])):
+        x = bf16(to_bits(x))
+        y, size = x.copy(), np.abs(x)
+        for j in range(rot // 2):
+            ia, ib = (2 * j, 2 * j + 1) if interleaved else (j, j + rot // 2)
+            c, s, a, b = np.cos(t[:, j])[:, None], np.sin(t[:, j])[:, None], x[..., ia], x[..., ib]
+            y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+            size[..., ia] = size[..., ib] = np.abs(a) + np.abs(b)
+        assert_rotated(out, y, size)
