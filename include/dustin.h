@@ -476,8 +476,10 @@ int dustin_page_map(const dustin_batch* bt, int32_t page, int32_t n_pages, const
  *             pages of Lcap rows, with slot = b * Lcap + position
  * Everything is fp32 with one rounding at the end.  Angles are reduced to a turn in whole
  * numbers, to 2^-33 of it at any position where |inv_freq| < 2^39, and then rounded to
- * fp32's 24 bits of half a turn, so that far positions lose nothing.  A normed head's sum of
- * squares has to stay within fp32's range (elements below about 2^60). */
+ * fp32's 24 bits of half a turn, so that far positions lose nothing.  Heads are normed however small
+ * they are (with eps < 2^-100, one whose squares underflow is scaled by a power of two
+ * first); elements of a normed head, and w, stay below about 2^60.  A head of zeros
+ * with eps = 0 is NaN, 0 / 0. */
 int dustin_norm_rope(const dustin_rope* r, const void* q, int64_t q_stride, const void* k,
                      int64_t k_stride, const void* v, int64_t v_stride, const void* q_w, const void* k_w,
                      const float* inv_freq, const int32_t* pos, const int32_t* slot, void* q_out,

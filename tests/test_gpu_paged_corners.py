@@ -54,3 +54,48 @@ def test_rope_angles_lose_nothing_at_far_positions(d, interleaved):
             y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
             size[..., ia] = size[..., ib] = np.abs(a) + np.abs(b)
         assert_rotated(out, y, size)
+
+
+def rope_heads(q, k, v, w, eps, d, page=16):
+    """One call without a rotation over pools of zeros: (q_out, rows of k, flags)."""
+    N, hkv = k.shape[:2]
+    kc, vc = (torch.zeros((pages_of(N, page), hkv, page, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = dk.binding.Workspace(dk.paged_workspace_bytes(dk.Batch(1, 1, 1, 1)))
+    got = dk.dustin_norm_rope(dk.Rope(0, eps=eps), q, k, v, *w, None, i32(np.zeros(N)), i32(np.arange(N)), kc, vc, ws=ws)
+    at = torch.arange(N, device="cuda")
+    return got, kc[at // page, :, at % page], dk.check(ws)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-38, 1e-32, 2.0 ** -100 * (1 - 2.0 ** -24), 2.0 ** -100, 1e-12, 1e-6, 1.0, 1e30])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rope_norms_heads_however_small(d, eps):
+    """Heads from the smallest bf16 to 2^60, the largest that the call takes: the squares
+    of small ones leave fp32's range, the norm does not.  Also heads with elements of
+    very different sizes."""
+    sizes = list(range(-126, 57, 3))
+    N = len(sizes)
+    f = torch.tensor([2.0 ** s for s in sizes], dtype=torch.float64, device="cuda").view(-1, 1, 1)
+    of_size = lambda t: (t.double().clamp(-3.9, 3.9) * f).to(torch.bfloat16)
+    q, k, v = of_size(normal(d, N, 3, d)), of_size(normal(d + 1, N, 2, d)), normal(d + 2, N, 2, d)
+    q[:, 1] = 2.0 ** -133                               # a head of denormals, and one large element among them
+    q[:, 2, 1:] = 2.0 ** -133
+    q[:, 2, 0] = f[:, 0, 0].to(torch.bfloat16)
+    k[:, 1, ::2] = 1.0
+    w = [(1 + normal(s, d, scale=0.3).float()).to(torch.bfloat16) for s in (3, 4)]
+    got, rows, flags = rope_heads(q, k, v, w, eps, d)
+    assert flags == 0
+    for x, y, wt in ((q, got, w[0]), (k, rows, w[1])):
+        xb = bf16(to_bits(x))
+        ref = xb / np.sqrt((xb * xb).mean(axis=-1, keepdims=True) + float(np.float32(eps))) * bf16(to_bits(wt))
+        assert_rotated(y, ref, np.abs(ref))
+
+
+def test_rope_zeros_without_eps_are_nan():
+    """0 / 0, in that head alone."""
+    q, k, v = normal(1, 4, 2, 64), normal(2, 4, 1, 64), normal(3, 4, 1, 64)
+    q[2, 1] = 0
+    w = [torch.ones(64, dtype=torch.bfloat16, device="cuda")] * 2
+    got, rows, flags = rope_heads(q, k, v, w, 0.0, 64)
+    assert flags == 0 and bool(got[2, 1].isnan().all()) and int(got.isnan().sum()) == 64 and not bool(rows.isnan().any())
+    got, _, _ = rope_heads(q, k, v, w, 1e-45, 64)
+    assert bool((got[2, 1] == 0).all()) and not bool(got.isnan().any())
