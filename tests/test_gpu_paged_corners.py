@@ -13,9 +13,10 @@ import sparse_kv_verify_gb300 as dk  # noqa: E402
 from synth import to_bits  # noqa: E402
 from oracle.dustin_oracle import bf16  # noqa: E402
 
-from _cache_cases import i32, normal  # noqa: E402
+from _cache_cases import assert_attended, attend64, i32, logit_error, normal  # noqa: E402
 from _paged_cases import Paged, assert_rotated, pages_of  # noqa: E402
 from _turns import angles  # noqa: E402
+from test_gpu_paged import check_map, random_pool  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -99,3 +100,56 @@ def test_rope_zeros_without_eps_are_nan():
     assert flags == 0 and bool(got[2, 1].isnan().all()) and int(got.isnan().sum()) == 64 and not bool(rows.isnan().any())
     got, _, _ = rope_heads(q, k, v, w, 1e-45, 64)
     assert bool((got[2, 1] == 0).all()) and not bool(got.isnan().any())
+
+
+# ---------------------------------------------------------------- page map
+
+
+@pytest.mark.parametrize("n,held", [(1, 0), (1, 3), (0, 1)])
+def test_map_of_a_length_next_to_2_to_31(n, held):
+    """seq_len + n_new passes 32 bits by itself: that request alone is flagged."""
+    rng = np.random.default_rng(1)
+    seq, new, table, have, free, n_free = random_pool(rng, 12, 16, 8, 20, 1)
+    seq[3], new[3] = 2 ** 31 - 1, n
+    have[3] = min(held, have[3])
+    r = check_map(seq, new, table, have, free, n_free, 16, int(new.sum()) + 7, 20)
+    assert r["flags"] == 16 and r["kv_len"][3] == 0 and (r["kv_len"][:3] == (seq + new)[:3]).all()
+
+
+# --------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("B,hq,hkv,d,page,longest", [
+    (40, 8, 1, 128, 16, 400), (40, 16, 4, 64, 128, 400), (300, 8, 2, 128, 64, 300), (300, 14, 2, 64, 16, 300),
+    (2000, 8, 1, 64, 16, 70)])
+def test_attn_batches_of_many_requests_with_chunks(B, hq, hkv, d, page, longest):
+    """More requests than a warp has lanes in the shape for chunks: single tokens, runs of
+    idle requests, and requests of more than four pairs of row tiles among them."""
+    rng = np.random.default_rng(B + d)
+    ctx = rng.integers(0, longest, B)
+    new = np.where(rng.random(B) < 0.2, rng.integers(2, 30, B), 1)
+    G = hq // hkv
+    pair = 2 * (128 // G)                                # tokens
+    for b in (0, B // 3, B - 5):                         # idle ones, the last five among them
+        new[b:b + 5] = 0
+    many = rng.permutation(np.flatnonzero(new))[:6 + B // 60]
+    new[many] = rng.integers(4 * pair + 1, 9 * pair, many.size)
+    new[B // 3 - 1] = 6 * pair                           # and some behind a chunk
+    assert (new > 4 * pair).sum() >= 4
+    x = Paged(ctx.tolist(), new.tolist(), hq, hkv, d, page, seed=B, pad=3)
+    ws = dk.binding.Workspace(dk.paged_workspace_bytes(x.batch(dk), hq, hkv, d))
+    o = torch.full((x.N, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((x.N, hq), 7.0, device="cuda")
+    dk.dustin_paged_attn(x.batch(dk), x.q, x.kc, x.vc, x.table, x.cu, x.kv_len, o, lse, ws=ws)
+    assert dk.check(ws) == 0
+    assert bool((o[-3:] == 7).all()) and bool((lse[-3:] == 7).all())
+    for b in range(B):
+        n, kv, at = int(new[b]), x.kv[b], int(x.cu_host[b])
+        if n == 0 or (B > 300 and n <= 4 * pair and b % 11):
+            continue
+        seen = torch.arange(kv, device="cuda") <= torch.arange(kv - n, kv, device="cuda").repeat_interleave(G).view(-1, 1)
+        for g in range(hkv):
+            pick = lambda t: t[at:at + n, g * G:(g + 1) * G].reshape(n * G, -1)
+            q, k, v = pick(x.q), x.rows(b, g, x.kc), x.rows(b, g, x.vc)
+            ro, rl, ra = [t.cpu().numpy() for t in attend64(q, k, v, seen)]
+            assert_attended(pick(o), pick(lse).squeeze(-1), ro, rl, ra, logit_error(q, k), kv)
