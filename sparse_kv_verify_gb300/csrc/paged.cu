@@ -45,9 +45,10 @@
 // every other key tile to lane 1, and lane 0 adds both lanes up at its end.
 // Batches of one row tile each: one lane, steps of 64 keys with two S buffers
 // (NB = 2).  Bytes bound them, so the second product is taken twice there, of P and
-// of what P's rounding left over: o's error is its own rounding's (0.0017 of o
-// against float64, with P alone 0.0019 to 0.0027; 243 instead of 242 us for the case
-// below).
+// of what P's rounding left over: o's error is its own rounding's, 0.0016 to 0.0017 of
+// o against float64 over 1 to 8 requests of 2 to 8 K rows.  The same requests in the
+// other shape, with P alone, have 0.0017 to 0.0022, chunks up to 0.0023.  (243 instead of 242 us for the
+// case below.)
 //
 // Tensor memory: S of lane 0 and 1 in columns [0, 128) and [128, 256), O in
 // [256, 256 + D) and [384, 384 + D).  A segment that covers its unit writes o and
@@ -59,9 +60,9 @@
 // What bounds it, 64/8/128:
 //   draft blocks of 16 requests over up to 32 K rows: the bytes, 241 us for 1.61 GB
 //   (6.7 TB/s, the rate of a plain copy);
-//   a 4096-token chunk over 28 K: 2.36 ms, 1.75 PFLOP/s (0.92 of cuBLAS's measured
-//   rate) while the clock holds; run on end it meets the power limit, 2.73 ms (cuBLAS
-//   then falls to 0.89 of its rate, too).  A step of both lanes takes 2900 cycles
+//   a 4096-token chunk over 28 K: 2.38 ms, 1.73 PFLOP/s (0.91 of cuBLAS's measured
+//   rate) while the clock holds; run on end it meets the power limit, 2.76 ms (cuBLAS
+//   then falls to 0.90 of its rate, too).  A step of both lanes takes 2900 cycles
 //   for 2048 of products: the chain of a lane, products -> S -> softmax (1300 to
 //   1500) -> P, is longer than the other lane's products hide;
 //   short prompts: about 3 us for a unit's start and end, as much as 2 tiles; most of it
@@ -69,7 +70,10 @@
 //   step are rolled (12 % of the code, 10 % of the time of 8 prompts: 200 us);
 //   tokens beside a chunk (32 over up to 16 K rows, and 1000 tokens): 362 us, bytes and
 //   products one after another, as a CTA has units of one kind at a time;
-//   one token over 4 K: 13 us, the latency of two launches.
+//   one token over 4 K: 13 us, the latency of two launches;
+//   more than some hundred requests: also the search for the shares (cut_of), below.
+// At d = 64 a step has half of those products and as much softmax: about 2300 cycles for 1024
+// of products, 1.90 ms for the same chunk.
 #include <type_traits>
 
 #include "common.cuh"
@@ -88,8 +92,9 @@ constexpr float kFarPast = 0x1p12f;   // sum of a step's weights past which a ro
 
 // The cost of a unit: `tile` for each key tile (two lanes' products; or one row
 // tile's, whose time is its bytes'), and for its start and end `extra`.  Fitted to
-// the CTAs' times over batches of prompts and of single tokens beside a chunk: two
-// lanes 1.33 us a tile and 3.2 a unit, one row tile 0.97 and 1.6.
+// the CTAs' times over batches of prompts and of single tokens beside a chunk, with
+// 64/8/128: two lanes 1.33 us a tile and 3.2 a unit, one row tile 0.97 and 1.6.  d = 64
+// takes the same weights; they were not fitted there.
 template <int LANES>
 struct Cost {
   static constexpr int tile(bool two) { return LANES == 1 ? 1 : two ? 11 : 8; }
@@ -215,6 +220,9 @@ __device__ __forceinline__ long long head_cost_warp(const PagedArgs& A, const Re
 // unit where one is near.  Each lane sums a run of neighbouring requests, those of
 // many units together with the others; one scan over the lanes finds the one whose
 // run holds the cut.  CTAs without a share get two equal cuts.
+// All other warps wait for it.  One token over 4 K among idle requests, us by their
+// number, in the shape with one lane: up to 32 12.8, 128 13.6, 512 15.5, 2048 26.8,
+// 8192 69.9; with two lanes 16.3, 17.3, 20.3, 36.5, 97.9.
 template <int LANES>
 __device__ __forceinline__ Cut cut_of(const PagedArgs& A, int next, Start& out) {
   const int lane = threadIdx.x & 31;
@@ -962,8 +970,11 @@ __global__ void __launch_bounds__(Cfg<D, LANES>::threads, 1) paged_kernel(const 
 }
 
 // Log-sum-exp merge of the segments of the unit that CTA blockIdx.x started and did
-// not end: one thread per four output columns of ROWS rows.  Units with two row
-// tiles are split in two or three, units of few rows among many CTAs.
+// not end: one thread per four output columns of M::rows rows.  The depth of the loads
+// goes by batches of many units where there are two lanes, whose units are cut in two
+// or three; the few units of a short chunk over a long context are cut among as many
+// CTAs as single tokens' are (32 tokens over 32 K rows, 64/8/128: 8 units, 19 segments
+// each; the whole call 46.4 us for 20.0 of bytes).
 constexpr int kMergeThreads = 256;
 template <int D, int LANES>
 struct Merge {

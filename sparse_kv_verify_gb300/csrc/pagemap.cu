@@ -235,6 +235,12 @@ cudaError_t launch_t(const PageMapArgs& a, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
+// Few rows: a CTA of few warps, whose scans and barriers are shorter.  Many: a cluster,
+// which shares the rows out.  us of a graph node by N, 16 to 256 requests that move no
+// page: 256 threads against 1024, N = 16 3.4 and 4.0, 256 4.0 and 4.3, 1024 5.5 and 4.5;
+// one CTA of 1024 against eight, N = 2048 5.3 and 4.8, 4096 7.2 and 4.6, 8192 10.7 and
+// 4.8, 32768 31.5 and 7.6.  (Each pair is even somewhat below its limit here, at about
+// 500 and 1500 rows; between them and the limits 1 to 2.5 us are left.)
 cudaError_t page_map_launch(const PageMapArgs& a, cudaStream_t stream) {
   if (a.B <= 256 && a.N <= 1024) return launch_t<256, 1>(a, 1, stream);
   const int ctas = a.N <= 4096 ? 1 : kClusterMax;

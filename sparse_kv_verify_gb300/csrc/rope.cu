@@ -236,8 +236,8 @@ cudaError_t launch_d(const RopeArgs& a, int num_sms, cudaStream_t stream) {
   const int heads = a.hq + 2 * a.hkv;
   // Tokens and splits of the heads: as many CTAs as fill the SMs where the batch is
   // short, ten runs of heads for each where it is long.  us by tokens of a CTA,
-  // 64/8/128, 16384 tokens (5 runs of heads a token): 1 106.7, 2 104.4, 4 107.1;
-  // 14/2/64, 5003 tokens (1 run): 2 8.0, 4 7.7, 6 9.9.
+  // 64/8/128, 16384 tokens (5 runs of heads a token): 1 107.6, 2 104.8, 4 106.2;
+  // 14/2/64, 5003 tokens (1 run): 2 8.4, 4 7.7, 6 9.1.
   const long long runs = ((long long)a.N * heads + GROUPS - 1) / GROUPS, ctas = (long long)kPerSm * num_sms;
   const int tb = int(std::min<long long>({kTokensMax, std::max(1LL, (long long)a.N / ctas),
                                           std::max(1, 10 * GROUPS / heads)}));
